@@ -72,6 +72,10 @@ int check_x(const void* x, int x_dtype) {
 
 }  // namespace
 
+int device_latch(unsigned** out) { return err_ptr(out); }
+
+void set_last_path(int path) { t_last_path = path; }
+
 int sm_count(int device) {
     if (device < 0 || device >= kMaxDevices) return 1;
     if (!g_sms[device]) {
@@ -149,7 +153,10 @@ const char* qmm_status_str(int status) {
     case QMM_ERR_UNIMPLEMENTED: return "unimplemented";
     case QMM_ERR_BAD_ARGUMENT: return "bad argument";
     case QMM_ERR_OUTPUT_TOO_SMALL: return "output buffer too small";
-    case QMM_ERR_WORKSPACE_TOO_SMALL: return "workspace too small (see qmoe_ffn_workspace_bytes)";
+    case QMM_ERR_WORKSPACE_TOO_SMALL:
+        return "workspace too small (see qmoe_ffn_workspace_bytes, qattn_decode_workspace_bytes)";
+    case QMM_ERR_CACHE_TOO_SMALL: return "key-value cache smaller than its pages (see qkv_page_bytes)";
+    case QMM_ERR_BAD_SLOT: return "cache slot, page id or sequence length out of range";
     case QMM_ERR_NOALLOC_LIMIT:
         return "problem needs more scratch than qgemm_noalloc's fixed array holds";
     case QMM_ERR_WORKSPACE_IN_CAPTURE:
@@ -453,6 +460,7 @@ int qmm_check_device_error(void* stream) {
     }
     if (v & DEV_ERR_TIMEOUT) return QMM_ERR_DEVICE_TIMEOUT;
     if (v & DEV_ERR_BAD_INDEX) return QMM_ERR_BAD_EXPERT_ID;
+    if (v & DEV_ERR_BAD_SLOT) return QMM_ERR_BAD_SLOT;
     return QMM_OK;
 }
 

@@ -1,0 +1,170 @@
+// kv_common.cuh -- what the rotary, cache and attention kernels share: element
+// types, vector access, the rotary phase and the layout of a paged cache.
+#pragma once
+
+#include "qmm.h"
+#include "qmm_internal.cuh"
+
+namespace qmm {
+
+// Row layouts of a paged key or value cache (bytes). Page p starts at
+// p * page_stride; in it each head has one contiguous unit:
+//   f16 / bf16   [page_size][D] values
+//   q8_0         [page_size][D] int8 codes, then [page_size][D / 32] f16 scales
+// (value = scale * code). Codes and scales apart keep every vector access
+// aligned; the bytes per row are those of 34-byte Q8_0 blocks.
+__host__ __device__ __forceinline__ size_t kv_row_bytes(int fmt, int64_t D) {
+    return static_cast<size_t>(fmt == QMM_KV_Q8_0 ? D + D / 16 : 2 * D);
+}
+
+struct KvCache {
+    uint8_t* k;
+    uint8_t* v;
+    int fmt;
+    int page_shift;          // log2(page_size)
+    int heads, D;
+    int64_t n_pages;
+    int64_t page_stride;     // bytes
+    __host__ __device__ int64_t unit() const {
+        return static_cast<int64_t>(kv_row_bytes(fmt, D)) << page_shift;
+    }
+};
+
+// N consecutive elements of type T (2 or 4 bytes each) as one access of
+// sizeof(T) * N bytes, up to 16 bytes; larger N takes several.
+template <int BYTES> struct VecOf;
+template <> struct VecOf<2> { using type = unsigned short; };
+template <> struct VecOf<4> { using type = unsigned; };
+template <> struct VecOf<8> { using type = uint2; };
+template <> struct VecOf<16> { using type = uint4; };
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+// Rounded to nearest even, once.
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Loads / stores N elements as fp32; the address is aligned to
+// min(16, N * sizeof(T)) bytes.
+template <typename T, int N> __device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
+    constexpr int B = N * static_cast<int>(sizeof(T)) < 16 ? N * static_cast<int>(sizeof(T)) : 16;
+    constexpr int PER = B / static_cast<int>(sizeof(T));
+    using V = typename VecOf<B>::type;
+#pragma unroll
+    for (int i = 0; i < N / PER; ++i) {
+        const V v = reinterpret_cast<const V*>(p)[i];
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[i * PER + j] = to_f32<T>(e[j]);
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void store_vec(T* p, const float (&x)[N]) {
+    constexpr int B = N * static_cast<int>(sizeof(T)) < 16 ? N * static_cast<int>(sizeof(T)) : 16;
+    constexpr int PER = B / static_cast<int>(sizeof(T));
+    using V = typename VecOf<B>::type;
+#pragma unroll
+    for (int i = 0; i < N / PER; ++i) {
+        V v;
+        T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) e[j] = from_f32<T>(x[i * PER + j]);
+        reinterpret_cast<V*>(p)[i] = v;
+    }
+}
+
+// cos and sin of 2 pi frac(pos * turns / 2^64). The product wraps modulo 2^64,
+// which drops whole turns exactly, so the angle is as good at position 10^6 as
+// at 1 (an fp32 product pos * frequency is off by up to 4e-3 rad at 10^5). The
+// top 32 bits of the fraction, as a signed half-turn count in [-1, 1), reach
+// sincospif with one rounding (2^-25).
+__device__ __forceinline__ void rope_cs(int32_t pos, uint64_t turns, float mscale, float& c, float& s) {
+    const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+    const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    sincospif(half_turns, &s, &c);
+    c *= mscale;
+    s *= mscale;
+}
+
+// Waits for the kernel before this one on the stream (a kernel launched with
+// programmatic stream serialisation may start before it has ended), and lets
+// the next such kernel start.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// k_rope.cu
+struct RopeArgs {
+    const void* X;
+    void* Y;
+    int dtype;                     // QMM_F32 / QMM_F16 / QMM_BF16
+    int64_t x_ts, x_hs, y_ts, y_hs;  // strides in elements
+    const int32_t* pos;
+    const uint64_t* turns;
+    int rot, layout;
+    float mscale;
+    int64_t T, H, D;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+// k_kv.cu
+struct KvStoreArgs {
+    KvCache c;
+    const void* K;
+    const void* V;
+    int dtype;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    const int64_t* slots;
+    const int32_t* pos;            // nullptr: K is stored as given
+    const uint64_t* turns;
+    int rot, layout;
+    float mscale;
+    int64_t T;
+    unsigned* err;
+};
+cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t s);
+
+struct KvLoadArgs {
+    KvCache c;
+    const int64_t* slots;
+    void* K;
+    void* V;
+    int dtype;
+    int64_t T;
+    unsigned* err;
+};
+cudaError_t launch_kv_load(const KvLoadArgs& a, cudaStream_t s);
+
+// k_attn.cu
+struct AttnArgs {
+    KvCache c;
+    const void* q;
+    int dtype;                     // of q and out
+    int64_t q_bs, q_hs;            // strides in elements
+    const int32_t* table;          // [B][table_stride] page ids
+    int64_t table_stride;
+    int table_width;               // pages a row may name
+    const int32_t* lens;
+    int max_len;
+    int64_t B;
+    int Hq;
+    float scale, softcap;
+    int window;
+    void* out;                     // [B][Hq][D]
+    float* lse;                    // [B][Hq] or nullptr
+    void* ws;
+    unsigned* err;
+};
+struct AttnPlan {
+    int splits;                    // most splits of one sequence
+    int chunk;                     // keys per split
+    int tiles;                     // head tiles of 8 per block
+    size_t ws_bytes;
+};
+bool attn_dim_ok(int D);
+AttnPlan attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms);
+cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+
+}  // namespace qmm

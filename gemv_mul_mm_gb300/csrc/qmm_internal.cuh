@@ -17,7 +17,14 @@ __host__ __device__ __forceinline__ int64_t imin64(int64_t a, int64_t b) { retur
 enum : unsigned {
     DEV_ERR_TIMEOUT = 1u,      // a bounded mbarrier wait ran out
     DEV_ERR_BAD_INDEX = 2u,    // an expert id or activation row out of range
+    DEV_ERR_BAD_SLOT = 4u,     // a cache slot, page id or sequence length out of range
 };
+
+// The current device's error latch; returns a qmm_status.
+int device_latch(unsigned** out);
+
+// Sets what qmm_last_path returns on this thread.
+void set_last_path(int path);
 
 // Number of streaming multiprocessors of `device` (cached).
 int sm_count(int device);

@@ -19,7 +19,10 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "qmm.h")
 KINDS = ["Q8_0", "Q4_0", "Q5_0", "Q4_K", "Q5_K", "Q6_K",
          "Q2_K", "Q3_K", "IQ4_NL", "IQ4_XS", "MXFP4", "Q4_1", "Q5_1", "Q8_1"]
 KIND_ID = {k: i for i, k in enumerate(KINDS)}
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
+KV_FORMATS = {"f16": 0, "bf16": 1, "q8_0": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 
 STATUS = {
     0: "QMM_OK", 1: "QMM_ERR_EMPTY_SHAPE", 2: "QMM_ERR_BAD_KIND", 3: "QMM_ERR_BAD_DTYPE",
@@ -28,10 +31,12 @@ STATUS = {
     9: "QMM_ERR_BAD_EXPERT_ID", 10: "QMM_ERR_CUDA", 11: "QMM_ERR_DEVICE_TIMEOUT",
     12: "QMM_ERR_UNIMPLEMENTED", 13: "QMM_ERR_BAD_ARGUMENT", 14: "QMM_ERR_OUTPUT_TOO_SMALL",
     15: "QMM_ERR_WORKSPACE_IN_CAPTURE", 16: "QMM_ERR_NOALLOC_LIMIT", 17: "QMM_ERR_WORKSPACE_TOO_SMALL",
+    18: "QMM_ERR_CACHE_TOO_SMALL", 19: "QMM_ERR_BAD_SLOT",
 }
 STATUS_ID = {v: k for k, v in STATUS.items()}
 
 PATH_AUTO, PATH_GENERIC, PATH_GEMV, PATH_TC, PATH_DEQUANT, PATH_GROUPED, PATH_MOE, PATH_REPACKED = range(8)
+PATH_ROPE, PATH_KV_STORE, PATH_KV_LOAD, PATH_ATTN = range(8, 12)
 FLAG_WEIGHTS_CONST = 1
 FLAG_Y_F16 = 2
 FLAG_Y_BF16 = 4
@@ -76,6 +81,18 @@ def _lib():
                                _P, _SZ, _P, _SZ, _P]
         L.qmoe_ffn_workspace_bytes.argtypes = [_I64, _I, _I64, _I64]
         L.qmoe_ffn_workspace_bytes.restype = _SZ
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        L.qkv_page_bytes.argtypes = [_I, _I, _I, _I]
+        L.qkv_page_bytes.restype = _SZ
+        L.qrope_turns.argtypes = [f64, _I, _I, f64, f64, f64, f64, _P, ctypes.POINTER(f32)]
+        L.qrope.argtypes = [_P, _I, _SZ, _I64, _I64, _P, _P, _I, _I, f32, _P, _SZ, _I64, _I64, _I64, _I64, _I64, _P]
+        L.qkv_store.argtypes = [_I, _P, _SZ, _I64, _I64, _P, _SZ, _I64, _I64, _I, _P, _P, _P, _I, _I, f32, _P, _P, _SZ,
+                                _I64, _I64, _I, _I64, _I, _I, _P]
+        L.qkv_load.argtypes = [_I, _P, _P, _P, _SZ, _I64, _I64, _I, _P, _P, _I, _SZ, _I64, _I, _I, _P]
+        L.qattn_decode.argtypes = [_I, _P, _I, _SZ, _I64, _I64, _P, _P, _SZ, _I64, _I64, _I, _P, _SZ, _I64, _I, _P, _I,
+                                   _I64, _I, _I, _I, f32, _I, f32, _P, _SZ, _P, _P, _SZ, _P]
+        L.qattn_decode_workspace_bytes.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
+        L.qattn_decode_workspace_bytes.restype = _SZ
         L.qmm_check_device_error.argtypes = [_P]
         L.qmm_selftest_wait_timeout.argtypes = [_I64, _P]
         L.qmm_set_path.argtypes = [_I]
@@ -276,6 +293,208 @@ def qmoe_ffn(kind, W_gu, gu_stride: int, W_down, down_stride: int, n_experts: in
                            _ptr(X), X.numel(), T, d_model, d_ff, _ptr(topk_ids), _ptr(topk_w), top_k,
                            _ptr(Y), Y.numel(), _ptr(workspace), workspace.numel(), _stream(stream)), "qmoe_ffn")
     return Y
+
+
+def _act(X, what: str) -> int:
+    """Element type of an f32 / f16 / bf16 tensor."""
+    import torch
+    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(X.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {X.dtype}")
+    return dt
+
+
+def _rows(X, what: str):
+    """(elements reachable, token stride, head stride) of a (T, H, D) tensor
+    whose last dimension is contiguous."""
+    if X.dim() != 3:
+        raise ValueError(f"{what} must have three dimensions (tokens, heads, dim), got {tuple(X.shape)}")
+    (T, H, D), (ts, hs, ds) = X.shape, X.stride()
+    if ds != 1 and D > 1:
+        raise ValueError(f"{what}'s last dimension must be contiguous")
+    return (T - 1) * ts + (H - 1) * hs + D if T and H and D else 0, ts, hs
+
+
+def _want(X, dtype, n, what: str, dev):
+    """A contiguous `dtype` tensor of `n` elements on `dev`."""
+    if X.dtype != dtype or not X.is_contiguous() or (n is not None and X.numel() != n):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n is not None else ""))
+    _on(X, dev, what)
+
+
+def _on(X, dev, what: str):
+    if X.device != dev:
+        raise ValueError(f"{what} is on {X.device}, not on {dev}")
+
+
+def _pages(k_cache, v_cache, dev):
+    """(pages, page stride, bytes) of a cache given as two (pages, bytes) uint8 tensors."""
+    import torch
+    for c, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if c.dtype != torch.uint8 or c.dim() != 2 or c.stride(1) != 1:
+            raise ValueError(f"{what} must be a (pages, bytes per page) uint8 tensor with contiguous pages")
+        _on(c, dev, what)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    n, nbytes = k_cache.shape
+    # one page alone has no stride to speak of
+    stride = k_cache.stride(0) if n > 1 else nbytes
+    return n, stride, (n - 1) * stride + nbytes if n else 0
+
+
+def _fmt(fmt) -> int:
+    return KV_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def qkv_page_bytes(fmt, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    return _lib().qkv_page_bytes(_fmt(fmt), page_size, n_kv_heads, head_dim)
+
+
+def qkv_cache(fmt, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
+    """A zeroed cache: (keys, values), each a (n_pages, bytes per page) uint8 tensor."""
+    import torch
+    nbytes = qkv_page_bytes(fmt, page_size, n_kv_heads, head_dim)
+    if not nbytes:
+        raise ValueError(f"no {fmt} cache has pages of {page_size} tokens, {n_kv_heads} heads of {head_dim}")
+    return tuple(torch.zeros((n_pages, nbytes), dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def qrope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                orig_len: float = 0.0, fast: Optional[float] = None, slow: float = 1.0, device="cuda"):
+    """(turns, mscale) for qrope and qkv_store: the int64 table of turns per
+    position (64-bit fractions) and the factor on the rotated values. `scaling`
+    is a key of ROPE_SCALINGS; "ramp" and "bands" need orig_len (fast: 32 and 4
+    by default)."""
+    import torch
+    kind = ROPE_SCALINGS[scaling]
+    if fast is None:
+        fast = 4.0 if scaling == "bands" else 32.0
+    host = (ctypes.c_uint64 * max(1, rot_dim // 2))()
+    m = ctypes.c_float()
+    _check(_lib().qrope_turns(base, rot_dim, kind, factor, orig_len, fast, slow, host, ctypes.byref(m)), "qrope_turns")
+    return torch.frombuffer(bytearray(host), dtype=torch.int64).to(device), m.value
+
+
+def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=None, stream=None):
+    """Rotary positions on X (T, H, D): the first 2 * turns.numel() values of
+    each head in pairs (i, i + rot/2) ("half") or (2i, 2i + 1)
+    ("interleaved"). positions: int32 (T,); turns: qrope_turns. X may be a
+    view; out=X rotates in place. Returns out (X's type)."""
+    import torch
+    dt = _act(X, "X")
+    n, ts, hs = _rows(X, "X")
+    T, H, D = X.shape
+    dev = X.device
+    _want(positions, torch.int32, T, "positions", dev)
+    _want(turns, torch.int64, None, "turns", dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=X.dtype, device=dev)
+        on, ots, ohs = T * H * D, H * D, D
+    else:
+        if out.shape != X.shape or out.dtype != X.dtype:
+            raise ValueError("out must have X's shape and type")
+        _on(out, dev, "out")
+        on, ots, ohs = _rows(out, "out")
+    _check(_lib().qrope(X.data_ptr(), dt, n, ts, hs, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
+                        ROPE_LAYOUTS[layout], mscale, out.data_ptr(), on, ots, ohs, T, H, D, _stream(stream)), "qrope")
+    return out
+
+
+def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None, turns=None, layout: str = "half",
+              mscale: float = 1.0, stream=None):
+    """Writes K and V (T, n_kv_heads, head_dim; views allowed) to `slots` (int64
+    (T,); -1 skips a token) of a paged cache of format "f16", "bf16" or "q8_0",
+    rotating K first when positions and turns are given. k_cache, v_cache:
+    (pages, bytes per page) uint8 tensors (qkv_cache)."""
+    import torch
+    dt = _act(K, "K")
+    if V.dtype != K.dtype or V.shape != K.shape:
+        raise ValueError("V must have K's shape and type")
+    kn, kts, khs = _rows(K, "K")
+    vn, vts, vhs = _rows(V, "V")
+    T, H, D = K.shape
+    dev = K.device
+    _on(V, dev, "V")
+    _want(slots, torch.int64, T, "slots", dev)
+    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
+    if (positions is None) != (turns is None):
+        raise ValueError("positions and turns go together")
+    pos = tur = rot = 0
+    if positions is not None:
+        _want(positions, torch.int32, T, "positions", dev)
+        _want(turns, torch.int64, None, "turns", dev)
+        pos, tur, rot = positions.data_ptr(), turns.data_ptr(), 2 * turns.numel()
+    _check(_lib().qkv_store(_fmt(fmt), K.data_ptr(), kn, kts, khs, V.data_ptr(), vn, vts, vhs, dt, slots.data_ptr(),
+                            pos, tur, rot, ROPE_LAYOUTS[layout], mscale, k_cache.data_ptr(), v_cache.data_ptr(), nbytes,
+                            n_pages, stride, page_size, T, H, D, _stream(stream)), "qkv_store")
+
+
+def qkv_load(fmt, slots, k_cache, v_cache, page_size: int, n_kv_heads: int, head_dim: int, dtype=None, stream=None):
+    """The keys and values in `slots` (int64 (T,); -1 gives zeros) as two (T,
+    n_kv_heads, head_dim) tensors of `dtype` (float32 by default)."""
+    import torch
+    dev = k_cache.device
+    T = slots.numel()
+    _want(slots, torch.int64, T, "slots", dev)
+    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
+    K = torch.empty((T, n_kv_heads, head_dim), dtype=dtype or torch.float32, device=dev)
+    V = torch.empty_like(K)
+    _check(_lib().qkv_load(_fmt(fmt), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, stride,
+                           page_size, K.data_ptr(), V.data_ptr(), _act(K, "K"), K.numel(), T, n_kv_heads, head_dim,
+                           _stream(stream)), "qkv_load")
+    return K, V
+
+
+def qattn_decode_workspace_bytes(fmt, dtype, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
+                                 window: int = 0) -> int:
+    import torch
+    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dtype]
+    return _lib().qattn_decode_workspace_bytes(_fmt(fmt), dt, batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
+
+
+def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int, n_kv_heads: int,
+                 scale: Optional[float] = None, window: int = 0, softcap: float = 0.0, max_len: Optional[int] = None,
+                 out=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of one new token per sequence, q (B, n_q_heads, head_dim), over
+    the paged cache: block_table int32 (B, pages), seq_lens int32 (B,) counting
+    the new token, whose key is stored already. scale defaults to
+    head_dim ** -0.5; max_len (a bound on seq_lens) to what the table holds; a
+    tighter one splits short batches better. Returns out (q's type), and lse
+    (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
+    uint8 tensor of qattn_decode_workspace_bytes(...)), allocated here with
+    torch if None."""
+    import torch
+    dt = _act(q, "q")
+    qn, qbs, qhs = _rows(q, "q")
+    B, H, D = q.shape
+    dev = q.device
+    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be an int32 tensor (sequences, pages) with contiguous rows")
+    _on(block_table, dev, "block_table")
+    _want(seq_lens, torch.int32, B, "seq_lens", dev)
+    width, tstride = block_table.shape[1], block_table.stride(0)
+    if max_len is None:
+        max_len = width * page_size
+    if out is None:
+        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+    else:
+        _want(out, q.dtype, B * H * D, "out", dev)
+    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if return_lse else None
+    L, f = _lib(), _fmt(fmt)
+    if workspace is None:
+        need = L.qattn_decode_workspace_bytes(f, dt, B, H, n_kv_heads, D, max_len, window)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _on(workspace, dev, "workspace")
+    _check(L.qattn_decode(f, q.data_ptr(), dt, qn, qbs, qhs, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages,
+                          stride, page_size, block_table.data_ptr(), (B - 1) * tstride + width if B else 0, tstride,
+                          width, seq_lens.data_ptr(), max_len, B, H, n_kv_heads, D,
+                          D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), out.numel(),
+                          _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)),
+           "qattn_decode")
+    return (out, lse) if return_lse else out
 
 
 def selftest_wait_timeout(cycles: int, stream=None):

@@ -79,8 +79,10 @@ typedef enum {
 } qmm_kind;
 
 /* Activation element type. f32 activations must be 4-byte aligned, f16
- * activations (IEEE binary16) 2-byte aligned. */
-typedef enum { QMM_F32 = 0, QMM_F16 = 1 } qmm_dtype;
+ * (IEEE binary16) and bfloat16 activations 2-byte aligned. The products take
+ * QMM_F32 and QMM_F16; the rotary, cache and attention operators take all
+ * three. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
 
 /* Status codes. The shape refusals mirror ferrox-cuda mul_mm.rs
  * `MulMmUnsupported`. */
@@ -102,7 +104,9 @@ typedef enum {
     QMM_ERR_OUTPUT_TOO_SMALL = 14,       /* y_elems < outputs to write */
     QMM_ERR_WORKSPACE_IN_CAPTURE = 15,   /* workspace would grow during stream capture */
     QMM_ERR_NOALLOC_LIMIT = 16,          /* qgemm_noalloc: scratch needed exceeds its fixed array */
-    QMM_ERR_WORKSPACE_TOO_SMALL = 17     /* caller-provided workspace smaller than required */
+    QMM_ERR_WORKSPACE_TOO_SMALL = 17,    /* caller-provided workspace smaller than required */
+    QMM_ERR_CACHE_TOO_SMALL = 18,        /* key-value cache smaller than its pages */
+    QMM_ERR_BAD_SLOT = 19                /* cache slot, page id or sequence length out of range */
 } qmm_status;
 
 /* Geometry of `kind`: bytes and elements of one block. Returns QMM_OK or
@@ -364,10 +368,161 @@ QMM_API int qmoe_ffn(int kind, const void* W_gu, size_t w_gu_bytes, size_t gu_st
 QMM_API size_t qmoe_ffn_workspace_bytes(int64_t T, int top_k, int64_t d_model, int64_t d_ff);
 
 /*
+ * The operators around the attention of a decoder layer, for serving: rotary
+ * positions, a paged key-value cache, and the attention of one new token a
+ * sequence over it. They take f32, f16 or bf16 activations with strides (in
+ * elements; the last dimension is contiguous), so that q, k and v may be views
+ * of one fused projection. They never allocate device memory, copy nothing to
+ * the host and can be captured in a graph.
+ *
+ * Key-value cache. Keys and values live in two buffers of `n_pages` pages of
+ * `page_size` tokens (a power of two, 8 to 4096), pages `page_stride` bytes
+ * apart (a multiple of 16, at least qkv_page_bytes; larger strides let
+ * layers share one allocation). In a page, head h has a unit of page_size
+ * rows of head_dim values (head_dim a multiple of 32):
+ *   QMM_KV_F16 / QMM_KV_BF16  the values, [page_size][head_dim]
+ *   QMM_KV_Q8_0               int8 codes [page_size][head_dim], then f16 scales
+ *                             [page_size][head_dim / 32]; value = scale * code.
+ *                             The bytes per token are those of Q8_0 blocks.
+ * Slot s of the cache is row s % page_size of page s / page_size.
+ */
+typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8_0 = 2 } qmm_kv_format;
+
+/* Bytes of one page of keys (or of values); 0 for a format, page size, head
+ * count or head dim the cache does not take. Host only, no CUDA call. */
+QMM_API size_t qkv_page_bytes(int fmt, int page_size, int n_kv_heads, int head_dim);
+
+/* Which elements of a head make a pair. */
+typedef enum { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 } qmm_rope_layout;
+
+/* Frequency scalings for contexts longer than a model was trained on. */
+typedef enum {
+    QMM_ROPE_PLAIN = 0,   /* f_i = base^(-2 i / rot_dim) */
+    QMM_ROPE_LINEAR = 1,  /* f_i / factor (positions interpolated) */
+    QMM_ROPE_BASE = 2,    /* base replaced by base * factor^(rot_dim / (rot_dim - 2)) */
+    QMM_ROPE_RAMP = 3,    /* pairs that make more than `fast` turns in orig_len positions are kept, fewer than `slow`
+                             divided by factor, a linear ramp over the pair index between; mscale = 0.1 ln(factor) + 1 */
+    QMM_ROPE_BANDS = 4    /* the same with the blend linear in the number of turns, and mscale = 1 */
+} qmm_rope_scaling;
+
+/*
+ * qrope_turns -- the frequency table of qrope, computed on the host in double.
+ * Entry i is the turns per position of pair i, f_i / (2 pi), as a 64-bit
+ * fraction (2^64 = one turn): position * entry modulo 2^64 is then the exact
+ * phase, at any position. Callers with frequencies of their own fill the table
+ * the same way. Copy it to the device once.
+ *
+ *   turns    host, rot_dim / 2 entries;  mscale  host, the factor on the
+ *            rotated values that the scaling asks for
+ *   factor   >= 1, not read by QMM_ROPE_PLAIN; orig_len, fast > slow > 0 are
+ *            read by QMM_ROPE_RAMP and QMM_ROPE_BANDS (customary: 32 and 1,
+ *            4 and 1)
+ */
+QMM_API int qrope_turns(double base, int rot_dim, int scaling, double factor, double orig_len, double fast,
+                        double slow, uint64_t* turns, float* mscale);
+
+/*
+ * qrope -- rotary positions on T tokens of H heads of D values. For pair
+ * i < rot_dim / 2, with a = 2 pi positions[t] * turns[i] / 2^64:
+ *
+ *   y1 = mscale (x1 cos a - x2 sin a),   y2 = mscale (x2 cos a + x1 sin a)
+ *
+ * (x1, x2) are elements i and i + rot_dim / 2 of the head (QMM_ROPE_HALF) or 2i
+ * and 2i + 1 (QMM_ROPE_INTERLEAVED); elements from rot_dim (even, <= D) on are
+ * copied. fp32 arithmetic, one rounding at the store. The gradient of the
+ * input is the same call on the output's gradient with negated positions.
+ *
+ *   X, Y        device, dtype, element (t, h, d) at t * ts + h * hs + d; Y may
+ *               be X with the same strides (in place), and must not overlap it
+ *               otherwise; x_elems, y_elems their sizes
+ *   positions   device int32 [T], any sign;  turns  device [rot_dim / 2]
+ */
+QMM_API int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, const int32_t* positions,
+                  const uint64_t* turns, int rot_dim, int layout, float mscale, void* Y, size_t y_elems, int64_t y_ts,
+                  int64_t y_hs, int64_t T, int64_t H, int64_t D, void* stream);
+
+/*
+ * qkv_store -- writes the keys and values of T tokens into the cache, rotating
+ * the keys first when positions and turns are given (both NULL: stored as they
+ * are), in one kernel. f16 and bf16 caches round once (to nearest even; an
+ * fp32 value beyond the f16 range becomes Inf). QMM_KV_Q8_0 quantises each 32
+ * consecutive values: d = f16(max |x| / 127), code = x / d rounded to nearest,
+ * in [-127, 127]; d = 0 gives codes 0; a block holding an Inf or NaN, or whose
+ * d overflows f16, gets d = NaN, so that it reads back as NaN.
+ *
+ *   K, V     device, dtype, element (t, h, d) at t * ts + h * hs + d; sizes in
+ *            elements
+ *   slots    device int64 [T]: the token's slot, or -1 to skip it. Slots other
+ *            than -1 must be distinct. One outside the cache writes nothing and
+ *            latches QMM_ERR_BAD_SLOT for qmm_check_device_error().
+ *   k_cache, v_cache  device, cache_bytes bytes each, 16-byte aligned
+ */
+QMM_API int qkv_store(int fmt, const void* K, size_t k_elems, int64_t k_ts, int64_t k_hs, const void* V,
+                      size_t v_elems, int64_t v_ts, int64_t v_hs, int dtype, const int64_t* slots,
+                      const int32_t* positions, const uint64_t* turns, int rot_dim, int layout, float mscale,
+                      void* k_cache, void* v_cache, size_t cache_bytes, int64_t n_pages, int64_t page_stride,
+                      int page_size, int64_t T, int n_kv_heads, int head_dim, void* stream);
+
+/*
+ * qkv_load -- reads T slots of the cache back as dense rows [T][n_kv_heads]
+ * [head_dim] of dtype (rounded once). Slot -1 gives zeros; one outside the cache
+ * gives NaN and latches QMM_ERR_BAD_SLOT. K and V are 16-byte aligned, kv_elems
+ * the size of each.
+ */
+QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const void* v_cache, size_t cache_bytes,
+                     int64_t n_pages, int64_t page_stride, int page_size, void* K, void* V, int dtype, size_t kv_elems,
+                     int64_t T, int n_kv_heads, int head_dim, void* stream);
+
+/*
+ * qattn_decode -- attention of one new token a sequence over the paged cache.
+ * For sequence b and query head h, with kv head h / (n_q_heads / n_kv_heads),
+ * keys k_j and values v_j of positions j in [max(0, len_b - window), len_b):
+ *
+ *   s_j = scale q . k_j        (softcap c > 0: c tanh(s_j / c))
+ *   out[b][h] = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse[b][h] = ln sum_j e^{s_j}
+ *
+ * The new token's own key is in the cache already (qkv_store first). Position
+ * j is row j % page_size of page block_table[b][j / page_size]. A sequence of
+ * length 0 gives zeros and lse = -inf. Whatever the cache holds outside the
+ * range, NaN included, has no effect. Long sequences are split over the GPU
+ * and joined in a fixed order: results are deterministic. Accumulation,
+ * softmax and joins are fp32; with fp32 q the result is fp32-accurate, 16-bit
+ * outputs are rounded once.
+ *
+ *   q            device, dtype, element (b, h, d) at b * q_bs + h * q_hs + d
+ *   block_table  device int32, row b at b * table_stride, table_width page ids;
+ *                entries past a sequence's length are not used
+ *   seq_lens     device int32 [B], 0 .. max_len. A length outside that range,
+ *                or a page id outside the cache, gives NaN in that sequence's
+ *                heads and latches QMM_ERR_BAD_SLOT.
+ *   max_len      host bound on seq_lens, at most table_width * page_size
+ *   window       0: the whole sequence
+ *   out          device, dtype, [B][n_q_heads][head_dim]; lse  fp32
+ *                [B][n_q_heads] or NULL
+ *   workspace    device scratch of the caller, 16-byte aligned, at least
+ *                qattn_decode_workspace_bytes(...) bytes (may be NULL where
+ *                that is 0); calls that overlap must not share it
+ * head_dim is 64, 96, 128 or 256 (QMM_ERR_UNIMPLEMENTED otherwise).
+ */
+QMM_API int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs,
+                         const void* k_cache, const void* v_cache, size_t cache_bytes, int64_t n_pages,
+                         int64_t page_stride, int page_size, const int32_t* block_table, size_t table_elems,
+                         int64_t table_stride, int table_width, const int32_t* seq_lens, int max_len, int64_t B,
+                         int n_q_heads, int n_kv_heads, int head_dim, float scale, int window, float softcap,
+                         void* out, size_t out_elems, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Scratch bytes qattn_decode needs on the current device (0: none, or an
+ * argument it refuses). */
+QMM_API size_t qattn_decode_workspace_bytes(int fmt, int dtype, int64_t B, int n_q_heads, int n_kv_heads, int head_dim,
+                                            int max_len, int window);
+
+/*
  * qmm_check_device_error -- synchronize `stream`, then read and clear the
  * device-side error latch of the current device. Returns QMM_OK,
  * QMM_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel ran out; that kernel's
- * output is unspecified), QMM_ERR_BAD_EXPERT_ID, or QMM_ERR_CUDA.
+ * output is unspecified), QMM_ERR_BAD_EXPERT_ID, QMM_ERR_BAD_SLOT, or
+ * QMM_ERR_CUDA.
  */
 QMM_API int qmm_check_device_error(void* stream);
 
@@ -392,7 +547,8 @@ QMM_API int qmm_set_path(int path);
 
 /* Which kernel family the most recent successful call on this host thread
  * launched: 1 generic, 2 streaming GEMV, 3 tensor-core GEMM, 4 dequant,
- * 5 grouped GEMV, 6 MoE layer, 7 repacked (split-K) GEMV; 0 before any call. */
+ * 5 grouped GEMV, 6 MoE layer, 7 repacked (split-K) GEMV, 8 rotary, 9 cache
+ * store, 10 cache load, 11 decode attention; 0 before any call. */
 QMM_API int qmm_last_path(void);
 
 /* Number of kernels this library has launched since load (all threads). */
