@@ -7,29 +7,25 @@
 // Every cached row is read once per group of query heads that share it, so the
 // operator is bound by those bytes (K and V rows of the lengths in range).
 //
-// Tiles. A warp takes 16 * SUB keys at a time with up to 8 * NT query heads of
-// one key-value head, and keeps the running maximum m, sum l and output O of
-// the softmax in registers (fp32). Both products run on mma.sync m16n8k16 with
-// the KEYS (first product) or the DIMS (second) on the 16-row side and the
-// query heads on the 8-column side: S^T = K Q^T and O^T = V^T P^T. A group of
-// up to eight heads then fills the columns, K and V are the A operands and are
-// used by one warp only, so they go straight from global memory into the
-// registers that feed the MMA -- no shared memory, no barrier in the loop. At 8
-// heads the tensor work is 8 FLOP per cached byte, a small part of what
-// mma.sync sustains; tcgen05's 128-row tiles would be 8/128 full here.
+// Tiles. A warp takes 16 keys at a time with up to 8 * NT query heads of one
+// key-value head, and keeps the running maximum m, sum l and output O of the
+// softmax in registers (fp32). Both products run on mma.sync m16n8k16 with the
+// KEYS (first product) or the DIMS (second) on the 16-row side and the query
+// heads on the 8-column side: S^T = K Q^T and O^T = V^T P^T. A group of up to
+// eight heads then fills the columns. At 8 heads the tensor work is 8 FLOP per
+// cached byte, a small part of what mma.sync sustains; tcgen05's 128-row tiles
+// would be 8/128 full here.
 //
-// Operand layout without transposes through memory:
-//   * K: the sum over dims does not depend on their order, so lane (g, t) loads
-//     8 consecutive dims 32c + 8t .. + 7 of keys g and g + 8, and the q fragment
-//     is built in the same order.
-//   * V: lane (g, t) loads VW consecutive dims of keys 2t, 2t+1, 2t+8, 2t+9;
-//     pairs of keys are zipped by byte permutes. Row g of MMA tile j is dim
-//     VW g + 2j, row g + 8 the dim after it.
-//   * P: the accumulator layout of S^T becomes the B operand of the second
-//     product through movmatrix (an 8 x 8 transpose in registers).
-// Each warp issues the loads of its next K tile as soon as the first product
-// has consumed the present one, and those of V after the second, so loads are
-// in flight through the whole loop.
+// Loads. Each warp has a ring of STAGES tiles in shared memory, filled by its
+// own 16-byte asynchronous copies: no barrier between warps, and the bytes in
+// flight do not depend on registers. Rows are padded by 16 bytes, so that the
+// 8 x 8 matrices that ldmatrix reads touch every bank once. ldmatrix gives K's
+// operand as it is and V's transposed. For Q8_0 a 16-bit matrix element is two
+// codes: lane (g, t) gets codes 4t .. 4t + 3 of key g (K), or dims 2g, 2g + 1
+// of keys 2t, 2t + 1 (V, transposed), and the byte permutes that widen the
+// codes put them in the order that the MMA wants; q is laid out to match.
+// P passes from the accumulator layout of S^T to the B operand of the second
+// product by movmatrix (an 8 x 8 transpose in registers).
 //
 // Rounding. Products of a 16-bit cache are exact in fp32. q and the softmax
 // weights p enter the MMAs as sums of 16-bit terms: two f16 terms carry 22
@@ -37,10 +33,23 @@
 // rounding then stays well under the output's own); with fp32 activations q
 // and p take as many as reach fp32 (f16: 2, bf16: 3). f16 terms need a bounded
 // range: fp32 / bf16 q rows are scaled by a power of two that puts their
-// largest magnitude in [2^9, 2^10), p is held as 2^14 e^{s - m}. Q8_0 codes are
-// integers, exact in f16 and bf16: K's block scale multiplies the fp32 partial
-// sums of its 32 dims, V's block scale multiplies p before it is split.
+// largest magnitude in [2^9, 2^10), and weights are held as 2^14 e^{s - m}.
+//
+// Q8_0 codes enter exactly. K: the biased code u = c + 128 in the low byte is
+// the f16 subnormal u 2^-24; the block's product starts at -128 2^-24 sum q to
+// take the bias out, and K's block scale multiplies the fp32 partial sum of the
+// 32 dims. The bias costs a factor of two in the sum's magnitude, no more,
+// because |u| < 256 against |c| < 128; in the second product, whose sums over
+// thousands of keys cancel, codes enter without bias (1024 + u minus 1152).
+// V's block scale d multiplies the two terms of p: t1 = rn(ph d), then
+// t2 = rn(pl d + (ph d - t1)), where the bracket is exact in one fma. A power
+// of two, from the running largest exponent of V's scales, keeps d near 1.
+//
+// The running maximum moves only where a score exceeds it (a vote over the
+// warp), so most tiles do without the maximum over lanes and the rescaling.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_common.cuh"
 
@@ -56,28 +65,29 @@ template <> struct Terms<QMM_KV_F16, true> { static constexpr int q = 2, p = 2; 
 template <> struct Terms<QMM_KV_BF16, false> { static constexpr int q = 1, p = 2; };   // bf16 q
 template <> struct Terms<QMM_KV_BF16, true> { static constexpr int q = 3, p = 3; };    // f16, fp32 q
 template <> struct Terms<QMM_KV_Q8_0, false> { static constexpr int q = 1, p = 2; };   // f16 q
-template <> struct Terms<QMM_KV_Q8_0, true> { static constexpr int q = 2, p = 3; };    // bf16, fp32 q
+template <> struct Terms<QMM_KV_Q8_0, true> { static constexpr int q = 2, p = 2; };    // bf16, fp32 q
 
 __host__ __device__ constexpr bool needs_hi(int fmt, int dtype) {
     return fmt == QMM_KV_BF16 ? dtype != QMM_BF16 : dtype != QMM_F16;
 }
 
+// d = a b + c
 template <bool BF>
 __device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                    unsigned b1) {
+                                    unsigned b1, float c0, float c1, float c2, float c3) {
     if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ unsigned transpose8x8(unsigned x) {
     unsigned y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -103,11 +113,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Four int8 codes (in byte order) as two f16 pairs, exactly: the biased code u =
-// c + 128 in the low mantissa byte of 1024 is the f16 number 1024 + u.
+// Four int8 codes as two f16 pairs, (bytes 0, 2) and (bytes 1, 3), exactly: the
+// biased code u = c + 128 in the low mantissa byte of 1024 is 1024 + u.
 __device__ __forceinline__ void codes_f16(unsigned x, unsigned& p0, unsigned& p1) {
-    x ^= 0x80808080u;
-    const unsigned a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const unsigned a = (x & 0x00ff00ffu) ^ 0x64806480u, b = __byte_perm(x, 0u, 0x4341) ^ 0x64806480u;
     const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1152
     const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
     const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
@@ -115,22 +124,14 @@ __device__ __forceinline__ void codes_f16(unsigned x, unsigned& p0, unsigned& p1
     p1 = *reinterpret_cast<const unsigned*>(&r1);
 }
 
-// Four int8 codes as two bf16 pairs, exactly: the low seven bits in the mantissa
-// of 128 give 128 + low7; the sign bit in the exponent's last place gives 128
-// or 256; their difference is the code.
-__device__ __forceinline__ void codes_bf16(unsigned x, unsigned& p0, unsigned& p1) {
-    const unsigned lo = x & 0x7f7f7f7fu, hi = x & 0x80808080u;
-    const unsigned a0 = __byte_perm(lo, 0x43434343u, 0x4140), a1 = __byte_perm(lo, 0x43434343u, 0x4342);
-    const unsigned b0 = __byte_perm(hi, 0x43434343u, 0x4140), b1 = __byte_perm(hi, 0x43434343u, 0x4342);
-    const __nv_bfloat162 r0 =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a0), *reinterpret_cast<const __nv_bfloat162*>(&b0));
-    const __nv_bfloat162 r1 =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a1), *reinterpret_cast<const __nv_bfloat162*>(&b1));
-    p0 = *reinterpret_cast<const unsigned*>(&r0);
-    p1 = *reinterpret_cast<const unsigned*>(&r1);
+// The same pairs as f16 subnormals (c + 128) 2^-24, exactly.
+__device__ __forceinline__ void codes_sub(unsigned x, unsigned& p0, unsigned& p1) {
+    p0 = (x & 0x00ff00ffu) ^ 0x00800080u;
+    p1 = __byte_perm(x, 0u, 0x4341) ^ 0x00800080u;
 }
 
-template <typename V> __device__ __forceinline__ V ldg(const uint8_t* p) { return *reinterpret_cast<const V*>(p); }
+__device__ __forceinline__ __half2 as_half2(unsigned x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ unsigned as_u32(__half2 x) { return *reinterpret_cast<const unsigned*>(&x); }
 
 __device__ __forceinline__ float load_act(const void* p, int dtype, int64_t i) {
     if (dtype == QMM_F32) return static_cast<const float*>(p)[i];
@@ -161,7 +162,7 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, int64_t b, int chun
 }
 
 // Partial results in the workspace: O [B * Hq][splits][D], then (m, l) pairs
-// [B * Hq][splits]; m in units of log2.
+// [B * Hq][splits]; m, the log2 of the unit of O and l.
 __device__ __forceinline__ float* ws_o(const AttnArgs& a, int splits, int64_t bh, int s) {
     return static_cast<float*>(a.ws) + (bh * splits + s) * a.c.D;
 }
@@ -171,23 +172,62 @@ __device__ __forceinline__ float2* ws_ml(const AttnArgs& a, int splits, int64_t 
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int FMT, int D, bool HI, int NT, int SUB>
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes global -> shared; `bytes` 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's newest groups are in flight.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(unsigned (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Shared-memory layout of a block: the warps' rings; after the loop, the
+// warps' outputs in the same place.
+template <int FMT, int D, int NT, int STAGES> struct Layout {
+    static constexpr bool Q8 = FMT == QMM_KV_Q8_0;
+    static constexpr int C = D / 32;
+    static constexpr int ROW = Q8 ? D : 2 * D;              // bytes of a row's codes or values
+    static constexpr int RS = ROW + 16;                     // row pitch
+    static constexpr int V0 = 16 * RS;                      // K rows, V rows, K scales, V scales
+    static constexpr int S0 = 32 * RS;
+    static constexpr int STAGE = S0 + (Q8 ? 64 * C : 0);
+    static constexpr int RING = STAGES * STAGE;             // of one warp
+    static constexpr int OD = D + 4;
+    static constexpr int JOIN = kWarps * 8 * NT * OD * 4;
+    static constexpr int BYTES = kWarps * RING > JOIN ? kWarps * RING : JOIN;
+};
+
+template <int FMT, int D, bool HI, int NT, int STAGES>
 __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int chunk, int head_chunks) {
+    using Lay = Layout<FMT, D, NT, STAGES>;
     constexpr bool Q8 = FMT == QMM_KV_Q8_0;
-    constexpr bool KBF = FMT == QMM_KV_BF16;          // operand type of K q and of V p
-    constexpr bool VBF = FMT != QMM_KV_F16;
+    constexpr bool BF = FMT == QMM_KV_BF16;           // operand type of both products: bf16, else f16
     constexpr int NQ = Terms<FMT, HI>::q, NP = Terms<FMT, HI>::p;
     constexpr int C = D / 32;                         // 32-dim blocks of a row
-    constexpr int KT = 16 * SUB;                      // keys per tile
-    constexpr int VW = !Q8 && D % 64 == 0 ? 8 : 4;    // dims per lane of a V row
-    constexpr int VC = D / (8 * VW);                  // V chunks of 8 * VW dims
-    constexpr float kBias = VBF ? 0.f : 14.f;
-    using KVec = typename VecOf<Q8 ? 8 : 16>::type;
-    using VVec = typename VecOf<Q8 ? 4 : 2 * VW>::type;
-    constexpr int KW = sizeof(KVec) / 4;
+    constexpr int KT = 16;                            // keys per tile
+    constexpr int ROW = Lay::ROW, RS = Lay::RS;
+    constexpr int MT = D / 16;                        // 16-dim tiles of the output
 
-    __shared__ float sm_o[kWarps][8 * NT][D + 4];     // the query rows first, the warps' outputs last
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float sm_q[8 * NT][D + 4];
     __shared__ float sm_m[kWarps][8 * NT], sm_l[kWarps][8 * NT], sm_scale[8 * NT];
+    __shared__ float sm_qsum[8 * NT][Q8 ? C : 1];
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     // block -> (sequence, key-value head, chunk of its query heads, split)
@@ -220,96 +260,82 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     const int32_t* table = a.table + b * a.table_stride;
     const int64_t unit = a.c.unit();
     const uint8_t* kbase = a.c.k + kh * unit;
-    const uint8_t* vbase = a.c.v + kh * unit;
+    const int64_t v_minus_k = a.c.v - a.c.k;
     bool bad = false;
 
-    // Page ids of the 8-key groups of a tile: a group lies in one page (pages
-    // hold 8 or more keys, tiles start at multiples of 16). Groups outside the
-    // range name a page inside it, so that every address is that of a page the
-    // sequence owns; their scores and V rows are masked below.
-    auto page_ids = [&](int base, int (&id)[2 * SUB]) {
+    // Page ids of the two 8-key groups of a tile: a group lies in one page
+    // (pages hold 8 or more keys, tiles start at multiples of 16). Groups
+    // outside the range name a page inside it, so that every address is that
+    // of a page the sequence owns.
+    auto page_ids = [&](int base, int (&id)[2]) {
 #pragma unroll
-        for (int i = 0; i < 2 * SUB; ++i) id[i] = table[max(page_lo, min((base + 8 * i) >> shift, page_hi))];
+        for (int i = 0; i < 2; ++i) id[i] = table[max(page_lo, min((base + 8 * i) >> shift, page_hi))];
     };
-    auto page_at = [&](int id) -> int64_t {
-        if (static_cast<unsigned>(id) >= static_cast<uint64_t>(a.c.n_pages)) {
-            bad = true;
-            id = 0;
+    const uint32_t ring = smem_addr(smem) + warp * Lay::RING;
+    // Copies one tile to a stage. The rows of an 8-key group are contiguous in
+    // the cache. Rows outside the range become zeros (what the cache holds
+    // there must not reach the products: 0 * NaN).
+    auto load_tile = [&](int base, const int (&id)[2], uint32_t stage) {
+        int64_t off[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool ok = static_cast<unsigned>(id[i]) < static_cast<uint64_t>(a.c.n_pages);
+            bad |= !ok;
+            off[i] = ok ? id[i] * a.c.page_stride : 0;
         }
-        return id * a.c.page_stride;
-    };
-    constexpr int ROW = Q8 ? D : 2 * D;               // bytes of a row's codes or values
-    KVec kreg[SUB][2][C];
-    VVec vreg[SUB][4][VC];
-    // Q8_0 scales of keys g, g + 8 of each 16-key group
-    __half kscale[Q8 ? SUB : 1][2][Q8 ? C : 1], vscale[Q8 ? SUB : 1][2][Q8 ? C : 1];
-    auto load_scales = [&](const uint8_t* p, __half (&d)[Q8 ? C : 1]) {
+        const int row0 = base & page_mask, row1 = (base + 8) & page_mask;
+        constexpr int CPR = ROW / 16;                 // 16-byte pieces of a row
+        const bool partial = base < rg.lo || base + KT > end;
         if constexpr (Q8) {
-            constexpr int B = C % 4 == 0 ? 8 : C % 2 == 0 ? 4 : 2;
-            using SV = typename VecOf<B>::type;
-#pragma unroll
-            for (int i = 0; i < 2 * C / B; ++i) {
-                const SV v = reinterpret_cast<const SV*>(p)[i];
-                const __half* e = reinterpret_cast<const __half*>(&v);
-#pragma unroll
-                for (int j = 0; j < B / 2; ++j) d[i * (B / 2) + j] = e[j];
+            if (lane < 4 * C) {                       // scales: C pieces per group, of K then of V
+                const int grp = lane / C % 2, col = lane % C;
+                const uint8_t* p = kbase + (lane < 2 * C ? 0 : v_minus_k) + (grp ? off[1] : off[0]) + (D << shift) +
+                                   (grp ? row1 : row0) * (2 * C) + col * 16;
+                copy16(stage + Lay::S0 + lane * 16, p, 16);
             }
         }
-    };
-    auto load_k = [&](int base, const int (&id)[2 * SUB]) {
+        const uint8_t* pk[2] = {kbase + off[0] + row0 * ROW + lane * 16, kbase + off[1] + row1 * ROW + lane * 16 - 8 * ROW};
+        const uint8_t* pv[2] = {pk[0] + v_minus_k, pk[1] + v_minus_k};
+        const uint32_t dst0 = stage + lane / CPR * RS + lane % CPR * 16;
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t* p = kbase + page_at(id[2 * s + i]);
-                const int row = (base + 16 * s + 8 * i + g) & page_mask;
-                const uint8_t* q = p + row * ROW + t * static_cast<int>(sizeof(KVec));
-#pragma unroll
-                for (int c = 0; c < C; ++c) kreg[s][i][c] = ldg<KVec>(q + c * (ROW / C));
-                if constexpr (Q8) load_scales(p + (D << shift) + row * (2 * C), kscale[s][i]);
-            }
-    };
-    auto load_v = [&](int base, const int (&id)[2 * SUB]) {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t* p = vbase + page_at(id[2 * s + i]);
-                const int row = (base + 16 * s + 8 * i + 2 * t) & page_mask;
-                const uint8_t* q = p + row * ROW + g * static_cast<int>(sizeof(VVec));
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int c = 0; c < VC; ++c)
-                        vreg[s][2 * i + k][c] = ldg<VVec>(q + k * ROW + c * (ROW / VC));
-                if constexpr (Q8) {
-                    const int srow = (base + 16 * s + 8 * i + g) & page_mask;
-                    load_scales(p + (D << shift) + srow * (2 * C), vscale[s][i]);
-                }
-            }
+        for (int i = 0; i < ROW / 32; ++i) {
+            const int q = 32 * i + lane;              // this lane's piece of the tile's rows
+            const int row = q / CPR;
+            const int grp = (ROW / 2) % 32 == 0 ? 32 * i / (ROW / 2) : row / 8;
+            const uint32_t dst = 32 % CPR == 0 ? dst0 + i * (32 / CPR) * RS : CPR == 32 ? dst0 + i * RS : stage + row * RS + q % CPR * 16;
+            int n = 16;
+            if (partial) n = base + row >= rg.lo && base + row < end ? 16 : 0;
+            copy16(dst, pk[grp] + i * 512, n);
+            copy16(dst + Lay::V0, pv[grp] + i * 512, n);
+        }
     };
 
-    const int stride = kWarps * KT;
+    constexpr int stride = kWarps * KT;
     int base = begin + warp * KT;
-    int id0[2 * SUB], id1[2 * SUB];
-    if (base < end) {
-        page_ids(base, id0);
-        page_ids(base + stride, id1);
-        load_k(base, id0);
-        load_v(base, id0);
+    int id[2];                                        // pages of the next tile to load
+    int ahead = base;                                 // its first key
+    page_ids(ahead, id);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (ahead < end) {
+            load_tile(ahead, id, ring + i * Lay::STAGE);
+            ahead += stride;
+            page_ids(ahead, id);
+        }
+        copies_commit();
     }
 
-    // ---- the query fragments: B operand, column g = head, dims in K's order
+    // ---- the query fragments: B operand, column g = head
     for (int i = threadIdx.x; i < 8 * NT * D; i += kThreads) {
         const int h = i / D, d = i % D;
-        sm_o[0][h][d] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
+        sm_q[h][d] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
     }
     __syncthreads();
-    constexpr bool NORM = HI && !KBF;                 // f16 terms of fp32 / bf16 rows
+    constexpr bool NORM = HI && !BF;                  // f16 terms of fp32 / bf16 rows
     if (NORM) {
         for (int h = warp; h < 8 * NT; h += kWarps) {
             float m = 0.f;
-            for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(sm_o[0][h][d]));
+            for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(sm_q[h][d]));
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             // m in [2^e, 2^(e+1)) -> factor 2^(9 - e); none for zeros and Inf
@@ -319,243 +345,321 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         }
         __syncthreads();
     }
-    unsigned qf[NT][NQ][4 * C];
-    float sc[NT][2];                                  // score scale of heads 2t, 2t + 1
+    if constexpr (Q8) {
+        // -128 2^-24 times the sum of the q terms of each 32-dim block
+        for (int i = threadIdx.x; i < 8 * NT * C; i += kThreads) {
+            const int h = i / C, c = i % C;
+            const float f = NORM ? sm_scale[h] : 1.f;
+            float sum = 0.f;
+            for (int d = 0; d < 32; ++d) {
+                const float x = sm_q[h][32 * c + d] * f;
+                float rest = x, none = 0.f;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) take16<false>(rest, none);
+                sum += x - rest;
+            }
+            sm_qsum[h][c] = sum * -7.62939453125e-06f;
+        }
+        __syncthreads();
+    }
+    unsigned qf[NT][NQ][MT][2];
+    float qb[NT][Q8 ? C : 1][2];                      // of heads 2t, 2t + 1
+    float sc[NT][2];                                  // score scale of heads 2t, 2t + 1, to log2 units unless capped
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const float f = NORM ? sm_scale[8 * n + g] : 1.f;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float x0 = sm_o[0][8 * n + g][32 * c + 8 * t + 2 * j] * f;
-                float x1 = sm_o[0][8 * n + g][32 * c + 8 * t + 2 * j + 1] * f;
+            for (int k = 0; k < 2; ++k) {
+                // dims 2t, 2t + 1 (+ 8) of the 16, or with Q8_0 4t, 4t + 2 (+ 1)
+                const int d = 16 * j + (Q8 ? 4 * t + k : 2 * t + 8 * k);
+                float x0 = sm_q[8 * n + g][d] * f, x1 = sm_q[8 * n + g][d + (Q8 ? 2 : 1)] * f;
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) qf[n][q][4 * c + j] = take16<KBF>(x0, x1);
+                for (int q = 0; q < NQ; ++q) qf[n][q][j][k] = take16<BF>(x0, x1);
             }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) sc[n][k] = NORM ? a.scale / sm_scale[8 * n + 2 * t + k] : a.scale;
+        for (int k = 0; k < 2; ++k) {
+            sc[n][k] = a.scale * (Q8 ? 16777216.f : 1.f) * (a.softcap > 0.f ? 1.f : kLog2e);
+            if (NORM) sc[n][k] /= sm_scale[8 * n + 2 * t + k];
+            if constexpr (Q8) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) qb[n][c][k] = sm_qsum[8 * n + 2 * t + k][c];
+            }
+        }
     }
 
-    float m[NT][2], l[NT][2], o[NT][VC][VW / 2][4];
+    // Weights are 2^(score - ref) <= 2^kTop: f16 terms use the top of their
+    // range. Before the first score, ref is kNone: every finite score exceeds it.
+    constexpr float kTop = BF ? 0.f : 14.f, kNone = -1e30f;
+    float ref[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
+        ref[n][0] = ref[n][1] = kNone;
         l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int j = 0; j < VW / 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][c][j][i] = 0.f;
+            for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
     }
+    // Q8_0: V's scales are below v_lim = 2^E and are multiplied by v_mul = 2^k,
+    // k = -E within f16's range; O carries that factor
+    __half2 v_lim = __float2half2_rn(0.f), v_mul = __float2half2_rn(1.f);
 
-#pragma unroll 1
-    for (; base < end; base += stride) {
-        int id2[2 * SUB];
-        const bool more = base + stride < end;
-        page_ids(base + 2 * stride, id2);
+    // matrix mi of an ldmatrix: lanes 8 mi .. 8 mi + 7 give its rows
+    const int mi = lane / 8, mr = lane % 8;
+    const uint32_t k_lane = (mr + 8 * (mi & 1)) * RS + 16 * (mi >> 1);
+    const uint32_t v_lane = Lay::V0 + (Q8 ? k_lane : (mr + 8 * (mi >> 1)) * RS + 16 * (mi & 1));
+    uint32_t stage = ring, fill = ring + (STAGES - 1) * Lay::STAGE;
+    const uint32_t ring_end = ring + Lay::RING, smem_base = smem_addr(smem);
+
+    // One tile. `slow`: some keys are masked, or scores are capped.
+    auto tile = [&](auto slow_tag) {
+        constexpr bool SLOW = decltype(slow_tag)::value;
         // ---- S^T = K Q^T
-        float sx[NT][SUB][4];
+        float sx[NT][4];
+        if constexpr (Q8) {
+            constexpr int B = C % 4 == 0 ? 8 : C % 2 == 0 ? 4 : 2;
+            using SV = typename VecOf<B>::type;
+            __half kscale[2][C];                      // of keys g, g + 8
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2 * C / B; ++k) {
+                    const SV x = reinterpret_cast<const SV*>(smem + (stage - smem_base) + Lay::S0 + (g + 8 * i) * (2 * C))[k];
+#pragma unroll
+                    for (int j = 0; j < B / 2; ++j) kscale[i][k * (B / 2) + j] = reinterpret_cast<const __half*>(&x)[j];
+                }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                unsigned w[4];                        // (key g, g + 8) of dims 0 .. 15, then of 16 .. 31
+                ldsm4(w, stage + k_lane + 32 * c);
+                unsigned x[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    codes_sub(w[2 * j], x[j][0], x[j][2]);
+                    codes_sub(w[2 * j + 1], x[j][1], x[j][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float acc[4] = {qb[n][c][0], qb[n][c][1], qb[n][c][0], qb[n][c][1]};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], qf[n][q][2 * c + j][0], qf[n][q][2 * c + j][1],
+                                    acc[0], acc[1], acc[2], acc[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float d = __half2float(kscale[i >> 1][c]);
+                        sx[n][i] = c == 0 ? d * acc[i] : fmaf(d, acc[i], sx[n][i]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                unsigned x[4];
+                ldsm4(x, stage + k_lane + 32 * j);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const bool first = j == 0 && q == 0;
+                        mma<BF>(sx[n], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1], first ? 0.f : sx[n][0],
+                                first ? 0.f : sx[n][1], first ? 0.f : sx[n][2], first ? 0.f : sx[n][3]);
+                    }
+            }
+        }
+
+        // ---- scores, in log2 units
+        if constexpr (SLOW) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = sx[n][i] * sc[n][i & 1];
+                    if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x / a.softcap);
+                    const int key = base + 8 * (i >> 1) + g;
+                    if (key < rg.lo || key >= end) x = -INFINITY;
+                    sx[n][i] = x;
+                }
+        }
+        auto rel = [&](int n, int i) {                // score - ref
+            return SLOW ? sx[n][i] - ref[n][i & 1] : fmaf(sx[n][i], sc[n][i & 1], -ref[n][i & 1]);
+        };
+        float y[NT][4];
+        bool grew = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
+            for (int i = 0; i < 4; ++i) {
+                y[n][i] = rel(n, i);
+                grew |= y[n][i] > kTop;
+            }
+        [[maybe_unused]] unsigned vd[2][Q8 ? C : 1];                   // V scales of keys (2t, 2t + 1) and (2t + 8, 2t + 9)
+        __half2 v_top = v_lim;
+        if constexpr (Q8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sx[n][s][i] = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t* p = smem + (stage - smem_base) + Lay::S0 + 32 * C + (2 * t + 8 * i) * (2 * C);
+                if constexpr (C % 2 == 0) {
+                    constexpr int B = C % 4 == 0 ? 8 : 4;
+                    using SV = typename VecOf<B>::type;
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
+                    for (int k = 0; k < 2 * C / B; ++k) {
+                        const SV x = reinterpret_cast<const SV*>(p)[k], z = reinterpret_cast<const SV*>(p + 2 * C)[k];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                unsigned x0[4], x1[4];                // dims 8t .. 8t + 7 of keys g and g + 8 as 16-bit pairs
-                if constexpr (Q8) {
-                    const unsigned* w0 = reinterpret_cast<const unsigned*>(&kreg[s][0][c]);
-                    const unsigned* w1 = reinterpret_cast<const unsigned*>(&kreg[s][1][c]);
-#pragma unroll
-                    for (int k = 0; k < KW; ++k) {
-                        codes_f16(w0[k], x0[2 * k], x0[2 * k + 1]);
-                        codes_f16(w1[k], x1[2 * k], x1[2 * k + 1]);
+                        for (int j = 0; j < B / 4; ++j) {
+                            const unsigned u = reinterpret_cast<const unsigned*>(&x)[j];
+                            const unsigned v = reinterpret_cast<const unsigned*>(&z)[j];
+                            vd[i][k * (B / 2) + 2 * j] = __byte_perm(u, v, 0x5410);
+                            vd[i][k * (B / 2) + 2 * j + 1] = __byte_perm(u, v, 0x7632);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        x0[k] = reinterpret_cast<const unsigned*>(&kreg[s][0][c])[k];
-                        x1[k] = reinterpret_cast<const unsigned*>(&kreg[s][1][c])[k];
-                    }
+                    for (int c = 0; c < C; ++c)
+                        vd[i][c] = reinterpret_cast<const unsigned short*>(p)[c] |
+                                   static_cast<unsigned>(reinterpret_cast<const unsigned short*>(p + 2 * C)[c]) << 16;
+                }
+                if constexpr (SLOW) {                 // rows outside the range are zeros, their scales are not
+                    const int key = base + 8 * i + 2 * t;
+                    const unsigned keep = (key >= rg.lo && key < end ? 0xffffu : 0u) |
+                                          (key + 1 >= rg.lo && key + 1 < end ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) vd[i][c] &= keep;
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (Q8) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                mma<KBF>(acc, x0[2 * j], x1[2 * j], x0[2 * j + 1], x1[2 * j + 1],
-                                         qf[n][q][4 * c + 2 * j], qf[n][q][4 * c + 2 * j + 1]);
-                        const float d0 = __half2float(kscale[s][0][c]), d1 = __half2float(kscale[s][1][c]);
-                        sx[n][s][0] = fmaf(d0, acc[0], sx[n][s][0]);
-                        sx[n][s][1] = fmaf(d0, acc[1], sx[n][s][1]);
-                        sx[n][s][2] = fmaf(d1, acc[2], sx[n][s][2]);
-                        sx[n][s][3] = fmaf(d1, acc[3], sx[n][s][3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                mma<KBF>(sx[n][s], x0[2 * j], x1[2 * j], x0[2 * j + 1], x1[2 * j + 1],
-                                         qf[n][q][4 * c + 2 * j], qf[n][q][4 * c + 2 * j + 1]);
-                    }
-                }
+                for (int c = 0; c < C; ++c) v_top = __hmax2(v_top, as_half2(vd[i][c]));
             }
-        if (more) load_k(base + stride, id1);
-
-        // ---- masks, running maximum, weights
-        const bool partial = base < rg.lo || base + KT > end;
-        float alpha[NT][2];
-        bool grew = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x = sx[n][s][i] * sc[n][i & 1];
-                    if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-                    x *= kLog2e;
-                    if (partial) {
-                        const int key = base + 16 * s + 8 * (i >> 1) + g;
-                        if (key < rg.lo || key >= end) x = -INFINITY;
-                    }
-                    sx[n][s][i] = x;
-                    mt[i & 1] = fmaxf(mt[i & 1], x);
-                }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 4));
-                mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 8));
-                mt[k] = fmaxf(mt[k], __shfl_xor_sync(0xffffffffu, mt[k], 16));
-                const float mn = fmaxf(m[n][k], mt[k]);
-                grew |= mn > m[n][k];
-                // before the first finite score m is -inf and O, l are zero: any
-                // finite reference gives weights 0
-                alpha[n][k] = mn == -INFINITY ? 1.f : ex2(m[n][k] - mn);
-                m[n][k] = mn;
-            }
+            grew |= !__hbleu2(v_top, v_lim);
         }
         if (__any_sync(0xffffffffu, grew)) {
+            float up = 1.f;                           // change of O's factor
+            if constexpr (Q8) {
+                const unsigned w = as_u32(v_top);
+                const unsigned top = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
+                if (top > (as_u32(v_lim) & 0xffffu)) {
+                    // scales are below 2^(field - 14) by their exponent field;
+                    // one step more, so that few tiles raise it again
+                    const int e = min(static_cast<int>(top >> 10) - 13, 16);
+                    const __half2 mul = __float2half2_rn(exp2f(static_cast<float>(max(-15, min(15, -e)))));
+                    up = __low2float(mul) / __low2float(v_mul);
+                    v_mul = mul;
+                    v_lim = __float2half2_rn(exp2f(static_cast<float>(e)));
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                l[n][0] *= alpha[n][0];
-                l[n][1] *= alpha[n][1];
+                float alpha[2];
 #pragma unroll
-                for (int c = 0; c < VC; ++c)
+                for (int k = 0; k < 2; ++k) {
+                    float mt = SLOW ? fmaxf(sx[n][k], sx[n][k + 2]) : fmaxf(sx[n][k] * sc[n][k], sx[n][k + 2] * sc[n][k]);
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                    const float now = fmaxf(ref[n][k], mt - kTop);
+                    alpha[k] = ex2(ref[n][k] - now);
+                    ref[n][k] = now;
+                    l[n][k] *= alpha[k];
+                    alpha[k] *= up;
+                }
 #pragma unroll
-                    for (int j = 0; j < VW / 2; ++j)
+                for (int j = 0; j < MT; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][c][j][i] *= alpha[n][i & 1];
+                    for (int i = 0; i < 4; ++i) o[n][j][i] *= alpha[i & 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[n][i] = rel(n, i);
             }
         }
+        // ---- weights, as the B operand of the second product
+        unsigned pf[NT][NP][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kBias;
-            const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kBias;
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sx[n][s][i] = ex2(sx[n][s][i] - (i & 1 ? r1 : r0));
-                    l[n][i & 1] += sx[n][s][i];
-                }
-        }
-
-        // ---- O^T += V^T P^T. Rows outside the range may hold anything (0 * NaN).
-        if (partial) {
-#pragma unroll
-            for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = base + 16 * s + 8 * (i >> 1) + 2 * t + (i & 1);
-                    if (key < rg.lo || key >= end) {
-#pragma unroll
-                        for (int c = 0; c < VC; ++c) vreg[s][i][c] = VVec{};
-                    }
-                    if constexpr (Q8) {
-                        const int skey = base + 16 * s + 8 * (i >> 1) + g;
-                        if ((i & 1) == 0 && (skey < rg.lo || skey >= end)) {
-#pragma unroll
-                            for (int c = 0; c < C; ++c) vscale[s][i >> 1][c] = __ushort_as_half(0);
-                        }
-                    }
-                }
-        }
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            unsigned pf[NT][NP][2];
-            if constexpr (!Q8) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float x[4] = {sx[n][s][0], sx[n][s][1], sx[n][s][2], sx[n][s][3]};
-#pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        pf[n][q][0] = transpose8x8(take16<VBF>(x[0], x[1]));
-                        pf[n][q][1] = transpose8x8(take16<VBF>(x[2], x[3]));
-                    }
-                }
+            for (int i = 0; i < 4; ++i) {
+                y[n][i] = ex2(y[n][i]);
+                l[n][i & 1] += y[n][i];
             }
 #pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                if constexpr (Q8) {
-                    const float d0 = __half2float(vscale[s][0][c]), d1 = __half2float(vscale[s][1][c]);
+            for (int q = 0; q < NP; ++q) {
+                pf[n][q][0] = transpose8x8(take16<BF>(y[n][0], y[n][1]));
+                pf[n][q][1] = transpose8x8(take16<BF>(y[n][2], y[n][3]));
+            }
+        }
+        // ---- O^T += V^T P^T
+        if constexpr (Q8) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                unsigned pd[NT][2][2];                // p times the block's scale
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 d = __hmul2(as_half2(vd[i][c]), v_mul);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float x[4] = {sx[n][s][0] * d0, sx[n][s][1] * d0, sx[n][s][2] * d1, sx[n][s][3] * d1};
-#pragma unroll
-                        for (int q = 0; q < NP; ++q) {
-                            pf[n][q][0] = transpose8x8(take16<VBF>(x[0], x[1]));
-                            pf[n][q][1] = transpose8x8(take16<VBF>(x[2], x[3]));
-                        }
+                        const __half2 hi = as_half2(pf[n][0][i]), t1 = __hmul2_rn(hi, d);
+                        pd[n][0][i] = as_u32(t1);
+                        pd[n][1][i] = as_u32(__hfma2(as_half2(pf[n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
                     }
                 }
-                unsigned f[VW / 2][4];                // A operand of each 16-dim tile
-                if constexpr (Q8) {
+                unsigned w[4];
+                ldsm4_trans(w, stage + v_lane + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {     // keys 2t, 2t + 1 (and + 8): bytes zipped, then widened
-                        const unsigned w0 = *reinterpret_cast<const unsigned*>(&vreg[s][2 * i][c]);
-                        const unsigned w1 = *reinterpret_cast<const unsigned*>(&vreg[s][2 * i + 1][c]);
-                        codes_bf16(__byte_perm(w0, w1, 0x5140), f[0][2 * i], f[0][2 * i + 1]);
-                        codes_bf16(__byte_perm(w0, w1, 0x7362), f[1][2 * i], f[1][2 * i + 1]);
-                    }
-                } else {
+                for (int j = 0; j < 2; ++j) {
+                    unsigned f[4];
+                    codes_f16(w[2 * j], f[0], f[1]);
+                    codes_f16(w[2 * j + 1], f[2], f[3]);
 #pragma unroll
-                    for (int j = 0; j < VW / 2; ++j)
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const unsigned w0 = reinterpret_cast<const unsigned*>(&vreg[s][2 * i][c])[j];
-                            const unsigned w1 = reinterpret_cast<const unsigned*>(&vreg[s][2 * i + 1][c])[j];
-                            f[j][2 * i] = __byte_perm(w0, w1, 0x5410);
-                            f[j][2 * i + 1] = __byte_perm(w0, w1, 0x7632);
+                        for (int n = 0; n < NT; ++n) {
+                            float(&d)[4] = o[n][2 * c + j];
+                            mma<BF>(d, f[0], f[1], f[2], f[3], pd[n][q][0], pd[n][q][1], d[0], d[1], d[2], d[3]);
                         }
                 }
+            }
+        } else {
 #pragma unroll
-                for (int j = 0; j < VW / 2; ++j)
+            for (int j = 0; j < MT; ++j) {
+                unsigned f[4];
+                ldsm4_trans(f, stage + v_lane + 32 * j);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int q = 0; q < NP; ++q)
 #pragma unroll
-                        for (int q = 0; q < NP; ++q)
-                            mma<VBF>(o[n][c][j], f[j][0], f[j][1], f[j][2], f[j][3], pf[n][q][0], pf[n][q][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        float(&d)[4] = o[n][j];
+                        mma<BF>(d, f[0], f[1], f[2], f[3], pf[n][q][0], pf[n][q][1], d[0], d[1], d[2], d[3]);
+                    }
             }
         }
-        if (more) load_v(base + stride, id1);
-#pragma unroll
-        for (int i = 0; i < 2 * SUB; ++i) id1[i] = id2[i];
+    };
+
+#pragma unroll 1
+    for (; base < end; base += stride) {
+        __syncwarp();                                 // every lane is done with the stage filled next
+        if (ahead < end) {
+            load_tile(ahead, id, fill);
+            ahead += stride;
+            page_ids(ahead, id);
+        }
+        copies_commit();
+        copies_wait<STAGES - 1>();
+        __syncwarp();                                 // the tile's copies by all lanes are visible
+        if (base < rg.lo || base + KT > end || a.softcap > 0.f) tile(std::true_type{});
+        else tile(std::false_type{});
+        fill = stage;
+        stage += Lay::STAGE;
+        if (stage == ring_end) stage = ring;
     }
 
     // ---- the block's warps joined
+    copies_wait<0>();
     bad = __any_sync(0xffffffffu, bad);
     if (bad && lane == 0) atomicOr(a.err, DEV_ERR_BAD_SLOT);
-    __syncthreads();                                  // sm_o's query rows are consumed
+    __syncthreads();                                  // every warp's ring is consumed
+    float* sm_o = reinterpret_cast<float*>(smem);     // [warp][head][OD]
+    constexpr int OD = Lay::OD;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -564,17 +668,18 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], 8);
             l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], 16);
             if (g == 0) {
-                sm_m[warp][8 * n + 2 * t + k] = m[n][k];
+                sm_m[warp][8 * n + 2 * t + k] = ref[n][k] == kNone ? -INFINITY : ref[n][k];
                 sm_l[warp][8 * n + 2 * t + k] = bad ? NAN : l[n][k];
             }
         }
+        float* p = sm_o + (warp * 8 * NT + 8 * n + 2 * t) * OD;
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int j = 0; j < VW / 2; ++j) {
-                const int d = 8 * VW * c + VW * g + 2 * j;
-                *reinterpret_cast<float2*>(&sm_o[warp][8 * n + 2 * t][d]) = make_float2(o[n][c][j][0], o[n][c][j][2]);
-                *reinterpret_cast<float2*>(&sm_o[warp][8 * n + 2 * t + 1][d]) = make_float2(o[n][c][j][1], o[n][c][j][3]);
+            for (int i = 0; i < 4; ++i) {
+                // row g of a tile is dim g, row g + 8 dim g + 8 (Q8_0: 2g and 2g + 1)
+                const int d = 16 * j + (Q8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+                p[(i & 1) * OD + d] = o[n][j][i] * (Q8 ? 1.f / __low2float(v_mul) : 1.f);
             }
     }
     __syncthreads();
@@ -588,13 +693,13 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         for (int w = 0; w < kWarps; ++w) {
             const float f = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - mm);
             ll += sm_l[w][h] == 0.f ? 0.f : f * sm_l[w][h];
-            oo = fmaf(f, sm_o[w][h][d], oo);
+            oo = fmaf(f, sm_o[(w * 8 * NT + h) * OD + d], oo);
         }
         const int64_t bh = b * a.Hq + h0 + h;
         if (rg.splits == 1) {
             // all scores -inf: 0 / 0, as the formula gives
             store_act(a.out, a.dtype, bh * D + d, oo / ll);
-            if (a.lse && d == 0) a.lse[bh] = (mm - kBias) * kLn2 + logf(ll);
+            if (a.lse && d == 0) a.lse[bh] = mm * kLn2 + logf(ll);
         } else {
             ws_o(a, splits, bh, split)[d] = oo;
             if (d == 0) *ws_ml(a, splits, bh, split) = make_float2(mm, ll);
@@ -602,11 +707,11 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     }
 }
 
-template <int FMT, int D, bool HI, int NT, int SUB, int MINB>
+template <int FMT, int D, bool HI, int NT, int STAGES, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB)
     k_attn(const __grid_constant__ AttnArgs a, int splits, int chunk, int head_chunks) {
     grid_dep_launch();
-    attn_block<FMT, D, HI, NT, SUB>(a, splits, chunk, head_chunks);
+    attn_block<FMT, D, HI, NT, STAGES>(a, splits, chunk, head_chunks);
 }
 
 // One format's launcher (a translation unit each): the kernel for the head dim,

@@ -12,8 +12,7 @@ constexpr int kJoinThreads = 256;
 // o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s of one head of one sequence
 // per block, in split order within each of the block's lanes' groups
 // (deterministic). A group of D / 4 threads adds every GROUPS-th split.
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a, int splits, int chunk,
-                                                            float bias) {
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a, int splits, int chunk) {
     grid_dep_wait();
     const int64_t bh = blockIdx.x;
     const Range r = range_of(a, bh / a.Hq, chunk);
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
             ll += sl[i];
         }
         store_act(a.out, a.dtype, bh * D + d, o / ll);
-        if (a.lse && d == 0) a.lse[bh] = (m - bias) * kLn2 + logf(ll);
+        if (a.lse && d == 0) a.lse[bh] = m * kLn2 + logf(ll);
     }
 }
 
@@ -74,11 +73,14 @@ AttnPlan attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int ma
     const int64_t step = 64;                           // four warps of 16 keys
     const int64_t steps = (keys + step - 1) / step;
     const int64_t slots = static_cast<int64_t>(sms) * 3;
-    // The split count with the least cost, in steps: waves of blocks times the
-    // steps of a block and its fixed part (query, join)
+    // The split count with the least cost in steps: waves of blocks, times the
+    // steps of a block and its fixed part (query, join). Only counts that fill
+    // a whole number of waves can be best.
     int64_t best = 1;
     double best_cost = 1e300;
-    for (int64_t s = 1; s <= std::min<int64_t>(steps, 512); ++s) {
+    for (int64_t w = 0; w <= 6; ++w) {
+        const int64_t s = w == 0 ? 1 : std::min<int64_t>({w * slots / items, steps, 512});
+        if (s < 1) continue;
         const int64_t per = (steps + s - 1) / s;
         const int64_t n = (steps + per - 1) / per;
         const double waves = static_cast<double>((items * n + slots - 1) / slots);
@@ -116,7 +118,7 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn::k_attn_join, a, p.splits, p.chunk, a.c.fmt == QMM_KV_F16 ? 14.f : 0.f);
+    e = cudaLaunchKernelEx(&cfg, attn::k_attn_join, a, p.splits, p.chunk);
     count_launch(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -295,51 +295,82 @@ def qmoe_ffn(kind, W_gu, gu_stride: int, W_down, down_stride: int, n_experts: in
     return Y
 
 
+def _torch():
+    """What the serving operators' bindings use of torch, looked up once: a call
+    on a decode step costs about as much on the host as on the GPU."""
+    global _T
+    if _T is None:
+        import torch
+        dtypes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(device):
+                return torch.cuda.current_stream(device).cuda_stream
+        _T = (torch, dtypes, raw, torch.cuda.current_device, torch.int32, torch.int64)
+    return _T
+
+
+_T = None
+
+
+def _device(X, what: str) -> int:
+    """Index of X's GPU, which must be the current one (kernels launch there)."""
+    dev = X.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dev != _torch()[3]():
+        raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
 def _act(X, what: str) -> int:
     """Element type of an f32 / f16 / bf16 tensor."""
-    import torch
-    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(X.dtype)
+    dt = _torch()[1].get(X.dtype)
     if dt is None:
         raise TypeError(f"{what} must be float32, float16 or bfloat16, got {X.dtype}")
     return dt
 
 
 def _rows(X, what: str):
-    """(elements reachable, token stride, head stride) of a (T, H, D) tensor
-    whose last dimension is contiguous."""
-    if X.dim() != 3:
-        raise ValueError(f"{what} must have three dimensions (tokens, heads, dim), got {tuple(X.shape)}")
-    (T, H, D), (ts, hs, ds) = X.shape, X.stride()
+    """(T, H, D, elements reachable, token stride, head stride) of a (T, H, D)
+    tensor whose last dimension is contiguous."""
+    shape, stride = X.shape, X.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have three dimensions (tokens, heads, dim), got {tuple(shape)}")
+    T, H, D = shape
+    ts, hs, ds = stride
     if ds != 1 and D > 1:
         raise ValueError(f"{what}'s last dimension must be contiguous")
-    return (T - 1) * ts + (H - 1) * hs + D if T and H and D else 0, ts, hs
+    return T, H, D, (T - 1) * ts + (H - 1) * hs + D if T and H and D else 0, ts, hs
 
 
-def _want(X, dtype, n, what: str, dev):
-    """A contiguous `dtype` tensor of `n` elements on `dev`."""
-    if X.dtype != dtype or not X.is_contiguous() or (n is not None and X.numel() != n):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n is not None else ""))
-    _on(X, dev, what)
+def _want(X, dtype, n, what: str, dev: int) -> int:
+    """Address of a contiguous `dtype` tensor of `n` elements on GPU `dev`."""
+    if X.dtype is not dtype or not X.is_contiguous() or (n >= 0 and X.numel() != n):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n >= 0 else ""))
+    if X.get_device() != dev:
+        raise ValueError(f"{what} is on {X.device}, not on cuda:{dev}")
+    return X.data_ptr()
 
 
-def _on(X, dev, what: str):
-    if X.device != dev:
-        raise ValueError(f"{what} is on {X.device}, not on {dev}")
+def _on(X, dev: int, what: str):
+    if X.get_device() != dev:
+        raise ValueError(f"{what} is on {X.device}, not on cuda:{dev}")
 
 
-def _pages(k_cache, v_cache, dev):
+def _pages(k_cache, v_cache, dev: int):
     """(pages, page stride, bytes) of a cache given as two (pages, bytes) uint8 tensors."""
-    import torch
-    for c, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if c.dtype != torch.uint8 or c.dim() != 2 or c.stride(1) != 1:
-            raise ValueError(f"{what} must be a (pages, bytes per page) uint8 tensor with contiguous pages")
-        _on(c, dev, what)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    n, nbytes = k_cache.shape
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 2 or stride[1] != 1 or k_cache.element_size() != 1:
+        raise ValueError("k_cache must be a (pages, bytes per page) uint8 tensor with contiguous pages")
+    if v_cache.shape != shape or v_cache.stride() != stride or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("v_cache must have k_cache's shape, strides and type")
+    _on(k_cache, dev, "k_cache")
+    _on(v_cache, dev, "v_cache")
+    n, nbytes = shape
     # one page alone has no stride to speak of
-    stride = k_cache.stride(0) if n > 1 else nbytes
-    return n, stride, (n - 1) * stride + nbytes if n else 0
+    ps = stride[0] if n > 1 else nbytes
+    return n, ps, (n - 1) * ps + nbytes if n else 0
 
 
 def _fmt(fmt) -> int:
@@ -380,23 +411,22 @@ def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=No
     each head in pairs (i, i + rot/2) ("half") or (2i, 2i + 1)
     ("interleaved"). positions: int32 (T,); turns: qrope_turns. X may be a
     view; out=X rotates in place. Returns out (X's type)."""
-    import torch
+    torch, _, raw, _, i32, i64 = _T or _torch()
     dt = _act(X, "X")
-    n, ts, hs = _rows(X, "X")
-    T, H, D = X.shape
-    dev = X.device
-    _want(positions, torch.int32, T, "positions", dev)
-    _want(turns, torch.int64, None, "turns", dev)
+    T, H, D, n, ts, hs = _rows(X, "X")
+    dev = _device(X, "X")
+    pos = _want(positions, i32, T, "positions", dev)
+    tur = _want(turns, i64, -1, "turns", dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=X.dtype, device=dev)
+        out = X.new_empty((T, H, D))
         on, ots, ohs = T * H * D, H * D, D
     else:
         if out.shape != X.shape or out.dtype != X.dtype:
             raise ValueError("out must have X's shape and type")
         _on(out, dev, "out")
-        on, ots, ohs = _rows(out, "out")
-    _check(_lib().qrope(X.data_ptr(), dt, n, ts, hs, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
-                        ROPE_LAYOUTS[layout], mscale, out.data_ptr(), on, ots, ohs, T, H, D, _stream(stream)), "qrope")
+        _, _, _, on, ots, ohs = _rows(out, "out")
+    _check(_lib().qrope(X.data_ptr(), dt, n, ts, hs, pos, tur, 2 * turns.numel(), ROPE_LAYOUTS[layout], mscale,
+                        out.data_ptr(), on, ots, ohs, T, H, D, raw(dev) if stream is None else stream), "qrope")
     return out
 
 
@@ -406,50 +436,51 @@ def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None
     (T,); -1 skips a token) of a paged cache of format "f16", "bf16" or "q8_0",
     rotating K first when positions and turns are given. k_cache, v_cache:
     (pages, bytes per page) uint8 tensors (qkv_cache)."""
-    import torch
+    torch, _, raw, _, i32, i64 = _T or _torch()
     dt = _act(K, "K")
     if V.dtype != K.dtype or V.shape != K.shape:
         raise ValueError("V must have K's shape and type")
-    kn, kts, khs = _rows(K, "K")
-    vn, vts, vhs = _rows(V, "V")
-    T, H, D = K.shape
-    dev = K.device
+    T, H, D, kn, kts, khs = _rows(K, "K")
+    _, _, _, vn, vts, vhs = _rows(V, "V")
+    dev = _device(K, "K")
     _on(V, dev, "V")
-    _want(slots, torch.int64, T, "slots", dev)
-    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
+    slot = _want(slots, i64, T, "slots", dev)
+    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
     if (positions is None) != (turns is None):
         raise ValueError("positions and turns go together")
     pos = tur = rot = 0
     if positions is not None:
-        _want(positions, torch.int32, T, "positions", dev)
-        _want(turns, torch.int64, None, "turns", dev)
-        pos, tur, rot = positions.data_ptr(), turns.data_ptr(), 2 * turns.numel()
-    _check(_lib().qkv_store(_fmt(fmt), K.data_ptr(), kn, kts, khs, V.data_ptr(), vn, vts, vhs, dt, slots.data_ptr(),
-                            pos, tur, rot, ROPE_LAYOUTS[layout], mscale, k_cache.data_ptr(), v_cache.data_ptr(), nbytes,
-                            n_pages, stride, page_size, T, H, D, _stream(stream)), "qkv_store")
+        pos = _want(positions, i32, T, "positions", dev)
+        tur = _want(turns, i64, -1, "turns", dev)
+        rot = 2 * turns.numel()
+    _check(_lib().qkv_store(_fmt(fmt), K.data_ptr(), kn, kts, khs, V.data_ptr(), vn, vts, vhs, dt, slot, pos, tur, rot,
+                            ROPE_LAYOUTS[layout], mscale, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps,
+                            page_size, T, H, D, raw(dev) if stream is None else stream), "qkv_store")
 
 
 def qkv_load(fmt, slots, k_cache, v_cache, page_size: int, n_kv_heads: int, head_dim: int, dtype=None, stream=None):
     """The keys and values in `slots` (int64 (T,); -1 gives zeros) as two (T,
     n_kv_heads, head_dim) tensors of `dtype` (float32 by default)."""
-    import torch
-    dev = k_cache.device
+    torch, dtypes, raw, _, _, i64 = _T or _torch()
+    dt = F32 if dtype is None else dtypes.get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    dev = _device(k_cache, "k_cache")
     T = slots.numel()
-    _want(slots, torch.int64, T, "slots", dev)
-    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
-    K = torch.empty((T, n_kv_heads, head_dim), dtype=dtype or torch.float32, device=dev)
-    V = torch.empty_like(K)
-    _check(_lib().qkv_load(_fmt(fmt), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, stride,
-                           page_size, K.data_ptr(), V.data_ptr(), _act(K, "K"), K.numel(), T, n_kv_heads, head_dim,
-                           _stream(stream)), "qkv_load")
+    slot = _want(slots, i64, T, "slots", dev)
+    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
+    # one allocation for both
+    KV = k_cache.new_empty((2, T, n_kv_heads, head_dim), dtype=dtype or torch.float32)
+    K, V = KV[0], KV[1]
+    _check(_lib().qkv_load(_fmt(fmt), slot, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps, page_size,
+                           K.data_ptr(), V.data_ptr(), dt, T * n_kv_heads * head_dim, T, n_kv_heads, head_dim,
+                           raw(dev) if stream is None else stream), "qkv_load")
     return K, V
 
 
 def qattn_decode_workspace_bytes(fmt, dtype, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
                                  window: int = 0) -> int:
-    import torch
-    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dtype]
-    return _lib().qattn_decode_workspace_bytes(_fmt(fmt), dt, batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
+    return _lib().qattn_decode_workspace_bytes(_fmt(fmt), _torch()[1][dtype], batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
 
 
 def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int, n_kv_heads: int,
@@ -463,36 +494,40 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
     uint8 tensor of qattn_decode_workspace_bytes(...)), allocated here with
     torch if None."""
-    import torch
+    torch, _, raw, _, i32, _ = _T or _torch()
     dt = _act(q, "q")
-    qn, qbs, qhs = _rows(q, "q")
-    B, H, D = q.shape
-    dev = q.device
-    n_pages, stride, nbytes = _pages(k_cache, v_cache, dev)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    B, H, D, qn, qbs, qhs = _rows(q, "q")
+    dev = _device(q, "q")
+    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
+    tshape = block_table.shape
+    if block_table.dtype is not i32 or len(tshape) != 2 or tshape[0] != B or \
+            (tshape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be an int32 tensor (sequences, pages) with contiguous rows")
     _on(block_table, dev, "block_table")
-    _want(seq_lens, torch.int32, B, "seq_lens", dev)
-    width, tstride = block_table.shape[1], block_table.stride(0)
+    lens = _want(seq_lens, i32, B, "seq_lens", dev)
+    width, ts = tshape[1], block_table.stride(0)
     if max_len is None:
         max_len = width * page_size
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+        out = q.new_empty((B, H, D))
+        optr = out.data_ptr()
     else:
-        _want(out, q.dtype, B * H * D, "out", dev)
-    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if return_lse else None
+        optr = _want(out, q.dtype, B * H * D, "out", dev)
+    lse = q.new_empty((B, H), dtype=torch.float32) if return_lse else None
     L, f = _lib(), _fmt(fmt)
+    wptr = wn = 0
     if workspace is None:
-        need = L.qattn_decode_workspace_bytes(f, dt, B, H, n_kv_heads, D, max_len, window)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        wn = L.qattn_decode_workspace_bytes(f, dt, B, H, n_kv_heads, D, max_len, window)
+        if wn:
+            workspace = k_cache.new_empty(wn)
+            wptr = workspace.data_ptr()
     else:
         _on(workspace, dev, "workspace")
-    _check(L.qattn_decode(f, q.data_ptr(), dt, qn, qbs, qhs, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages,
-                          stride, page_size, block_table.data_ptr(), (B - 1) * tstride + width if B else 0, tstride,
-                          width, seq_lens.data_ptr(), max_len, B, H, n_kv_heads, D,
-                          D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), out.numel(),
-                          _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)),
+        wptr, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(L.qattn_decode(f, q.data_ptr(), dt, qn, qbs, qhs, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps,
+                          page_size, block_table.data_ptr(), (B - 1) * ts + width if B else 0, ts, width, lens, max_len,
+                          B, H, n_kv_heads, D, D ** -0.5 if scale is None else scale, window, softcap, optr, B * H * D,
+                          lse.data_ptr() if return_lse else 0, wptr, wn, raw(dev) if stream is None else stream),
            "qattn_decode")
     return (out, lse) if return_lse else out
 
