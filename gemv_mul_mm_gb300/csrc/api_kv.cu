@@ -214,7 +214,9 @@ size_t qattn_decode_workspace_bytes(int fmt, int dtype, int64_t B, int n_q_heads
         return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    return attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev)).ws_bytes;
+    AttnPlan p;
+    if (attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev), &p) != cudaSuccess) return 0;
+    return p.ws_bytes;
 }
 
 int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs, const void* k_cache,
@@ -248,7 +250,9 @@ int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs
         return QMM_ERR_OUTPUT_TOO_SMALL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
-    const AttnPlan p = attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev));
+    AttnPlan p;
+    if (attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev), &p) != cudaSuccess)
+        return QMM_ERR_CUDA;
     if (p.ws_bytes) {
         if (!workspace) return QMM_ERR_NULL_POINTER;
         if (workspace_bytes < p.ws_bytes) return QMM_ERR_WORKSPACE_TOO_SMALL;

@@ -71,18 +71,18 @@ __host__ __device__ constexpr bool needs_hi(int fmt, int dtype) {
     return fmt == QMM_KV_BF16 ? dtype != QMM_BF16 : dtype != QMM_F16;
 }
 
-// d = a b + c
+// d += a b
 template <bool BF>
 __device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                    unsigned b1, float c0, float c1, float c2, float c3) {
+                                    unsigned b1) {
     if constexpr (BF)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ unsigned transpose8x8(unsigned x) {
@@ -175,8 +175,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 bytes global -> shared; `bytes` 0 writes zeros and reads nothing.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+// 16 bytes global -> shared.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same with bytes 16; bytes 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const uint8_t* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -204,9 +208,10 @@ template <int FMT, int D, int NT, int STAGES> struct Layout {
     static constexpr int C = D / 32;
     static constexpr int ROW = Q8 ? D : 2 * D;              // bytes of a row's codes or values
     static constexpr int RS = ROW + 16;                     // row pitch
-    static constexpr int V0 = 16 * RS;                      // K rows, V rows, K scales, V scales
-    static constexpr int S0 = 32 * RS;
-    static constexpr int STAGE = S0 + (Q8 ? 64 * C : 0);
+    static constexpr int KT = 16;                           // keys per stage
+    static constexpr int V0 = KT * RS;                      // K rows, V rows, K scales, V scales
+    static constexpr int S0 = 2 * KT * RS, SV = 2 * C * KT; // (bytes of K's scales)
+    static constexpr int STAGE = S0 + (Q8 ? 2 * SV : 0);
     static constexpr int RING = STAGES * STAGE;             // of one warp
     static constexpr int OD = D + 4;
     static constexpr int JOIN = kWarps * 8 * NT * OD * 4;
@@ -220,7 +225,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     constexpr bool BF = FMT == QMM_KV_BF16;           // operand type of both products: bf16, else f16
     constexpr int NQ = Terms<FMT, HI>::q, NP = Terms<FMT, HI>::p;
     constexpr int C = D / 32;                         // 32-dim blocks of a row
-    constexpr int KT = 16;                            // keys per tile
+    constexpr int KT = Lay::KT;                       // keys per tile
     constexpr int ROW = Lay::ROW, RS = Lay::RS;
     constexpr int MT = D / 16;                        // 16-dim tiles of the output
 
@@ -242,6 +247,14 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     const int h0 = kh * group + hc * 8 * NT;          // first query head
     const int nh = min(8 * NT, group - hc * 8 * NT);
 
+    // the query rows, read before anything waits for the lengths
+    constexpr int QN = 8 * NT * D / kThreads;
+    float qv[QN];
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+        const int j = i * kThreads + threadIdx.x, h = j / D, d = j % D;
+        qv[i] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
+    }
     const Range rg = range_of(a, b, chunk);
     if (rg.splits == 0) {                             // nothing to attend to (or a bad length)
         if (split == 0) {
@@ -263,53 +276,67 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     const int64_t v_minus_k = a.c.v - a.c.k;
     bool bad = false;
 
-    // Page ids of the two 8-key groups of a tile: a group lies in one page
-    // (pages hold 8 or more keys, tiles start at multiples of 16). Groups
-    // outside the range name a page inside it, so that every address is that
-    // of a page the sequence owns.
+    // Pages of a tile: one for its 16 keys, or with pages of 8 one for each half
+    // (tiles start at multiples of 16). Halves outside the range name a page
+    // inside it, so that every address is that of a page the sequence owns.
+    const bool small_pages = shift < 4;
+    auto page_id = [&](int key) { return table[max(page_lo, min(key >> shift, page_hi))]; };
     auto page_ids = [&](int base, int (&id)[2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) id[i] = table[max(page_lo, min((base + 8 * i) >> shift, page_hi))];
+        id[0] = page_id(base);
+        if (small_pages) id[1] = page_id(base + 8);
+    };
+    auto page_at = [&](int id) {                      // this head's K rows in a page
+        if (static_cast<uint64_t>(static_cast<unsigned>(id)) >= static_cast<uint64_t>(a.c.n_pages)) {
+            bad = true;
+            id = 0;
+        }
+        return kbase + static_cast<uint64_t>(static_cast<unsigned>(id)) * static_cast<uint64_t>(a.c.page_stride);
     };
     const uint32_t ring = smem_addr(smem) + warp * Lay::RING;
-    // Copies one tile to a stage. The rows of an 8-key group are contiguous in
+    constexpr int CPR = ROW / 16;                     // 16-byte pieces of a row
+    // this lane's first piece of a tile
+    const uint32_t dst_lane = lane / CPR * RS + lane % CPR * 16;
+    // Copies one tile to a stage. Its rows (of either half) are contiguous in
     // the cache. Rows outside the range become zeros (what the cache holds
     // there must not reach the products: 0 * NaN).
     auto load_tile = [&](int base, const int (&id)[2], uint32_t stage) {
-        int64_t off[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool ok = static_cast<unsigned>(id[i]) < static_cast<uint64_t>(a.c.n_pages);
-            bad |= !ok;
-            off[i] = ok ? id[i] * a.c.page_stride : 0;
-        }
+        const uint8_t* page[2];
+        page[0] = page_at(id[0]);
+        page[1] = small_pages ? page_at(id[1]) : page[0];
         const int row0 = base & page_mask, row1 = (base + 8) & page_mask;
-        constexpr int CPR = ROW / 16;                 // 16-byte pieces of a row
-        const bool partial = base < rg.lo || base + KT > end;
         if constexpr (Q8) {
-            if (lane < 4 * C) {                       // scales: C pieces per group, of K then of V
-                const int grp = lane / C % 2, col = lane % C;
-                const uint8_t* p = kbase + (lane < 2 * C ? 0 : v_minus_k) + (grp ? off[1] : off[0]) + (D << shift) +
-                                   (grp ? row1 : row0) * (2 * C) + col * 16;
-                copy16(stage + Lay::S0 + lane * 16, p, 16);
+            if (lane < 4 * C) {                       // scales: C pieces per half, of K then of V
+                const int col = lane % C;
+                const uint8_t* p = (lane / C & 1 ? page[1] + row1 * (2 * C) : page[0] + row0 * (2 * C)) + (D << shift) + col * 16;
+                const uint32_t dst = stage + Lay::S0 + lane % (2 * C) * 16;
+                copy16(lane < 2 * C ? dst : dst + Lay::SV, lane < 2 * C ? p : p + v_minus_k);
             }
         }
-        const uint8_t* pk[2] = {kbase + off[0] + row0 * ROW + lane * 16, kbase + off[1] + row1 * ROW + lane * 16 - 8 * ROW};
-        const uint8_t* pv[2] = {pk[0] + v_minus_k, pk[1] + v_minus_k};
-        const uint32_t dst0 = stage + lane / CPR * RS + lane % CPR * 16;
+        const uint8_t* pk[2] = {page[0] + row0 * ROW + lane * 16, page[1] + (row1 - 8) * ROW + lane * 16};
+        const bool partial = base < rg.lo || base + KT > end;
+        auto copies = [&](auto some, auto two) {      // some rows are zeros; two pages
 #pragma unroll
-        for (int i = 0; i < ROW / 32; ++i) {
-            const int q = 32 * i + lane;              // this lane's piece of the tile's rows
-            const int row = q / CPR;
-            const int grp = (ROW / 2) % 32 == 0 ? 32 * i / (ROW / 2) : row / 8;
-            const uint32_t dst = 32 % CPR == 0 ? dst0 + i * (32 / CPR) * RS : CPR == 32 ? dst0 + i * RS : stage + row * RS + q % CPR * 16;
-            int n = 16;
-            if (partial) n = base + row >= rg.lo && base + row < end ? 16 : 0;
-            copy16(dst, pk[grp] + i * 512, n);
-            copy16(dst + Lay::V0, pv[grp] + i * 512, n);
-        }
+            for (int i = 0; i < ROW / 32; ++i) {
+                const int q = 32 * i + lane, row = q / CPR;
+                const int half = !decltype(two)::value ? 0 : (ROW / 2) % 32 == 0 ? 32 * i / (ROW / 2) : row / 8;
+                const uint32_t dst = 32 % CPR == 0 ? stage + dst_lane + i * (32 / CPR) * RS
+                                     : CPR == 32   ? stage + dst_lane + i * RS
+                                                   : stage + row * RS + q % CPR * 16;
+                const uint8_t* src = pk[half] + i * 512;
+                if constexpr (decltype(some)::value) {
+                    const int n = base + row >= rg.lo && base + row < end ? 16 : 0;
+                    copy16_or_zero(dst, src, n);
+                    copy16_or_zero(dst + Lay::V0, src + v_minus_k, n);
+                } else {
+                    copy16(dst, src);
+                    copy16(dst + Lay::V0, src + v_minus_k);
+                }
+            }
+        };
+        if (partial) copies(std::true_type{}, std::true_type{});
+        else if (small_pages) copies(std::false_type{}, std::true_type{});
+        else copies(std::false_type{}, std::false_type{});
     };
-
     constexpr int stride = kWarps * KT;
     int base = begin + warp * KT;
     int id[2];                                        // pages of the next tile to load
@@ -326,9 +353,10 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     }
 
     // ---- the query fragments: B operand, column g = head
-    for (int i = threadIdx.x; i < 8 * NT * D; i += kThreads) {
-        const int h = i / D, d = i % D;
-        sm_q[h][d] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+        const int j = i * kThreads + threadIdx.x;
+        sm_q[j / D][j % D] = qv[i];
     }
     __syncthreads();
     constexpr bool NORM = HI && !BF;                  // f16 terms of fp32 / bf16 rows
@@ -346,19 +374,23 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         __syncthreads();
     }
     if constexpr (Q8) {
-        // -128 2^-24 times the sum of the q terms of each 32-dim block
-        for (int i = threadIdx.x; i < 8 * NT * C; i += kThreads) {
-            const int h = i / C, c = i % C;
+        // -128 2^-24 times the sum of the q terms of each 32-dim block, four lanes
+        // to a block
+        for (int i = threadIdx.x; i < 8 * NT * C * 4; i += kThreads) {
+            const int h = i / (4 * C), c = i / 4 % C;
             const float f = NORM ? sm_scale[h] : 1.f;
             float sum = 0.f;
-            for (int d = 0; d < 32; ++d) {
-                const float x = sm_q[h][32 * c + d] * f;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                const float x = sm_q[h][32 * c + 4 * d + i % 4] * f;
                 float rest = x, none = 0.f;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) take16<false>(rest, none);
                 sum += x - rest;
             }
-            sm_qsum[h][c] = sum * -7.62939453125e-06f;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (i % 4 == 0) sm_qsum[h][c] = sum * -7.62939453125e-06f;
         }
         __syncthreads();
     }
@@ -413,26 +445,27 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     uint32_t stage = ring, fill = ring + (STAGES - 1) * Lay::STAGE;
     const uint32_t ring_end = ring + Lay::RING, smem_base = smem_addr(smem);
 
-    // One tile. `slow`: some keys are masked, or scores are capped.
+    // One tile. SLOW: some keys are masked, or scores are capped.
     auto tile = [&](auto slow_tag) {
         constexpr bool SLOW = decltype(slow_tag)::value;
+        [[maybe_unused]] const uint8_t* scales = smem + (stage - smem_base) + Lay::S0;
         // ---- S^T = K Q^T
         float sx[NT][4];
         if constexpr (Q8) {
             constexpr int B = C % 4 == 0 ? 8 : C % 2 == 0 ? 4 : 2;
             using SV = typename VecOf<B>::type;
-            __half kscale[2][C];                      // of keys g, g + 8
+            __half kscale[2][C];                  // of keys g, g + 8
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 2 * C / B; ++k) {
-                    const SV x = reinterpret_cast<const SV*>(smem + (stage - smem_base) + Lay::S0 + (g + 8 * i) * (2 * C))[k];
+                    const SV x = reinterpret_cast<const SV*>(scales + (g + 8 * i) * (2 * C))[k];
 #pragma unroll
                     for (int j = 0; j < B / 2; ++j) kscale[i][k * (B / 2) + j] = reinterpret_cast<const __half*>(&x)[j];
                 }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                unsigned w[4];                        // (key g, g + 8) of dims 0 .. 15, then of 16 .. 31
+                unsigned w[4];                    // (key g, g + 8) of dims 0 .. 15, then of 16 .. 31
                 ldsm4(w, stage + k_lane + 32 * c);
                 unsigned x[2][4];
 #pragma unroll
@@ -447,8 +480,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int q = 0; q < NQ; ++q)
-                            mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], qf[n][q][2 * c + j][0], qf[n][q][2 * c + j][1],
-                                    acc[0], acc[1], acc[2], acc[3]);
+                            mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], qf[n][q][2 * c + j][0], qf[n][q][2 * c + j][1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float d = __half2float(kscale[i >> 1][c]);
@@ -458,17 +490,17 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             }
         } else {
 #pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sx[n][i] = 0.f;
+#pragma unroll
             for (int j = 0; j < MT; ++j) {
                 unsigned x[4];
                 ldsm4(x, stage + k_lane + 32 * j);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        const bool first = j == 0 && q == 0;
-                        mma<BF>(sx[n], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1], first ? 0.f : sx[n][0],
-                                first ? 0.f : sx[n][1], first ? 0.f : sx[n][2], first ? 0.f : sx[n][3]);
-                    }
+                    for (int q = 0; q < NQ; ++q) mma<BF>(sx[n], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1]);
             }
         }
 
@@ -497,12 +529,12 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 y[n][i] = rel(n, i);
                 grew |= y[n][i] > kTop;
             }
-        [[maybe_unused]] unsigned vd[2][Q8 ? C : 1];                   // V scales of keys (2t, 2t + 1) and (2t + 8, 2t + 9)
+        [[maybe_unused]] unsigned vd[2][Q8 ? C : 1];   // V scales of keys (2t, 2t + 1) and (2t + 8, 2t + 9)
         __half2 v_top = v_lim;
         if constexpr (Q8) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint8_t* p = smem + (stage - smem_base) + Lay::S0 + 32 * C + (2 * t + 8 * i) * (2 * C);
+                const uint8_t* p = scales + Lay::SV + (2 * t + 8 * i) * (2 * C);
                 if constexpr (C % 2 == 0) {
                     constexpr int B = C % 4 == 0 ? 8 : 4;
                     using SV = typename VecOf<B>::type;
@@ -521,9 +553,9 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 #pragma unroll
                     for (int c = 0; c < C; ++c)
                         vd[i][c] = reinterpret_cast<const unsigned short*>(p)[c] |
-                                   static_cast<unsigned>(reinterpret_cast<const unsigned short*>(p + 2 * C)[c]) << 16;
+                                      static_cast<unsigned>(reinterpret_cast<const unsigned short*>(p + 2 * C)[c]) << 16;
                 }
-                if constexpr (SLOW) {                 // rows outside the range are zeros, their scales are not
+                if constexpr (SLOW) {             // rows outside the range are zeros, their scales are not
                     const int key = base + 8 * i + 2 * t;
                     const unsigned keep = (key >= rg.lo && key < end ? 0xffffu : 0u) |
                                           (key + 1 >= rg.lo && key + 1 < end ? 0xffff0000u : 0u);
@@ -573,65 +605,96 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 for (int i = 0; i < 4; ++i) y[n][i] = rel(n, i);
             }
         }
-        // ---- weights, as the B operand of the second product
-        unsigned pf[NT][NP][2];
+        // ---- weights, as the B operand of the second product: O^T += V^T P^T.
+        // A weight below 2^-32 of the largest has lost most of its bits to f16's
+        // subnormals. With activations whose type shows that (WIDE), a tile that
+        // has such weights takes them in bands of 2^24, each scaled up with O.
+        constexpr bool WIDE = HI && !BF;
+        constexpr float kLow = -18.f, kBand = 24.f;
+        int bands = 1;
+        if constexpr (WIDE) {
+            bool low = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[n][i] = ex2(y[n][i]);
-                l[n][i & 1] += y[n][i];
-            }
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                pf[n][q][0] = transpose8x8(take16<BF>(y[n][0], y[n][1]));
-                pf[n][q][1] = transpose8x8(take16<BF>(y[n][2], y[n][3]));
-            }
+                for (int i = 0; i < 4; ++i) low |= y[n][i] < kLow;
+            if (__any_sync(0xffffffffu, low)) bands = 4;
         }
-        // ---- O^T += V^T P^T
-        if constexpr (Q8) {
+#pragma unroll 1
+        for (int k = 0; k < bands; ++k) {
+            unsigned pf[NT][NP][2];
+            if (k) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                unsigned pd[NT][2][2];                // p times the block's scale
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const __half2 d = __hmul2(as_half2(vd[i][c]), v_mul);
+                    for (int j = 0; j < MT; ++j)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const __half2 hi = as_half2(pf[n][0][i]), t1 = __hmul2_rn(hi, d);
-                        pd[n][0][i] = as_u32(t1);
-                        pd[n][1][i] = as_u32(__hfma2(as_half2(pf[n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
-                    }
+                        for (int i = 0; i < 4; ++i) o[n][j][i] *= 16777216.f;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = ex2(WIDE ? y[n][i] + kBand * static_cast<float>(k) : y[n][i]);
+                    if (!WIDE || k == 0) l[n][i & 1] += x[i];
+                    if (WIDE && bands > 1 &&
+                        (y[n][i] < kLow - kBand * static_cast<float>(k) || (k && y[n][i] >= kLow - kBand * static_cast<float>(k - 1))))
+                        x[i] = 0.f;
                 }
-                unsigned w[4];
-                ldsm4_trans(w, stage + v_lane + 32 * c);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    unsigned f[4];
-                    codes_f16(w[2 * j], f[0], f[1]);
-                    codes_f16(w[2 * j + 1], f[2], f[3]);
+                for (int q = 0; q < NP; ++q) {
+                    pf[n][q][0] = transpose8x8(take16<BF>(x[0], x[1]));
+                    pf[n][q][1] = transpose8x8(take16<BF>(x[2], x[3]));
+                }
+            }
+            if constexpr (Q8) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                for (int c = 0; c < C; ++c) {
+                    unsigned pd[NT][2][2];            // p times the block's scale
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const __half2 d = __hmul2(as_half2(vd[i][c]), v_mul);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float(&d)[4] = o[n][2 * c + j];
-                            mma<BF>(d, f[0], f[1], f[2], f[3], pd[n][q][0], pd[n][q][1], d[0], d[1], d[2], d[3]);
+                            const __half2 hi = as_half2(pf[n][0][i]), t1 = __hmul2_rn(hi, d);
+                            pd[n][0][i] = as_u32(t1);
+                            pd[n][1][i] = as_u32(__hfma2(as_half2(pf[n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
                         }
+                    }
+                    unsigned w[4];
+                    ldsm4_trans(w, stage + v_lane + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        unsigned f[4];
+                        codes_f16(w[2 * j], f[0], f[1]);
+                        codes_f16(w[2 * j + 1], f[2], f[3]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma<BF>(o[n][2 * c + j], f[0], f[1], f[2], f[3], pd[n][q][0], pd[n][q][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    unsigned f[4];
+                    ldsm4_trans(f, stage + v_lane + 32 * j);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma<BF>(o[n][j], f[0], f[1], f[2], f[3], pf[n][q][0], pf[n][q][1]);
                 }
             }
-        } else {
+        }
+        if (WIDE && bands > 1) {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                unsigned f[4];
-                ldsm4_trans(f, stage + v_lane + 32 * j);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int q = 0; q < NP; ++q)
+                for (int j = 0; j < MT; ++j)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float(&d)[4] = o[n][j];
-                        mma<BF>(d, f[0], f[1], f[2], f[3], pf[n][q][0], pf[n][q][1], d[0], d[1], d[2], d[3]);
-                    }
-            }
+                    for (int i = 0; i < 4; ++i) o[n][j][i] *= 2.117582368135751e-22f;   // 2^-72
         }
     };
 
@@ -683,26 +746,47 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nh * D; i += kThreads) {
-        const int h = i / D, d = i % D;
-        float mm = -INFINITY;
+    // m and l of the block, and each warp's factor in sm_m
+    if (threadIdx.x < 8 * NT) {
+        const int h = threadIdx.x;
+        float mm = -INFINITY, ll = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][h]);
-        float ll = 0.f, oo = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - mm);
             ll += sm_l[w][h] == 0.f ? 0.f : f * sm_l[w][h];
-            oo = fmaf(f, sm_o[(w * 8 * NT + h) * OD + d], oo);
+            sm_m[w][h] = f;
+        }
+        sm_l[0][h] = ll;
+        if (h < nh) {
+            const int64_t bh = b * a.Hq + h0 + h;
+            if (rg.splits > 1) *ws_ml(a, splits, bh, split) = make_float2(mm, ll);
+            else if (a.lse) a.lse[bh] = mm * kLn2 + logf(ll);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = sm_m[w][h];
+            const float4 v = *reinterpret_cast<const float4*>(&sm_o[(w * 8 * NT + h) * OD + d]);
+            x.x = fmaf(f, v.x, x.x);
+            x.y = fmaf(f, v.y, x.y);
+            x.z = fmaf(f, v.z, x.z);
+            x.w = fmaf(f, v.w, x.w);
         }
         const int64_t bh = b * a.Hq + h0 + h;
-        if (rg.splits == 1) {
-            // all scores -inf: 0 / 0, as the formula gives
-            store_act(a.out, a.dtype, bh * D + d, oo / ll);
-            if (a.lse && d == 0) a.lse[bh] = mm * kLn2 + logf(ll);
+        if (rg.splits > 1) {
+            *reinterpret_cast<float4*>(ws_o(a, splits, bh, split) + d) = x;
         } else {
-            ws_o(a, splits, bh, split)[d] = oo;
-            if (d == 0) *ws_ml(a, splits, bh, split) = make_float2(mm, ll);
+            const float ll = sm_l[0][h];              // all scores -inf: 0 / 0, as the formula gives
+            store_act(a.out, a.dtype, bh * D + d, x.x / ll);
+            store_act(a.out, a.dtype, bh * D + d + 1, x.y / ll);
+            store_act(a.out, a.dtype, bh * D + d + 2, x.z / ll);
+            store_act(a.out, a.dtype, bh * D + d + 3, x.w / ll);
         }
     }
 }
@@ -711,12 +795,21 @@ template <int FMT, int D, bool HI, int NT, int STAGES, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB)
     k_attn(const __grid_constant__ AttnArgs a, int splits, int chunk, int head_chunks) {
     grid_dep_launch();
+    grid_dep_wait();
     attn_block<FMT, D, HI, NT, STAGES>(a, splits, chunk, head_chunks);
 }
 
 // One format's launcher (a translation unit each): the kernel for the head dim,
-// activation type and head tiles, on `blocks` blocks.
-template <int FMT> cudaError_t launch_fmt(const AttnArgs& a, const AttnPlan& p, int64_t blocks, int head_chunks, cudaStream_t s);
+// activation type and head tiles. With blocks 0 nothing is launched and
+// *resident gets the number of its blocks that fit an SM together.
+struct Launch {
+    AttnArgs a;
+    AttnPlan p;
+    int64_t blocks;
+    cudaStream_t stream;
+    int* resident;
+};
+template <int FMT> cudaError_t launch_fmt(const Launch& l, int D, bool hi, int tiles);
 
 }  // namespace attn
 }  // namespace qmm

@@ -9,52 +9,63 @@
 namespace qmm {
 namespace attn {
 
-// Shared memory beyond 48 KB has to be allowed once per kernel and device.
-template <int FMT, int D, bool HI, int NT, int STAGES, int MINB>
-cudaError_t go_with(const AttnArgs& a, const AttnPlan& p, int64_t blocks, int head_chunks, cudaStream_t s) {
-    constexpr int bytes = Layout<FMT, D, NT, STAGES>::BYTES;
+// Shared memory beyond 48 KB has to be allowed once per kernel and device; the
+// resident blocks are looked up at the same time.
+template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
+    constexpr int bytes = Layout<FMT, D, NT, STAGES>::BYTES, kDevices = 64;
     auto kernel = k_attn<FMT, D, HI, NT, STAGES, MINB>;
-    static std::atomic<uint64_t> allowed{0};
+    static std::atomic<int> fits[kDevices];
     int dev = 0;
-    cudaGetDevice(&dev);
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev < kDevices ? fits[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        if (e != cudaSuccess) return e;
-        allowed.fetch_or(bit, std::memory_order_relaxed);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, bytes);
+        if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+        if (dev < kDevices) fits[dev].store(n, std::memory_order_release);
     }
-    kernel<<<static_cast<unsigned>(blocks), kThreads, bytes, s>>>(a, p.splits, p.chunk, head_chunks);
-    count_launch(1);
-    return cudaGetLastError();
+    if (l.resident) *l.resident = n;
+    if (l.blocks == 0) return cudaSuccess;
+    return launch_chained(kernel, dim3(static_cast<unsigned>(l.blocks)), kThreads, bytes, l.stream, l.a, l.p.splits, l.p.chunk,
+                          l.p.head_chunks);
 }
 
-template <int FMT, int D, bool HI, int NT>
-cudaError_t go(const AttnArgs& a, const AttnPlan& p, int64_t blocks, int head_chunks, cudaStream_t s) {
-    return go_with<FMT, D, HI, NT, 3, 2>(a, p, blocks, head_chunks, s);
+// Depth of a warp's ring and blocks per SM, measured on 64 sequences of 8192
+// tokens (GB/s over the measured copy bandwidth). Three stages: two of 32 keys
+// reach 0.96 instead of 1.00 (f16) and 0.83 instead of 0.85 (q8_0). f16 and bf16
+// fill the memory system with two blocks per SM. q8_0 is bound by instructions
+// and needs the third, 0.85 against 0.78 (f16 activations), where its registers
+// allow one: at dim 256 and with 16 heads spills cost more than it brings (0.47
+// against 0.71, 0.43 against 0.52).
+template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
+    if constexpr (FMT == QMM_KV_Q8_0 && D <= 128 && NT == 1) return go_with<FMT, D, HI, NT, 3, 3>(l);
+    else return go_with<FMT, D, HI, NT, 3, 2>(l);
 }
 
-template <int FMT, int D>
-cudaError_t pick(const AttnArgs& a, const AttnPlan& p, int64_t blocks, int head_chunks, cudaStream_t s) {
-    const bool hi = needs_hi(FMT, a.dtype);
+template <int FMT, int D> cudaError_t pick(const Launch& l, bool hi, int tiles) {
     if constexpr (D <= 128) {
-        if (p.tiles == 2) return hi ? go<FMT, D, true, 2>(a, p, blocks, head_chunks, s) : go<FMT, D, false, 2>(a, p, blocks, head_chunks, s);
+        if (tiles == 2) return hi ? go<FMT, D, true, 2>(l) : go<FMT, D, false, 2>(l);
     }
-    return hi ? go<FMT, D, true, 1>(a, p, blocks, head_chunks, s) : go<FMT, D, false, 1>(a, p, blocks, head_chunks, s);
+    return hi ? go<FMT, D, true, 1>(l) : go<FMT, D, false, 1>(l);
 }
 
-template <int FMT>
-cudaError_t launch_fmt(const AttnArgs& a, const AttnPlan& p, int64_t blocks, int head_chunks, cudaStream_t s) {
-    switch (a.c.D) {
-    case 64: return pick<FMT, 64>(a, p, blocks, head_chunks, s);
-    case 96: return pick<FMT, 96>(a, p, blocks, head_chunks, s);
-    case 128: return pick<FMT, 128>(a, p, blocks, head_chunks, s);
-    default: return pick<FMT, 256>(a, p, blocks, head_chunks, s);
+template <int FMT> cudaError_t launch_fmt(const Launch& l, int D, bool hi, int tiles) {
+    switch (D) {
+    case 64: return pick<FMT, 64>(l, hi, tiles);
+    case 96: return pick<FMT, 96>(l, hi, tiles);
+    case 128: return pick<FMT, 128>(l, hi, tiles);
+    default: return pick<FMT, 256>(l, hi, tiles);
     }
 }
 
-template cudaError_t launch_fmt<QMM_ATTN_FMT>(const AttnArgs&, const AttnPlan&, int64_t, int, cudaStream_t);
+template cudaError_t launch_fmt<QMM_ATTN_FMT>(const Launch&, int, bool, int);
 
 }  // namespace attn
 }  // namespace qmm

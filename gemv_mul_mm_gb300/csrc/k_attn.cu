@@ -1,5 +1,6 @@
 // k_attn.cu -- qattn_decode: the split over the length, the launch and the join.
 #include <algorithm>
+#include <cmath>
 
 #include "attn_kernel.cuh"
 
@@ -13,6 +14,7 @@ constexpr int kJoinThreads = 256;
 // per block, in split order within each of the block's lanes' groups
 // (deterministic). A group of D / 4 threads adds every GROUPS-th split.
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a, int splits, int chunk) {
+    grid_dep_launch();
     grid_dep_wait();
     const int64_t bh = blockIdx.x;
     const Range r = range_of(a, bh / a.Hq, chunk);
@@ -56,71 +58,80 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     }
 }
 
+cudaError_t launch_one(const Launch& l, int fmt, int D) {
+    switch (fmt) {
+    case QMM_KV_F16: return launch_fmt<QMM_KV_F16>(l, D, l.p.hi, l.p.tiles);
+    case QMM_KV_BF16: return launch_fmt<QMM_KV_BF16>(l, D, l.p.hi, l.p.tiles);
+    default: return launch_fmt<QMM_KV_Q8_0>(l, D, l.p.hi, l.p.tiles);
+    }
+}
+
 }  // namespace
 }  // namespace attn
 
 bool attn_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 
-AttnPlan attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms) {
-    (void)fmt;
-    (void)dtype;
-    AttnPlan p;
+cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms, AttnPlan* p) {
     const int group = Hq / Hkv;
-    p.tiles = group > 8 && D <= 128 ? 2 : 1;
-    const int head_chunks = (group + 8 * p.tiles - 1) / (8 * p.tiles);
-    const int64_t items = B * Hkv * head_chunks;
-    const int64_t keys = std::max<int64_t>(1, window > 0 ? std::min<int64_t>(max_len, window + 15) : max_len);
-    const int64_t step = 64;                           // four warps of 16 keys
+    // Query heads per block: 16 halve the reads of a group of more than 8 (D = 256
+    // has no registers for them).
+    p->tiles = group > 8 && D <= 128 ? 2 : 1;
+    p->head_chunks = (group + 8 * p->tiles - 1) / (8 * p->tiles);
+    p->hi = attn::needs_hi(fmt, dtype);
+    int resident = 0;
+    attn::Launch l{};
+    l.p = *p;
+    l.resident = &resident;
+    const cudaError_t e = attn::launch_one(l, fmt, D);
+    if (e != cudaSuccess) return e;
+    const int64_t items = B * Hkv * p->head_chunks;
+    const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + 15) : max_len;
+    constexpr int64_t step = attn::kWarps * 16;
     const int64_t steps = (keys + step - 1) / step;
-    const int64_t slots = static_cast<int64_t>(sms) * 3;
-    // The split count with the least cost in steps: waves of blocks, times the
-    // steps of a block and its fixed part (query, join). Only counts that fill
-    // a whole number of waves can be best.
+    // The split count n with the least expected time, in steps of 64 keys (an SM
+    // takes about 0.6 us for one, however many blocks share it): the steps of
+    // the busiest SM, plus a block's fixed part (8: query, first loads, warps
+    // joined), of which further waves hide a part, plus the join. Candidates
+    // give every SM a whole number of blocks, or are powers of two. Lengths
+    // are known on the device only: a batch is taken to be anything between
+    // its bound and half of it. A smaller count wins within 5 %.
+    auto busiest = [&](double blocks, int64_t per) {
+        const double load = blocks / sms, waves = std::ceil(load / resident);
+        return (load <= resident ? std::ceil(load) : load + 0.5) * static_cast<double>(per) + 8.0 + 5.6 * (waves - 1);
+    };
+    auto cost = [&](int64_t n, int64_t per) {
+        const double full = busiest(static_cast<double>(items) * n, per);
+        const double half = B >= 4 ? busiest(0.5 * static_cast<double>(items) * n, per) : full;
+        return 0.5 * (full + half) + (n > 1 ? 4.0 + 0.02 * static_cast<double>(n) : 0.0);
+    };
     int64_t best = 1;
-    double best_cost = 1e300;
-    for (int64_t w = 0; w <= 6; ++w) {
-        const int64_t s = w == 0 ? 1 : std::min<int64_t>({w * slots / items, steps, 512});
-        if (s < 1) continue;
-        const int64_t per = (steps + s - 1) / s;
-        const int64_t n = (steps + per - 1) / per;
-        const double waves = static_cast<double>((items * n + slots - 1) / slots);
-        const double cost = waves * (per + 4.0) + (n > 1 ? 4.0 + 0.02 * n : 0.0);
-        if (cost < best_cost) {
-            best_cost = cost;
+    double best_cost = cost(1, steps);
+    const int64_t most = std::min<int64_t>(steps, 512);
+    for (int i = 0; i < 18; ++i) {
+        const int64_t s = i < 9 ? int64_t(2) << i : (i - 8) * sms / items;
+        if (s < 2 || s > most) continue;
+        const int64_t per = (steps + s - 1) / s, n = (steps + per - 1) / per;
+        const double c = cost(n, per);
+        if (n < best ? c <= best_cost * 1.05 : c < best_cost * 0.95) {
+            best_cost = c;
             best = n;
         }
     }
     const int64_t per = (steps + best - 1) / best;
-    p.chunk = static_cast<int>(per * step);
-    p.splits = static_cast<int>((keys + p.chunk - 1) / p.chunk);
-    p.ws_bytes = p.splits > 1 ? static_cast<size_t>(B) * Hq * p.splits * (D * 4 + 8) : 0;
-    return p;
+    p->chunk = static_cast<int>(per * step);
+    p->splits = static_cast<int>(best);
+    p->ws_bytes = best > 1 ? static_cast<size_t>(B) * Hq * best * (D * 4 + 8) : 0;
+    return cudaSuccess;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-    const int group = a.Hq / a.c.heads;
-    const int head_chunks = (group + 8 * p.tiles - 1) / (8 * p.tiles);
-    const int64_t blocks = a.B * a.c.heads * head_chunks * p.splits;
+    const int64_t blocks = a.B * a.c.heads * p.head_chunks * p.splits;
     if (blocks > 0x7fffffff || a.B * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e;
-    switch (a.c.fmt) {
-    case QMM_KV_F16: e = attn::launch_fmt<QMM_KV_F16>(a, p, blocks, head_chunks, s); break;
-    case QMM_KV_BF16: e = attn::launch_fmt<QMM_KV_BF16>(a, p, blocks, head_chunks, s); break;
-    default: e = attn::launch_fmt<QMM_KV_Q8_0>(a, p, blocks, head_chunks, s); break;
-    }
+    const attn::Launch l{a, p, blocks, s, nullptr};
+    const cudaError_t e = attn::launch_one(l, a.c.fmt, a.c.D);
     if (e != cudaSuccess || p.splits == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hq));
-    cfg.blockDim = dim3(attn::kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn::k_attn_join, a, p.splits, p.chunk);
-    count_launch(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_chained(attn::k_attn_join, dim3(static_cast<unsigned>(a.B * a.Hq)), attn::kJoinThreads, 0, s, a, p.splits,
+                          p.chunk);
 }
 
 }  // namespace qmm

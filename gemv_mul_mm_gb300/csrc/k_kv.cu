@@ -94,6 +94,8 @@ __device__ __forceinline__ void pair_of(int e, int rot, bool half, int& pair, in
 // it reads too, so no row is staged and no lane waits for another.
 template <typename T, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_kv_store(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
+    grid_dep_launch();
+    grid_dep_wait();
     const int64_t id0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     const bool active = id0 < threads;
     const int64_t id = active ? id0 : threads - 1;
@@ -167,6 +169,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_store(KvStoreArgs a, int64_t th
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_load(KvLoadArgs a, int64_t threads, int head_groups, int heads_per) {
+    grid_dep_launch();
+    grid_dep_wait();
     const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (id >= threads) return;
     const int vecs = a.c.D / N;
@@ -240,9 +244,7 @@ template <typename T> cudaError_t store(const KvStoreArgs& a, cudaStream_t s) {
     const bool al = reinterpret_cast<uintptr_t>(a.K) % 16 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0 &&
                     a.k_ts * S % 16 == 0 && a.k_hs * S % 16 == 0 && a.v_ts * S % 16 == 0 && a.v_hs * S % 16 == 0;
     auto go = [&](auto kernel) {
-        kernel<<<static_cast<unsigned>(g.blocks), kThreads, 0, s>>>(a, g.threads, g.groups, g.per);
-        count_launch(1);
-        return cudaGetLastError();
+        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks)), kThreads, 0, s, a, g.threads, g.groups, g.per);
     };
     switch (a.c.fmt) {
     case QMM_KV_F16: return al ? go(k_kv_store<T, QMM_KV_F16, true>) : go(k_kv_store<T, QMM_KV_F16, false>);
@@ -255,9 +257,7 @@ template <typename T> cudaError_t load(const KvLoadArgs& a, cudaStream_t s) {
     const Shape g = shape(a.T, a.c.heads, a.c.D);
     if (g.blocks > 0x7fffffff) return cudaErrorInvalidValue;
     auto go = [&](auto kernel) {
-        kernel<<<static_cast<unsigned>(g.blocks), kThreads, 0, s>>>(a, g.threads, g.groups, g.per);
-        count_launch(1);
-        return cudaGetLastError();
+        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks)), kThreads, 0, s, a, g.threads, g.groups, g.per);
     };
     switch (a.c.fmt) {
     case QMM_KV_F16: return go(k_kv_load<T, QMM_KV_F16>);

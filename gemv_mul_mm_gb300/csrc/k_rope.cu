@@ -20,6 +20,8 @@ constexpr int kThreads = 256;
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) k_rope(RopeArgs a, int64_t threads, int units, int rot_units, int head_groups,
                                                    int heads_per) {
+    grid_dep_launch();
+    grid_dep_wait();
     const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (id >= threads) return;
     const int u = static_cast<int>(id % units);
@@ -104,10 +106,8 @@ template <typename T, int N> cudaError_t run(const RopeArgs& a, cudaStream_t s) 
     const int64_t threads = a.T * units * groups;
     const int64_t blocks = (threads + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    k_rope<T, N><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, threads, units, rot_units, groups,
-                                                                    static_cast<int>(per));
-    count_launch(1);
-    return cudaGetLastError();
+    return launch_chained(k_rope<T, N>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, s, a, threads, units, rot_units, groups,
+                          static_cast<int>(per));
 }
 
 template <typename T> cudaError_t pick(const RopeArgs& a, cudaStream_t s) {

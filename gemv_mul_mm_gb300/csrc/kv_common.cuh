@@ -89,11 +89,34 @@ __device__ __forceinline__ void rope_cs(int32_t pos, uint64_t turns, float mscal
     s *= mscale;
 }
 
-// Waits for the kernel before this one on the stream (a kernel launched with
-// programmatic stream serialisation may start before it has ended), and lets
-// the next such kernel start.
+// Programmatic dependent launch: the operators here are launched so that the
+// next kernel on the stream may become resident while the one before it still
+// runs (it saves about a microsecond per launch in a chain of short kernels).
+// Each of their kernels lets its successor start at once and touches memory only
+// after the wait, which returns when its predecessor has completed.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // reported to the caller, not left for the next one
+        return e;
+    }
+    count_launch(1);
+    return cudaSuccess;
+}
 
 // k_rope.cu
 struct RopeArgs {
@@ -160,11 +183,13 @@ struct AttnArgs {
 struct AttnPlan {
     int splits;                    // most splits of one sequence
     int chunk;                     // keys per split
-    int tiles;                     // head tiles of 8 per block
+    int tiles;                     // 8-head tiles of a head group
+    int head_chunks;               // head groups per key-value head
+    bool hi;                       // the kernel with more terms
     size_t ws_bytes;
 };
 bool attn_dim_ok(int D);
-AttnPlan attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms);
+cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms, AttnPlan* p);
 cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
 }  // namespace qmm
