@@ -611,36 +611,64 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         // has such weights takes them in bands of 2^24, each scaled up with O.
         constexpr bool WIDE = HI && !BF;
         constexpr float kLow = -18.f, kBand = 24.f;
-        int bands = 1;
+        // band k of weights: [kLow - 24 k, kLow - 24 (k - 1)), the first without an
+        // upper end
+        auto in_band = [&](float x, int k) {
+            const float lo = kLow - kBand * static_cast<float>(k);
+            return x >= lo && (k == 0 || x < lo + kBand);
+        };
+        unsigned bands = 1;                           // those that have a weight in this tile
         if constexpr (WIDE) {
             bool low = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) low |= y[n][i] < kLow;
-            if (__any_sync(0xffffffffu, low)) bands = 4;
-        }
+                for (int i = 0; i < 4; ++i) low |= y[n][i] < kLow && y[n][i] >= kLow - 3 * kBand;
+            if (__any_sync(0xffffffffu, low)) {
 #pragma unroll 1
-        for (int k = 0; k < bands; ++k) {
-            unsigned pf[NT][NP][2];
-            if (k) {
+                for (int k = 1; k < 4; ++k) {
+                    bool in = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int j = 0; j < MT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][j][i] *= 16777216.f;
+                        for (int i = 0; i < 4; ++i) in |= in_band(y[n][i], k);
+                    bands |= (__any_sync(0xffffffffu, in) ? 1u : 0u) << k;
+                }
             }
+        }
+        auto scale_o = [&](float f) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (WIDE) l[n][i & 1] += ex2(y[n][i]);
+        int up = 0;                                   // O holds 2^up times itself
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            if (WIDE && !(bands >> k & 1)) {
+                if (bands >> k == 0) break;
+                continue;
+            }
+            if (WIDE && k) {
+                scale_o(ex2(kBand * static_cast<float>(k) - static_cast<float>(up)));
+                up = static_cast<int>(kBand) * k;
+            }
+            unsigned pf[NT][NP][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[i] = ex2(WIDE ? y[n][i] + kBand * static_cast<float>(k) : y[n][i]);
-                    if (!WIDE || k == 0) l[n][i & 1] += x[i];
-                    if (WIDE && bands > 1 &&
-                        (y[n][i] < kLow - kBand * static_cast<float>(k) || (k && y[n][i] >= kLow - kBand * static_cast<float>(k - 1))))
-                        x[i] = 0.f;
+                    if (!WIDE) l[n][i & 1] += x[i];
+                    if (WIDE && bands > 1 && !in_band(y[n][i], k)) x[i] = isnan(x[i]) ? x[i] : 0.f;
                 }
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
@@ -687,15 +715,9 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                         for (int n = 0; n < NT; ++n) mma<BF>(o[n][j], f[0], f[1], f[2], f[3], pf[n][q][0], pf[n][q][1]);
                 }
             }
+            if constexpr (!WIDE) break;
         }
-        if (WIDE && bands > 1) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][j][i] *= 2.117582368135751e-22f;   // 2^-72
-        }
+        if (WIDE && up) scale_o(ex2(static_cast<float>(-up)));
     };
 
 #pragma unroll 1

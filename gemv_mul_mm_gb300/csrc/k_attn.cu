@@ -89,15 +89,18 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     constexpr int64_t step = attn::kWarps * 16;
     const int64_t steps = (keys + step - 1) / step;
     // The split count n with the least expected time, in steps of 64 keys (an SM
-    // takes about 0.6 us for one, however many blocks share it): the steps of
-    // the busiest SM, plus a block's fixed part (8: query, first loads, warps
-    // joined), of which further waves hide a part, plus the join. Candidates
-    // give every SM a whole number of blocks, or are powers of two. Lengths
-    // are known on the device only: a batch is taken to be anything between
-    // its bound and half of it. A smaller count wins within 5 %.
+    // takes 0.5 to 0.7 us for one, and q8_0 a quarter more for each block
+    // missing from a full SM): the steps of the busiest SM, plus a block's
+    // fixed part (8: query, first loads, warps joined), of which further waves
+    // hide a part, plus the join. Candidates give every SM a whole number of
+    // blocks, or are powers of two. Lengths are known on the device only: a
+    // batch is taken to be anything between its bound and half of it. A
+    // smaller count wins within 3 %.
     auto busiest = [&](double blocks, int64_t per) {
         const double load = blocks / sms, waves = std::ceil(load / resident);
-        return (load <= resident ? std::ceil(load) : load + 0.5) * static_cast<double>(per) + 8.0 + 5.6 * (waves - 1);
+        const double idle = fmt == QMM_KV_Q8_0 && load < resident ? resident - std::ceil(load) : 0.0;
+        return (load <= resident ? std::ceil(load) : load + 0.5) * (1.0 + 0.25 * idle) * static_cast<double>(per) + 8.0 +
+               5.6 * (waves - 1);
     };
     auto cost = [&](int64_t n, int64_t per) {
         const double full = busiest(static_cast<double>(items) * n, per);
@@ -112,7 +115,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
         if (s < 2 || s > most) continue;
         const int64_t per = (steps + s - 1) / s, n = (steps + per - 1) / per;
         const double c = cost(n, per);
-        if (n < best ? c <= best_cost * 1.05 : c < best_cost * 0.95) {
+        if (n < best ? c <= best_cost * 1.03 : c < best_cost * 0.97) {
             best_cost = c;
             best = n;
         }
