@@ -118,7 +118,7 @@ int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, 
     if (!dtype_ok(dtype)) return QMM_ERR_BAD_DTYPE;
     if (T < 0 || H < 0 || D < 0 || x_ts < 0 || x_hs < 0 || y_ts < 0 || y_hs < 0) return QMM_ERR_BAD_ARGUMENT;
     if (T == 0 || H == 0 || D == 0) return QMM_ERR_EMPTY_SHAPE;
-    if (T > kBig || H > 65536 || D > 65536 || x_ts > kBig || x_hs > kBig || y_ts > kBig || y_hs > kBig)
+    if (T > kBig || H > 65536 || D > 2048 || x_ts > kBig || x_hs > kBig || y_ts > kBig || y_hs > kBig)
         return QMM_ERR_BAD_ARGUMENT;
     if (!X || !Y) return QMM_ERR_NULL_POINTER;
     if (!aligned(X, esize(dtype)) || !aligned(Y, esize(dtype))) return QMM_ERR_MISALIGNED;

@@ -5,6 +5,7 @@
 // own one 32-element block. Head dims are multiples of 32, so a block never
 // straddles a row or a warp.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_common.cuh"
 
@@ -14,62 +15,103 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int N = 8;
 
-// Elements [e, e + 8) of a row in fp32.
-template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T* p, float (&x)[N]) {
-    if constexpr (ALIGNED) {
-        load_vec<T, N>(p, x);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = to_f32<T>(p[j]);
-    }
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// a / 127 rounded once, for 0 <= a < 2^128 away from subnormal quotients (which
+// f16 rounds to 0): the product with the rounded reciprocal, corrected once by
+// its exact remainder (Markstein's scheme).
+__device__ __forceinline__ float over_127(float a) {
+    constexpr float r = 1.f / 127.f;
+    const float q = a * r;
+    return fmaf(fmaf(-q, 127.f, a), r, q);
 }
 
 // Q8_0: d = f16(max |x| / 127), code = rint(x / d) in [-127, 127], each division
 // rounded once; a block of zeros (or whose d underflows) has d = 0 and codes
 // 0. A block that holds an Inf or NaN, or whose d overflows f16, gets d = NaN
 // and reads back as NaN, so that a bad activation stays visible.
+//
+// x / d is first taken as x * (1 / d), off by less than 2^-15 at |x / d| <= 128:
+// only quotients that near to half an integer can round the other way, and
+// only lanes that hold one divide (once in some thousand values). Adding 1.5 *
+// 2^23 rounds to an integer and leaves its low byte in the low byte.
 __device__ __forceinline__ void quant8(const float (&x)[N], uint2& codes, __half& d) {
-    float amax = 0.f;
-    bool bad = false;
+    float amax = fabsf(x[0]);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        amax = fmaxf(amax, fabsf(x[j]));
-        bad |= !isfinite(x[j]);
-    }
-    if (bad) amax = INFINITY;
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    d = __float2half_rn(__fdiv_rn(amax, 127.f));
+    for (int j = 1; j < N; ++j) amax = max_nan(amax, fabsf(x[j]));
+    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    d = __float2half_rn(over_127(amax));
     const float df = __half2float(d);
-    const bool finite = isfinite(df);
-    if (!finite) d = __ushort_as_half(0x7fff);
-    unsigned w[2] = {0u, 0u};
-    if (finite && df > 0.f) {
+    if (!(df < INFINITY)) d = __ushort_as_half(0x7fff);
+    codes = make_uint2(0u, 0u);
+    if (!(df > 0.f && df < INFINITY)) return;
+    constexpr float kRound = 12582912.f;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df));
+    float q[N];
+    float off = 0.f;                     // the largest distance of a quotient from its integer
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int q = max(-127, min(127, __float2int_rn(__fdiv_rn(x[j], df))));
-            w[j / 4] |= (static_cast<unsigned>(q) & 0xffu) << (8 * (j % 4));
-        }
+    for (int j = 0; j < N; j += 2) {
+        const float2 v = make_float2(x[j], x[j + 1]), rr = make_float2(r, r);
+        const float2 n = fma2(v, rr, make_float2(kRound, kRound));
+        const float2 m = fma2(n, make_float2(-1.f, -1.f), make_float2(kRound, kRound));   // minus the integer
+        const float2 e = fma2(v, rr, m);
+        off = fmaxf(fmaxf(off, fabsf(e.x)), fabsf(e.y));
+        q[j] = n.x;
+        q[j + 1] = n.y;
+    }
+    // a subnormal d is coarse: quotients reach 190 and are clamped
+    if (off > 0.49996f || df < 6.103515625e-05f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = fmaxf(-127.f, fminf(127.f, rintf(__fdiv_rn(x[j], df)))) + kRound;
+    }
+    unsigned w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const unsigned a = __byte_perm(__float_as_uint(q[4 * k]), __float_as_uint(q[4 * k + 1]), 0x0040);
+        const unsigned b = __byte_perm(__float_as_uint(q[4 * k + 2]), __float_as_uint(q[4 * k + 3]), 0x0040);
+        w[k] = __byte_perm(a, b, 0x5410);
     }
     codes = make_uint2(w[0], w[1]);
 }
 
-// All 32 lanes of a warp call this together (quant8 shuffles); `active` lanes
-// write.
+// Where a thread's eight elements of a row go: the same place in every head's
+// unit. All 32 lanes of a warp call put8 together (quant8 shuffles); lanes with
+// `writes` false write nothing.
 template <int FMT>
-__device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t row, int e, const float (&x)[N], bool active) {
+__device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t row, int e, const float (&x)[N], bool writes) {
     if constexpr (FMT == QMM_KV_Q8_0) {
         uint2 codes;
         __half d;
         quant8(x, codes, d);
-        if (!active) return;
+        if (!writes) return;
         *reinterpret_cast<uint2*>(unit + row * c.D + e) = codes;
         if (e % 32 == 0)
             reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
     } else {
-        if (!active) return;
+        if (!writes) return;
         using T = typename std::conditional<FMT == QMM_KV_F16, __half, __nv_bfloat16>::type;
-        store_vec<T, N>(reinterpret_cast<T*>(unit) + row * c.D + e, x);
+        Vec<T, N> v;
+        v.set(x);
+        v.store(reinterpret_cast<T*>(unit) + row * c.D + e);
     }
 }
 
@@ -88,24 +130,23 @@ __device__ __forceinline__ void pair_of(int e, int rot, bool half, int& pair, in
     }
 }
 
-// One thread: eight elements of `heads_per` heads of one token, of K or of V.
+// One thread: eight elements of `heads_per` heads of one token, of K (blockIdx.y
+// 0) or of V.
 // Key elements are rotated as y_e = x_e cos a + sign x_partner sin a; the
 // partner vector (half layout) is read through L1, which the lane that owns
 // it reads too, so no row is staged and no lane waits for another.
-template <typename T, int FMT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) k_kv_store(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
+template <typename T, int FMT, bool ALIGNED, bool ROPE>
+__global__ void __launch_bounds__(kThreads, ROPE ? 3 : 5) k_kv_store(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
     grid_dep_launch();
     grid_dep_wait();
     const int64_t id0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     const bool active = id0 < threads;
-    const int64_t id = active ? id0 : threads - 1;
-    const int vecs = a.c.D / N;
-    const int e = static_cast<int>(id % vecs) * N;
-    int64_t r = id / vecs;
-    const bool is_v = r & 1;
-    r >>= 1;
-    const int hg = static_cast<int>(r % head_groups);
-    const int64_t t = r / head_groups;
+    int vec, hg;
+    int64_t r, t;
+    div_mod(active ? id0 : threads - 1, a.c.D / N, r, vec);
+    const int e = vec * N;
+    const bool is_v = blockIdx.y;        // keys and values in blocks of their own: one path a warp
+    div_mod(r, head_groups, t, hg);
     const int h0 = hg * heads_per, h1 = min(h0 + heads_per, a.c.heads);
     const int64_t slot = a.slots[t];
     const bool bad = slot < -1 || slot >= (a.c.n_pages << a.c.page_shift);
@@ -114,56 +155,71 @@ __global__ void __launch_bounds__(kThreads) k_kv_store(KvStoreArgs a, int64_t th
     const int64_t page = writes ? slot >> a.c.page_shift : 0;
     const int64_t row = writes ? slot & ((1ll << a.c.page_shift) - 1) : 0;
     uint8_t* base = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride;
+    constexpr int kB = ROPE || sizeof(T) == 4 ? 2 : 4;   // heads whose loads are in flight together
     const int64_t unit = a.c.unit();
-    const bool turn = !is_v && a.pos && e < a.rot;
+    const bool turn = ROPE && !is_v && e < a.rot;
     const bool half = a.layout == QMM_ROPE_HALF;
     // all eight partners are one aligned vector
     const bool vec_pair = ALIGNED && half && a.rot % (2 * N) == 0;
 
     float c[N], s[N];
-    if (turn) {
-        const int32_t pos = a.pos[t];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            c[j] = 1.f;
-            s[j] = 0.f;
-            if (e + j < a.rot) {
-                int pair, partner;
-                float sign;
-                pair_of(e + j, a.rot, half, pair, partner, sign);
-                rope_cs(pos, a.turns[pair], a.mscale, c[j], s[j]);
-                s[j] *= sign;
-            }
-        }
-    }
     const T* x = static_cast<const T*>(is_v ? a.V : a.K) + t * (is_v ? a.v_ts : a.k_ts);
     const int64_t hs = is_v ? a.v_hs : a.k_hs;
-#pragma unroll 4
-    for (int i = 0; i < heads_per; ++i) {
-        const int h = min(h0 + i, h1 - 1);   // the last group repeats its last head: lanes stay together
-        const T* xh = x + h * hs;
-        float v[N];
-        load8<T, ALIGNED>(xh + e, v);
-        if (turn) {
-            float w[N];
-            if (vec_pair) {
-                load8<T, ALIGNED>(xh + (e < a.rot / 2 ? e + a.rot / 2 : e - a.rot / 2), w);
-            } else if (!half) {
+    const int partner = e < a.rot / 2 ? e + a.rot / 2 : e - a.rot / 2;
+#pragma unroll 1
+    for (int i = 0; i < heads_per; i += kB) {
+        Vec<T, N> v[kB], w[kB];
+        // the last group repeats its last head: lanes stay together
+        auto head = [&](int k) { return min(h0 + i + k, h1 - 1); };
 #pragma unroll
-                for (int j = 0; j < N; ++j) w[j] = v[j ^ 1];
-            } else {
+        for (int k = 0; k < kB; ++k) {
+            const T* xh = x + head(k) * hs;
+            if constexpr (ALIGNED) v[k].load(xh + e);
+            else v[k].load_unaligned(xh + e);
+            if (turn && vec_pair) w[k].load(xh + partner);
+        }
+        if (turn && i == 0) {               // behind the first loads
+            const int32_t pos = a.pos[t];
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    int pair, partner = e + j;
+            for (int j = 0; j < N; ++j) {
+                c[j] = 1.f;
+                s[j] = 0.f;
+                if (e + j < a.rot) {
+                    int pair, partner;
                     float sign;
-                    if (e + j < a.rot) pair_of(e + j, a.rot, half, pair, partner, sign);
-                    w[j] = to_f32<T>(xh[partner]);
+                    pair_of(e + j, a.rot, half, pair, partner, sign);
+                    rope_cs(pos, a.turns[pair], a.mscale, c[j], s[j]);
+                    s[j] *= sign;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = e + j < a.rot ? v[j] * c[j] + w[j] * s[j] : v[j];
         }
-        put8<FMT>(a.c, base + h * unit, row, e, v, writes);
+#pragma unroll
+        for (int k = 0; k < kB; ++k) {
+            if (i + k >= heads_per) break;
+            float f[N];
+            v[k].get(f);
+            if (turn) {
+                float g[N];
+                if (vec_pair) {
+                    w[k].get(g);
+                } else if (!half) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) g[j] = f[j ^ 1];
+                } else {
+                    const T* xh = x + head(k) * hs;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        int pair, other = e + j;
+                        float sign;
+                        if (e + j < a.rot) pair_of(e + j, a.rot, half, pair, other, sign);
+                        g[j] = to_f32<T>(xh[other]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = e + j < a.rot ? f[j] * c[j] + g[j] * s[j] : f[j];
+            }
+            put8<FMT>(a.c, base + head(k) * unit, row, e, f, writes);
+        }
     }
 }
 
@@ -173,46 +229,65 @@ __global__ void __launch_bounds__(kThreads) k_kv_load(KvLoadArgs a, int64_t thre
     grid_dep_wait();
     const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (id >= threads) return;
-    const int vecs = a.c.D / N;
-    const int e = static_cast<int>(id % vecs) * N;
-    int64_t r = id / vecs;
-    const bool is_v = r & 1;
-    r >>= 1;
-    const int hg = static_cast<int>(r % head_groups);
-    const int64_t t = r / head_groups;
+    int vec, hg;
+    int64_t r, t;
+    div_mod(id, a.c.D / N, r, vec);
+    const int e = vec * N;
+    const bool is_v = blockIdx.y;
+    div_mod(r, head_groups, t, hg);
     const int h0 = hg * heads_per, h1 = min(h0 + heads_per, a.c.heads);
     const int64_t slot = a.slots[t];
     const bool bad = slot < -1 || slot >= (a.c.n_pages << a.c.page_shift);
     if (bad && e == 0) atomicOr(a.err, DEV_ERR_BAD_SLOT);
     T* y = static_cast<T*>(is_v ? a.V : a.K) + t * a.c.heads * a.c.D + e;
     if (bad || slot < 0) {
-        float v[N];
+        float f[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = bad ? NAN : 0.f;
-        for (int h = h0; h < h1; ++h) store_vec<T, N>(y + static_cast<int64_t>(h) * a.c.D, v);
+        for (int j = 0; j < N; ++j) f[j] = bad ? NAN : 0.f;
+        Vec<T, N> v;
+        v.set(f);
+        for (int h = h0; h < h1; ++h) v.store(y + static_cast<int64_t>(h) * a.c.D);
         return;
     }
+    constexpr int kB = 4;                // heads whose loads are in flight together
     const int64_t row = slot & ((1ll << a.c.page_shift) - 1);
     const int64_t unit = a.c.unit();
     const uint8_t* base = (is_v ? a.c.v : a.c.k) + (slot >> a.c.page_shift) * a.c.page_stride;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-        const uint8_t* p = base + h * unit;
-        float v[N];
-        if constexpr (FMT == QMM_KV_Q8_0) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p + row * a.c.D + e);
-            const float d = __half2float(
-                reinterpret_cast<const __half*>(p + (static_cast<int64_t>(a.c.D) << a.c.page_shift))[row * (a.c.D / 32) + e / 32]);
+    const int64_t at = row * a.c.D + e, scale_at = (static_cast<int64_t>(a.c.D) << a.c.page_shift) + (row * (a.c.D / 32) + e / 32) * 2;
+#pragma unroll 1
+    for (int h = h0; h < h1; h += kB) {
+        using S = typename std::conditional<FMT == QMM_KV_BF16, __nv_bfloat16, __half>::type;
+        Vec<S, N> v[kB];
+        uint2 w[kB];
+        __half d[kB];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const unsigned word = j < 4 ? w.x : w.y;
-                v[j] = d * static_cast<float>(static_cast<int8_t>(word >> (8 * (j % 4))));
+        for (int k = 0; k < kB; ++k) {
+            const uint8_t* p = base + min(h + k, h1 - 1) * unit;
+            if constexpr (FMT == QMM_KV_Q8_0) {
+                w[k] = *reinterpret_cast<const uint2*>(p + at);
+                d[k] = *reinterpret_cast<const __half*>(p + scale_at);
+            } else {
+                v[k].load(reinterpret_cast<const S*>(p) + at);
             }
-        } else {
-            using S = typename std::conditional<FMT == QMM_KV_F16, __half, __nv_bfloat16>::type;
-            load_vec<S, N>(reinterpret_cast<const S*>(p) + row * a.c.D + e, v);
         }
-        store_vec<T, N>(y + static_cast<int64_t>(h) * a.c.D, v);
+#pragma unroll
+        for (int k = 0; k < kB; ++k) {
+            if (h + k >= h1) break;
+            float f[N];
+            if constexpr (FMT == QMM_KV_Q8_0) {
+                // code + 128 in the low byte of 2^23, less 2^23 + 128: exact
+                const float df = __half2float(d[k]);
+                const unsigned u[2] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u};
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    f[j] = df * (__uint_as_float(__byte_perm(u[j / 4], 0x4b000000u, 0x7440 + j % 4)) - 8388736.f);
+            } else {
+                v[k].get(f);
+            }
+            Vec<T, N> out;
+            out.set(f);
+            out.store(y + static_cast<int64_t>(h + k) * a.c.D);
+        }
     }
 }
 
@@ -232,7 +307,7 @@ Shape shape(int64_t T, int heads, int D) {
     Shape s;
     s.per = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({heads, 8, all / want})));
     s.groups = (heads + s.per - 1) / s.per;
-    s.threads = T * 2 * (D / N) * s.groups;
+    s.threads = T * (D / N) * s.groups;        // of keys, and as many of values
     s.blocks = (s.threads + kThreads - 1) / kThreads;
     return s;
 }
@@ -244,12 +319,17 @@ template <typename T> cudaError_t store(const KvStoreArgs& a, cudaStream_t s) {
     const bool al = reinterpret_cast<uintptr_t>(a.K) % 16 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0 &&
                     a.k_ts * S % 16 == 0 && a.k_hs * S % 16 == 0 && a.v_ts * S % 16 == 0 && a.v_hs * S % 16 == 0;
     auto go = [&](auto kernel) {
-        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks)), kThreads, 0, s, a, g.threads, g.groups, g.per);
+        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks), 2), kThreads, 0, s, a, g.threads, g.groups, g.per);
+    };
+    auto pick = [&](auto fmt) {
+        constexpr int F = decltype(fmt)::value;
+        if (a.pos) return al ? go(k_kv_store<T, F, true, true>) : go(k_kv_store<T, F, false, true>);
+        return al ? go(k_kv_store<T, F, true, false>) : go(k_kv_store<T, F, false, false>);
     };
     switch (a.c.fmt) {
-    case QMM_KV_F16: return al ? go(k_kv_store<T, QMM_KV_F16, true>) : go(k_kv_store<T, QMM_KV_F16, false>);
-    case QMM_KV_BF16: return al ? go(k_kv_store<T, QMM_KV_BF16, true>) : go(k_kv_store<T, QMM_KV_BF16, false>);
-    default: return al ? go(k_kv_store<T, QMM_KV_Q8_0, true>) : go(k_kv_store<T, QMM_KV_Q8_0, false>);
+    case QMM_KV_F16: return pick(std::integral_constant<int, QMM_KV_F16>{});
+    case QMM_KV_BF16: return pick(std::integral_constant<int, QMM_KV_BF16>{});
+    default: return pick(std::integral_constant<int, QMM_KV_Q8_0>{});
     }
 }
 
@@ -257,7 +337,7 @@ template <typename T> cudaError_t load(const KvLoadArgs& a, cudaStream_t s) {
     const Shape g = shape(a.T, a.c.heads, a.c.D);
     if (g.blocks > 0x7fffffff) return cudaErrorInvalidValue;
     auto go = [&](auto kernel) {
-        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks)), kThreads, 0, s, a, g.threads, g.groups, g.per);
+        return launch_chained(kernel, dim3(static_cast<unsigned>(g.blocks), 2), kThreads, 0, s, a, g.threads, g.groups, g.per);
     };
     switch (a.c.fmt) {
     case QMM_KV_F16: return go(k_kv_load<T, QMM_KV_F16>);

@@ -4,6 +4,14 @@
 //   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a)
 // (x1, x2) = elements (i, i + rot/2) (half layout) or (2i, 2i + 1)
 // (interleaved). Elements from rot on are copied.
+//
+// Bound by reading X and writing Y. An item is two vectors of N elements of one
+// head (half layout: N elements of the first half and their partners;
+// interleaved: 2 N consecutive ones; past rot: up to 2 N copied). A block takes
+// a few tokens and up to four items a thread; it loads them all, computes each
+// (token, pair)'s cos and sin once into shared memory meanwhile (a thread that
+// computed its own spent as many instructions on them as on four heads), and
+// then rotates and stores.
 #include <algorithm>
 
 #include "kv_common.cuh"
@@ -12,70 +20,88 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kItems = 4;        // items per thread, loads in flight together
+constexpr int kAngles = 1024;    // (token, pair)s per block
 
-// A thread holds two vectors of N elements of each of its heads: in the half
-// layout N elements of the first half and their partners, interleaved 2 N
-// consecutive elements; past `rot` it copies 2 N (the last thread N)
-// elements. cos and sin are computed once per thread and serve all its heads.
+struct RopeShape {
+    int units, rot_units;        // items of a head, those of them that rotate
+    int heads;                   // heads per block
+    int tokens;                  // tokens per block
+    int head_groups;
+};
+
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) k_rope(RopeArgs a, int64_t threads, int units, int rot_units, int head_groups,
-                                                   int heads_per) {
+__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeShape g) {
     grid_dep_launch();
     grid_dep_wait();
-    const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    if (id >= threads) return;
-    const int u = static_cast<int>(id % units);
-    const int64_t th = id / units;
-    const int hg = static_cast<int>(th % head_groups);
-    const int64_t t = th / head_groups;
-    const int64_t h0 = static_cast<int64_t>(hg) * heads_per;
-    const int64_t h1 = imin64(h0 + heads_per, a.H);
-    const bool turn = u < rot_units;
+    __shared__ float2 cs[kAngles];   // [token][j][unit]: pair unit * N + j, units side by side for the reads
+    const int hg = static_cast<int>(blockIdx.x % static_cast<unsigned>(g.head_groups));
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(g.head_groups)) * g.tokens;
+    const int tokens = static_cast<int>(imin64(g.tokens, a.T - t0));
+    const int h0 = hg * g.heads, heads = static_cast<int>(imin64(g.heads, a.H - h0));
+    const int pairs = a.rot / 2;
     const bool half = a.layout == QMM_ROPE_HALF;
-    const int64_t e0 = turn ? (half ? static_cast<int64_t>(u) * N : static_cast<int64_t>(u) * 2 * N)
-                            : a.rot + static_cast<int64_t>(u - rot_units) * 2 * N;
-    const int64_t e1 = turn && half ? e0 + a.rot / 2 : e0 + N;
-    const bool second = e1 < a.D;
 
-    float c[N], s[N];
-    if (turn) {
-        const int32_t pos = a.pos[t];
+    Vec<T, N> v0[kItems], v1[kItems];
+    int unit[kItems], tok[kItems];
+    int64_t off_x[kItems], off_y[kItems];
+    // item = (token, head, unit), units innermost; a thread's items are 256 apart
 #pragma unroll
-        for (int j = 0; j < N; ++j) rope_cs(pos, a.turns[u * N + j], a.mscale, c[j], s[j]);
+    for (int k = 0; k < kItems; ++k) {
+        const unsigned i = threadIdx.x + k * kThreads, th = i / static_cast<unsigned>(g.units);
+        unit[k] = static_cast<int>(i - th * g.units);
+        tok[k] = static_cast<int>(th / static_cast<unsigned>(heads));
+        const int h = h0 + static_cast<int>(th) - tok[k] * heads;
+        const bool turn = unit[k] < g.rot_units;
+        const int e0 = turn ? (half ? unit[k] * N : unit[k] * 2 * N) : a.rot + (unit[k] - g.rot_units) * 2 * N;
+        off_x[k] = (t0 + tok[k]) * a.x_ts + h * a.x_hs + e0;
+        off_y[k] = (t0 + tok[k]) * a.y_ts + h * a.y_hs + e0;
+        if (tok[k] < tokens) {
+            const T* x = static_cast<const T*>(a.X) + off_x[k];
+            v0[k].load(x);
+            if (turn) v1[k].load(x + (half ? pairs : N));
+            else if (e0 + N < a.D) v1[k].load(x + N);
+        }
     }
-    const T* x = static_cast<const T*>(a.X) + t * a.x_ts;
-    T* y = static_cast<T*>(a.Y) + t * a.y_ts;
-#pragma unroll 4
-    for (int64_t h = h0; h < h1; ++h) {
-        float v0[N], v1[N];
-        load_vec<T, N>(x + h * a.x_hs + e0, v0);
-        if (second) load_vec<T, N>(x + h * a.x_hs + e1, v1);
-        if (turn) {
-            if (half) {
+    for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+        const int tt = i / pairs, p = i - tt * pairs;
+        float2 v;
+        rope_cs(a.pos[t0 + tt], a.turns[p], a.mscale, v.x, v.y);
+        cs[tt * pairs + p % N * g.rot_units + p / N] = v;
+    }
+    __syncthreads();
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float x1 = v0[j], x2 = v1[j];
-                    v0[j] = x1 * c[j] - x2 * s[j];
-                    v1[j] = x2 * c[j] + x1 * s[j];
-                }
-            } else if constexpr (N == 1) {
-                const float x1 = v0[0], x2 = v1[0];
-                v0[0] = x1 * c[0] - x2 * s[0];
-                v1[0] = x2 * c[0] + x1 * s[0];
+    for (int k = 0; k < kItems; ++k) {
+        if (tok[k] >= tokens) break;
+        const bool turn = unit[k] < g.rot_units;
+        if (turn) {
+            float f0[N], f1[N];
+            v0[k].get(f0);
+            v1[k].get(f1);
+            const float2* c = cs + tok[k] * pairs + unit[k];
+            auto turn_pair = [&](float& x1, float& x2, int j) {
+                const float2 w = c[j * g.rot_units];
+                const float y1 = x1 * w.x - x2 * w.y;
+                x2 = x2 * w.x + x1 * w.y;
+                x1 = y1;
+            };
+            if (half || N == 1) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) turn_pair(f0[j], f1[j], j);
             } else {
 #pragma unroll
                 for (int j = 0; j < N / 2; ++j) {
-                    float x1 = v0[2 * j], x2 = v0[2 * j + 1];
-                    v0[2 * j] = x1 * c[j] - x2 * s[j];
-                    v0[2 * j + 1] = x2 * c[j] + x1 * s[j];
-                    x1 = v1[2 * j], x2 = v1[2 * j + 1];
-                    v1[2 * j] = x1 * c[N / 2 + j] - x2 * s[N / 2 + j];
-                    v1[2 * j + 1] = x2 * c[N / 2 + j] + x1 * s[N / 2 + j];
+                    turn_pair(f0[2 * j], f0[(2 * j + 1) % N], j);
+                    turn_pair(f1[2 * j], f1[(2 * j + 1) % N], N / 2 + j);
                 }
             }
+            v0[k].set(f0);
+            v1[k].set(f1);
         }
-        store_vec<T, N>(y + h * a.y_hs + e0, v0);
-        if (second) store_vec<T, N>(y + h * a.y_hs + e1, v1);
+        T* y = static_cast<T*>(a.Y) + off_y[k];
+        v0[k].store(y);
+        if (turn) v1[k].store(y + (half ? pairs : N));
+        else if (a.rot + (unit[k] - g.rot_units) * 2 * N + N < a.D) v1[k].store(y + N);
     }
 }
 
@@ -92,22 +118,21 @@ bool vec_ok(const RopeArgs& a, int n, int size) {
 
 template <typename T, int N> cudaError_t run(const RopeArgs& a, cudaStream_t s) {
     const bool in_place = a.X == a.Y && a.x_ts == a.y_ts && a.x_hs == a.y_hs;
-    const int rot_units = a.rot / (2 * N);
-    const int rest = static_cast<int>((a.D - a.rot + 2 * N - 1) / (2 * N));
-    const int units = rot_units + (in_place ? 0 : rest);
-    // heads per thread: as many as leave about two blocks of 256 threads per SM
-    // in flight, so that cos and sin are shared; one where the call is small
+    RopeShape g;
+    g.rot_units = a.rot / (2 * N);
+    g.units = g.rot_units + (in_place ? 0 : static_cast<int>((a.D - a.rot + 2 * N - 1) / (2 * N)));
+    // A block's items: four a thread where that leaves a block per SM, else one
     int dev = 0;
     cudaGetDevice(&dev);
-    const int64_t want = static_cast<int64_t>(sm_count(dev)) * 2 * kThreads;
-    const int64_t all = a.T * units * a.H;
-    const int64_t per = std::max<int64_t>(1, std::min<int64_t>({a.H, 16, all / want}));
-    const int groups = static_cast<int>((a.H + per - 1) / per);
-    const int64_t threads = a.T * units * groups;
-    const int64_t blocks = (threads + kThreads - 1) / kThreads;
+    const int64_t all = a.T * a.H * g.units;
+    const int items = all >= static_cast<int64_t>(sm_count(dev)) * kItems * kThreads ? kItems * kThreads : kThreads;
+    g.heads = static_cast<int>(std::min<int64_t>(a.H, std::max(1, items / g.units)));
+    g.head_groups = static_cast<int>((a.H + g.heads - 1) / g.heads);
+    // (units is at most 1024: one head always fits)
+    g.tokens = std::max(1, std::min(items / (g.heads * g.units), kAngles / (a.rot / 2)));
+    const int64_t blocks = (a.T + g.tokens - 1) / g.tokens * g.head_groups;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_chained(k_rope<T, N>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, s, a, threads, units, rot_units, groups,
-                          static_cast<int>(per));
+    return launch_chained(k_rope<T, N>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, s, a, g);
 }
 
 template <typename T> cudaError_t pick(const RopeArgs& a, cudaStream_t s) {

@@ -48,31 +48,49 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Loads / stores N elements as fp32; the address is aligned to
-// min(16, N * sizeof(T)) bytes.
-template <typename T, int N> __device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
-    constexpr int B = N * static_cast<int>(sizeof(T)) < 16 ? N * static_cast<int>(sizeof(T)) : 16;
-    constexpr int PER = B / static_cast<int>(sizeof(T));
+// N elements of type T as they lie in memory, moved in accesses of up to 16
+// bytes (the address is aligned to min(16, N * sizeof(T)) bytes). Kernels load
+// the vectors of several heads before they use the first: the stores between
+// could alias, so the compiler does not.
+template <typename T, int N> struct Vec {
+    static constexpr int B = N * static_cast<int>(sizeof(T)) < 16 ? N * static_cast<int>(sizeof(T)) : 16;
+    static constexpr int PER = B / static_cast<int>(sizeof(T));
     using V = typename VecOf<B>::type;
+    V v[N / PER];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < N / PER; ++i) {
-        const V v = reinterpret_cast<const V*>(p)[i];
-        const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) x[i * PER + j] = to_f32<T>(e[j]);
+        for (int i = 0; i < N / PER; ++i) v[i] = reinterpret_cast<const V*>(p)[i];
     }
-}
-template <typename T, int N> __device__ __forceinline__ void store_vec(T* p, const float (&x)[N]) {
-    constexpr int B = N * static_cast<int>(sizeof(T)) < 16 ? N * static_cast<int>(sizeof(T)) : 16;
-    constexpr int PER = B / static_cast<int>(sizeof(T));
-    using V = typename VecOf<B>::type;
+    __device__ __forceinline__ void load_unaligned(const T* p) {
+        T* e = reinterpret_cast<T*>(v);
 #pragma unroll
-    for (int i = 0; i < N / PER; ++i) {
-        V v;
-        T* e = reinterpret_cast<T*>(&v);
+        for (int j = 0; j < N; ++j) e[j] = p[j];
+    }
+    __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) e[j] = from_f32<T>(x[i * PER + j]);
-        reinterpret_cast<V*>(p)[i] = v;
+        for (int i = 0; i < N / PER; ++i) reinterpret_cast<V*>(p)[i] = v[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+        const T* e = reinterpret_cast<const T*>(v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = to_f32<T>(e[j]);
+    }
+    __device__ __forceinline__ void set(const float (&x)[N]) {
+        T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) e[j] = from_f32<T>(x[j]);
+    }
+};
+
+// q = a / b, r = a % b for 0 <= a, 0 < b; 32-bit where a allows it.
+__device__ __forceinline__ void div_mod(int64_t a, int b, int64_t& q, int& r) {
+    if (a >> 32) {
+        q = a / b;
+        r = static_cast<int>(a - q * b);
+    } else {
+        const unsigned u = static_cast<unsigned>(a), d = u / static_cast<unsigned>(b);
+        q = d;
+        r = static_cast<int>(u - d * static_cast<unsigned>(b));
     }
 }
 

@@ -422,7 +422,7 @@ QMM_API int qrope_turns(double base, int rot_dim, int scaling, double factor, do
                         double slow, uint64_t* turns, float* mscale);
 
 /*
- * qrope -- rotary positions on T tokens of H heads of D values. For pair
+ * qrope -- rotary positions on T tokens of H heads of D values (D <= 2048). For pair
  * i < rot_dim / 2, with a = 2 pi positions[t] * turns[i] / 2^64:
  *
  *   y1 = mscale (x1 cos a - x2 sin a),   y2 = mscale (x2 cos a + x1 sin a)
