@@ -297,7 +297,12 @@ def qmoe_ffn(kind, W_gu, gu_stride: int, W_down, down_stride: int, n_experts: in
 
 def _torch():
     """What the serving operators' bindings use of torch, looked up once: a call
-    on a decode step costs about as much on the host as on the GPU."""
+    on a decode step costs about as much on the host as on the GPU.
+
+    (torch, element types, raw stream of a device, current device, new tensor).
+    The raw stream, the device and the allocation go around torch's Python and
+    dispatcher layers where this torch has the direct functions (an allocation
+    then takes 0.8 us instead of 2 to 6)."""
     global _T
     if _T is None:
         import torch
@@ -306,7 +311,12 @@ def _torch():
         if raw is None:
             def raw(device):
                 return torch.cuda.current_stream(device).cuda_stream
-        _T = (torch, dtypes, raw, torch.cuda.current_device, torch.int32, torch.int64)
+        current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+        if new is None:
+            def new(shape, strides, dtype):
+                return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+        _T = (torch, dtypes, raw, current, new)
     return _T
 
 
@@ -318,14 +328,14 @@ def _device(X, what: str) -> int:
     dev = X.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if dev != _torch()[3]():
+    if dev != _T[3]():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
 
 
 def _act(X, what: str) -> int:
     """Element type of an f32 / f16 / bf16 tensor."""
-    dt = _torch()[1].get(X.dtype)
+    dt = (_T or _torch())[1].get(X.dtype)
     if dt is None:
         raise TypeError(f"{what} must be float32, float16 or bfloat16, got {X.dtype}")
     return dt
@@ -411,14 +421,14 @@ def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=No
     each head in pairs (i, i + rot/2) ("half") or (2i, 2i + 1)
     ("interleaved"). positions: int32 (T,); turns: qrope_turns. X may be a
     view; out=X rotates in place. Returns out (X's type)."""
-    torch, _, raw, _, i32, i64 = _T or _torch()
+    torch, _, raw, _, new = _T or _torch()
     dt = _act(X, "X")
     T, H, D, n, ts, hs = _rows(X, "X")
     dev = _device(X, "X")
-    pos = _want(positions, i32, T, "positions", dev)
-    tur = _want(turns, i64, -1, "turns", dev)
+    pos = _want(positions, torch.int32, T, "positions", dev)
+    tur = _want(turns, torch.int64, -1, "turns", dev)
     if out is None:
-        out = X.new_empty((T, H, D))
+        out = new((T, H, D), (H * D, D, 1), X.dtype)
         on, ots, ohs = T * H * D, H * D, D
     else:
         if out.shape != X.shape or out.dtype != X.dtype:
@@ -436,7 +446,7 @@ def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None
     (T,); -1 skips a token) of a paged cache of format "f16", "bf16" or "q8_0",
     rotating K first when positions and turns are given. k_cache, v_cache:
     (pages, bytes per page) uint8 tensors (qkv_cache)."""
-    torch, _, raw, _, i32, i64 = _T or _torch()
+    torch, _, raw, _, _ = _T or _torch()
     dt = _act(K, "K")
     if V.dtype != K.dtype or V.shape != K.shape:
         raise ValueError("V must have K's shape and type")
@@ -444,14 +454,14 @@ def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None
     _, _, _, vn, vts, vhs = _rows(V, "V")
     dev = _device(K, "K")
     _on(V, dev, "V")
-    slot = _want(slots, i64, T, "slots", dev)
+    slot = _want(slots, torch.int64, T, "slots", dev)
     n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
     if (positions is None) != (turns is None):
         raise ValueError("positions and turns go together")
     pos = tur = rot = 0
     if positions is not None:
-        pos = _want(positions, i32, T, "positions", dev)
-        tur = _want(turns, i64, -1, "turns", dev)
+        pos = _want(positions, torch.int32, T, "positions", dev)
+        tur = _want(turns, torch.int64, -1, "turns", dev)
         rot = 2 * turns.numel()
     _check(_lib().qkv_store(_fmt(fmt), K.data_ptr(), kn, kts, khs, V.data_ptr(), vn, vts, vhs, dt, slot, pos, tur, rot,
                             ROPE_LAYOUTS[layout], mscale, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps,
@@ -461,17 +471,17 @@ def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None
 def qkv_load(fmt, slots, k_cache, v_cache, page_size: int, n_kv_heads: int, head_dim: int, dtype=None, stream=None):
     """The keys and values in `slots` (int64 (T,); -1 gives zeros) as two (T,
     n_kv_heads, head_dim) tensors of `dtype` (float32 by default)."""
-    torch, dtypes, raw, _, _, i64 = _T or _torch()
+    torch, dtypes, raw, _, new = _T or _torch()
     dt = F32 if dtype is None else dtypes.get(dtype)
     if dt is None:
         raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     dev = _device(k_cache, "k_cache")
     T = slots.numel()
-    slot = _want(slots, i64, T, "slots", dev)
+    slot = _want(slots, torch.int64, T, "slots", dev)
     n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
-    # one allocation for both
-    KV = k_cache.new_empty((2, T, n_kv_heads, head_dim), dtype=dtype or torch.float32)
-    K, V = KV[0], KV[1]
+    shape, strides = (T, n_kv_heads, head_dim), (n_kv_heads * head_dim, head_dim, 1)
+    K = new(shape, strides, dtype or torch.float32)
+    V = new(shape, strides, dtype or torch.float32)
     _check(_lib().qkv_load(_fmt(fmt), slot, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps, page_size,
                            K.data_ptr(), V.data_ptr(), dt, T * n_kv_heads * head_dim, T, n_kv_heads, head_dim,
                            raw(dev) if stream is None else stream), "qkv_load")
@@ -494,32 +504,32 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
     uint8 tensor of qattn_decode_workspace_bytes(...)), allocated here with
     torch if None."""
-    torch, _, raw, _, i32, _ = _T or _torch()
+    torch, _, raw, _, new = _T or _torch()
     dt = _act(q, "q")
     B, H, D, qn, qbs, qhs = _rows(q, "q")
     dev = _device(q, "q")
     n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
     tshape = block_table.shape
-    if block_table.dtype is not i32 or len(tshape) != 2 or tshape[0] != B or \
+    if block_table.dtype is not torch.int32 or len(tshape) != 2 or tshape[0] != B or \
             (tshape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be an int32 tensor (sequences, pages) with contiguous rows")
     _on(block_table, dev, "block_table")
-    lens = _want(seq_lens, i32, B, "seq_lens", dev)
+    lens = _want(seq_lens, torch.int32, B, "seq_lens", dev)
     width, ts = tshape[1], block_table.stride(0)
     if max_len is None:
         max_len = width * page_size
     if out is None:
-        out = q.new_empty((B, H, D))
+        out = new((B, H, D), (H * D, D, 1), q.dtype)
         optr = out.data_ptr()
     else:
         optr = _want(out, q.dtype, B * H * D, "out", dev)
-    lse = q.new_empty((B, H), dtype=torch.float32) if return_lse else None
+    lse = new((B, H), (H, 1), torch.float32) if return_lse else None
     L, f = _lib(), _fmt(fmt)
     wptr = wn = 0
     if workspace is None:
         wn = L.qattn_decode_workspace_bytes(f, dt, B, H, n_kv_heads, D, max_len, window)
         if wn:
-            workspace = k_cache.new_empty(wn)
+            workspace = new((wn,), (1,), torch.uint8)
             wptr = workspace.data_ptr()
     else:
         _on(workspace, dev, "workspace")
