@@ -489,10 +489,13 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 }
             }
         } else {
+            float acc[NT][NQ][4];                     // a sum for each term: the small ones keep their bits
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sx[n][i] = 0.f;
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][q][i] = 0.f;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 unsigned x[4];
@@ -500,8 +503,16 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) mma<BF>(sx[n], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1]);
+                    for (int q = 0; q < NQ; ++q) mma<BF>(acc[n][q], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1]);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sx[n][i] = acc[n][NQ - 1][i];
+#pragma unroll
+                    for (int q = NQ - 2; q >= 0; --q) sx[n][i] += acc[n][q][i];
+                }
         }
 
         // ---- scores, in log2 units
@@ -608,7 +619,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         // ---- weights, as the B operand of the second product: O^T += V^T P^T.
         // A weight below 2^-32 of the largest has lost most of its bits to f16's
         // subnormals. With activations whose type shows that (WIDE), a tile that
-        // has such weights takes them in bands of 2^24, each scaled up with O.
+        // has such weights takes them in bands of 2^24, each scaled into range.
         constexpr bool WIDE = HI && !BF;
         constexpr float kLow = -18.f, kBand = 24.f;
         // band k of weights: [kLow - 24 k, kLow - 24 (k - 1)), the first without an
@@ -636,30 +647,33 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 }
             }
         }
-        auto scale_o = [&](float f) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
-        };
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (WIDE) l[n][i & 1] += ex2(y[n][i]);
-        int up = 0;                                   // O holds 2^up times itself
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             if (WIDE && !(bands >> k & 1)) {
                 if (bands >> k == 0) break;
                 continue;
             }
-            if (WIDE && k) {
-                scale_o(ex2(kBand * static_cast<float>(k) - static_cast<float>(up)));
-                up = static_cast<int>(kBand) * k;
-            }
+            // the MMA's sum cuts off what does not fit in 24 bits: over thousands of
+            // tiles that is a bias of 1e-5 and more. With HI each tile's product
+            // is summed apart and added to O with rounding.
+            [[maybe_unused]] const float down = WIDE ? ex2(-kBand * static_cast<float>(k)) : 1.f;
+            auto add = [&](int n, int j, const unsigned (&f)[4], const unsigned (&p)[NP][2]) {
+                if constexpr (HI) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = NP - 1; q >= 0; --q) mma<BF>(d, f[0], f[1], f[2], f[3], p[q][0], p[q][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][j][i] = WIDE ? fmaf(d[i], down, o[n][j][i]) : o[n][j][i] + d[i];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) mma<BF>(o[n][j], f[0], f[1], f[2], f[3], p[q][0], p[q][1]);
+                }
+            };
             unsigned pf[NT][NP][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -698,10 +712,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                         codes_f16(w[2 * j], f[0], f[1]);
                         codes_f16(w[2 * j + 1], f[2], f[3]);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma<BF>(o[n][2 * c + j], f[0], f[1], f[2], f[3], pd[n][q][0], pd[n][q][1]);
+                        for (int n = 0; n < NT; ++n) add(n, 2 * c + j, f, pd[n]);
                     }
                 }
             } else {
@@ -710,14 +721,11 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                     unsigned f[4];
                     ldsm4_trans(f, stage + v_lane + 32 * j);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma<BF>(o[n][j], f[0], f[1], f[2], f[3], pf[n][q][0], pf[n][q][1]);
+                    for (int n = 0; n < NT; ++n) add(n, j, f, pf[n]);
                 }
             }
             if constexpr (!WIDE) break;
         }
-        if (WIDE && up) scale_o(ex2(static_cast<float>(-up)));
     };
 
 #pragma unroll 1

@@ -107,12 +107,16 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
         const double half = B >= 4 ? busiest(0.5 * static_cast<double>(items) * n, per) : full;
         return 0.5 * (full + half) + (n > 1 ? 4.0 + 0.02 * static_cast<double>(n) : 0.0);
     };
-    int64_t best = 1;
-    double best_cost = cost(1, steps);
-    const int64_t most = std::min<int64_t>(steps, 512);
+    // Without HI the MMAs sum a block's keys, cutting off bits (see the kernel):
+    // 16384 keys are 1.2e-5 of the result, little against a 16-bit output's own
+    // rounding, and more are not taken.
+    const int64_t least = p->hi ? 1 : (steps + 255) / 256;
+    int64_t best = least;
+    double best_cost = cost(best, (steps + best - 1) / best);
+    const int64_t most = std::max(least, std::min<int64_t>(steps, 512));
     for (int i = 0; i < 18; ++i) {
         const int64_t s = i < 9 ? int64_t(2) << i : (i - 8) * sms / items;
-        if (s < 2 || s > most) continue;
+        if (s < 2 || s <= least || s > most) continue;
         const int64_t per = (steps + s - 1) / s, n = (steps + per - 1) / per;
         const double c = cost(n, per);
         if (n < best ? c <= best_cost * 1.03 : c < best_cost * 0.97) {
