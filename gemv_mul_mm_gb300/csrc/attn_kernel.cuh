@@ -423,7 +423,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 
     // Weights are 2^(score - ref) <= 2^kTop: f16 terms use the top of their
     // range. Before the first score, ref is kNone: every finite score exceeds it.
-    constexpr float kTop = BF ? 0.f : 14.f, kNone = -1e30f;
+    constexpr float kTop = BF ? 0.f : 14.f, kNone = -3e38f;
     float ref[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

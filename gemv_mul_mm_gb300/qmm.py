@@ -8,6 +8,7 @@ raises; there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -493,6 +494,11 @@ def qattn_decode_workspace_bytes(fmt, dtype, batch: int, n_q_heads: int, n_kv_he
     return _lib().qattn_decode_workspace_bytes(_fmt(fmt), _torch()[1][dtype], batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
 
 
+@functools.lru_cache(maxsize=4096)
+def _attn_workspace(device: int, *sizes) -> int:
+    return _lib().qattn_decode_workspace_bytes(*sizes)
+
+
 def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int, n_kv_heads: int,
                  scale: Optional[float] = None, window: int = 0, softcap: float = 0.0, max_len: Optional[int] = None,
                  out=None, return_lse: bool = False, workspace=None, stream=None):
@@ -527,7 +533,7 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     L, f = _lib(), _fmt(fmt)
     wptr = wn = 0
     if workspace is None:
-        wn = L.qattn_decode_workspace_bytes(f, dt, B, H, n_kv_heads, D, max_len, window)
+        wn = _attn_workspace(dev, f, dt, B, H, n_kv_heads, D, max_len, window)
         if wn:
             workspace = new((wn,), (1,), torch.uint8)
             wptr = workspace.data_ptr()
