@@ -482,9 +482,12 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                         for (int q = 0; q < NQ; ++q)
                             mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], qf[n][q][2 * c + j][0], qf[n][q][2 * c + j][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 4; i += 2) {
                         const float d = __half2float(kscale[i >> 1][c]);
-                        sx[n][i] = c == 0 ? d * acc[i] : fmaf(d, acc[i], sx[n][i]);
+                        const float2 x = fma2(make_float2(d, d), make_float2(acc[i], acc[i + 1]),
+                                              c == 0 ? make_float2(0.f, 0.f) : make_float2(sx[n][i], sx[n][i + 1]));
+                        sx[n][i] = x.x;
+                        sx[n][i + 1] = x.y;
                     }
                 }
             }
@@ -529,7 +532,9 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 }
         }
         auto rel = [&](int n, int i) {                // score - ref
-            return SLOW ? sx[n][i] - ref[n][i & 1] : fmaf(sx[n][i], sc[n][i & 1], -ref[n][i & 1]);
+            // not fused: ref is a rounded score, and against the exact product the
+            // rounding itself would be the difference once scores pass 2^24
+            return SLOW ? sx[n][i] - ref[n][i & 1] : __fmul_rn(sx[n][i], sc[n][i & 1]) - ref[n][i & 1];
         };
         float y[NT][4];
         bool grew = false;
@@ -598,7 +603,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 float alpha[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float mt = SLOW ? fmaxf(sx[n][k], sx[n][k + 2]) : fmaxf(sx[n][k] * sc[n][k], sx[n][k + 2] * sc[n][k]);
+                    float mt = SLOW ? fmaxf(sx[n][k], sx[n][k + 2]) : fmaxf(__fmul_rn(sx[n][k], sc[n][k]), __fmul_rn(sx[n][k + 2], sc[n][k]));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
@@ -668,7 +673,12 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 #pragma unroll
                     for (int q = NP - 1; q >= 0; --q) mma<BF>(d, f[0], f[1], f[2], f[3], p[q][0], p[q][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][j][i] = WIDE ? fmaf(d[i], down, o[n][j][i]) : o[n][j][i] + d[i];
+                    for (int i = 0; i < 4; i += 2) {
+                        const float2 x = fma2(make_float2(d[i], d[i + 1]), make_float2(down, down),
+                                              make_float2(o[n][j][i], o[n][j][i + 1]));
+                        o[n][j][i] = x.x;
+                        o[n][j][i + 1] = x.y;
+                    }
                 } else {
 #pragma unroll
                     for (int q = 0; q < NP; ++q) mma<BF>(o[n][j], f[0], f[1], f[2], f[3], p[q][0], p[q][1]);

@@ -92,7 +92,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     // takes 0.5 to 0.7 us for one, and q8_0 a quarter more for each block
     // missing from a full SM): the steps of the busiest SM, plus a block's
     // fixed part (8: query, first loads, warps joined), which further waves hide
-    // where memory and not instructions bound them (f16, bf16), plus the join. Candidates give every SM a whole number of
+    // where memory bounds them and a neighbour is resident, plus the join. Candidates give every SM a whole number of
     // blocks, or are powers of two. Lengths are known on the device only: a
     // batch is taken to be anything between its bound and half of it. A
     // smaller count wins within 3 %.
@@ -100,7 +100,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
         const double load = blocks / sms, waves = std::ceil(load / resident);
         const double idle = fmt == QMM_KV_Q8_0 && load < resident ? resident - std::ceil(load) : 0.0;
         return (load <= resident ? std::ceil(load) : load + 0.5) * (1.0 + 0.25 * idle) * static_cast<double>(per) + 8.0 +
-               (fmt == QMM_KV_Q8_0 ? 8.0 : 2.0) * (waves - 1);
+               (fmt == QMM_KV_Q8_0 || resident == 1 ? 8.0 : 2.0) * (waves - 1);
     };
     auto cost = [&](int64_t n, int64_t per) {
         const double full = busiest(static_cast<double>(items) * n, per);

@@ -22,18 +22,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     return r;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{.reg .b64 a, b, c, d;\n\t"
-        "mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, d;}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 // a / 127 rounded once, for 0 <= a < 2^128 away from subnormal quotients (which
 // f16 rounds to 0): the product with the rounded reciprocal, corrected once by
 // its exact remainder (Markstein's scheme).

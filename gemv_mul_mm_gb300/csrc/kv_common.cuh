@@ -94,6 +94,18 @@ __device__ __forceinline__ void div_mod(int64_t a, int b, int64_t& q, int& r) {
     }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // cos and sin of 2 pi frac(pos * turns / 2^64). The product wraps modulo 2^64,
 // which drops whole turns exactly, so the angle is as good at position 10^6 as
 // at 1 (an fp32 product pos * frequency is off by up to 4e-3 rad at 10^5). The

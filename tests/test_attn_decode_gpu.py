@@ -125,6 +125,26 @@ def test_many_sequences_are_not_split_below_their_need(Q):
     check(Q, problem(Q, "q8_0", "f16", 128, 2, 4, 16, [int(v) for v in np.random.RandomState(1).randint(0, 700, 150)], 4))
 
 
+@pytest.mark.parametrize("fmt,dt", [("f16", "f16"), ("q8_0", "f16"), ("bf16", "f32"), ("q8_0", "f32")])
+def test_one_long_sequence_among_many_short_ones(Q, fmt, dt):
+    """A batch large enough that nothing has to be split to fill the GPU: the
+    sums over a long sequence keep their accuracy all the same. Against the
+    result's 2-norm: 16-bit outputs their own rounding and the 2^-16 of the
+    weights, fp32 outputs the score error 2.5 delta of the derived tolerance,
+    of which a sum over many keys shows far less (2e-6)."""
+    lens = [1 + i % 3 for i in range(300)] + [40000]
+    p = problem(Q, fmt, dt, 64, 2, 2, 64, lens, 11)
+    out, _ = check(Q, p)
+    table = p["host"][0]
+    import torch
+    j = np.arange(lens[-1])
+    pg, row = torch.from_numpy(table[-1, j // 64].astype(np.int64)).cuda(), torch.from_numpy(j % 64).cuda()
+    K, V = (U.cache_values(fmt, c, 64, 2, 64)[pg, :, row] for c in (p["kc"], p["vc"]))
+    want = U.attend(p["q"][-1].double(), K, V, 0.125, 0.0, dt)[0]
+    rel = float((out[-1].double() - want).norm() / want.norm())
+    assert rel < (2e-6 if dt == "f32" else 2.0 ** -11 + 2.0 ** -16)
+
+
 def test_strided_query_and_explicit_scale(Q):
     import torch
     p = problem(Q, "f16", "f16", 64, 2, 2, 16, [50, 3], 8)
@@ -172,6 +192,22 @@ def test_keys_of_minus_infinity_are_masked_and_all_of_them_give_nan(Q):
     assert bool(((out[0].double() - want).abs() <= tol).all()) and bool(((lse[0].double() - wl).abs() <= ltol).all())
     assert bool(torch.isnan(out[1]).all()) and bool((lse[1] == -math.inf).all())
     assert Q.check_device_error() == 0
+
+
+def test_enormous_scores(Q):
+    """Scores near the ends of fp32's range: no reference value of the softmax
+    is mistaken for them."""
+    import torch
+    p = problem(Q, "bf16", "f32", 64, 1, 2, 16, [100], 3)
+    p["q"].mul_(1e34)
+    out, lse = call(Q, p, return_lse=True)
+    K, V = (U.cache_values("bf16", c, 16, 1, 64) for c in (p["kc"], p["vc"]))
+    j = np.arange(100)
+    pg, row = torch.from_numpy(p["host"][0][0, j // 16].astype(np.int64)).cuda(), torch.from_numpy(j % 16).cuda()
+    s = torch.einsum("hd,nd->hn", p["q"][0].double(), K[pg, 0, row]) * 0.125
+    best = s.argmax(-1)                                               # scores lie 1e33 apart: one key takes all
+    assert bool(((out[0].double() - V[pg, 0, row][best]).abs() <= 2.0 ** -22 * V[pg, 0, row][best].abs() + 1e-30).all())
+    assert bool(((lse[0].double() / s.amax(-1) - 1).abs() < 1e-5).all())
 
 
 def test_nan_in_one_sequence_stays_there(Q):
