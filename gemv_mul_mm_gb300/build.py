@@ -1,7 +1,8 @@
 """Builds libqmm.so in-tree with nvcc for sm_103a (no cmake).
 
 Each .cu translation unit compiles in parallel into an object, then one
-link step makes the shared library. Used by ``__graft_entry__.build()`` and
+link step makes the shared library. csrc/pycall.c, the CPython bindings of the
+serving operators, becomes the extension module _pycall.so. Used by ``__graft_entry__.build()`` and
 by the Python binding when the library is missing or stale.
 """
 from __future__ import annotations
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
+PYCALL_SRC = os.path.join(CSRC, "pycall.c")
+PYCALL = os.path.join(HERE, "_pycall.so")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -56,7 +60,25 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def build_pycall(force: bool = False) -> str:
+    deps = [PYCALL_SRC, os.path.join(ROOT, "include", "qmm.h")]
+    if not force and os.path.exists(PYCALL) and all(os.path.getmtime(f) <= os.path.getmtime(PYCALL) for f in deps):
+        return PYCALL
+    cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
+    if cc is None:
+        raise RuntimeError("no C compiler found")
+    tmp = PYCALL + ".tmp"
+    cmd = [cc, "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(ROOT, "include"), PYCALL_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for pycall.c:\n{r.stderr}")
+    os.replace(tmp, PYCALL)
+    return PYCALL
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_pycall(force)
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

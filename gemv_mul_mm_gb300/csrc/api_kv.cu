@@ -54,6 +54,30 @@ int check_cache(KvCache* c, int fmt, const void* k, const void* v, size_t cache_
     return QMM_OK;
 }
 
+// attn_plan on the current device. A thread's last plan is kept with its sizes:
+// a workspace query and its call, and the layers of one step, share it.
+int plan_for(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, AttnPlan* p) {
+    struct Key {
+        int64_t B;
+        int dev, fmt, dtype, Hq, Hkv, D, max_len, window;
+        bool operator==(const Key& o) const {
+            return B == o.B && dev == o.dev && fmt == o.fmt && dtype == o.dtype && Hq == o.Hq && Hkv == o.Hkv && D == o.D &&
+                   max_len == o.max_len && window == o.window;
+        }
+    };
+    static thread_local Key last{};      // B 0: none
+    static thread_local AttnPlan plan{};
+    Key k{B, 0, fmt, dtype, Hq, Hkv, D, max_len, window};
+    if (cudaGetDevice(&k.dev) != cudaSuccess) return QMM_ERR_CUDA;
+    if (!(k == last)) {
+        last.B = 0;
+        if (attn_plan(fmt, dtype, B, Hq, Hkv, D, max_len, window, sm_count(k.dev), &plan) != cudaSuccess) return QMM_ERR_CUDA;
+        last = k;
+    }
+    *p = plan;
+    return QMM_OK;
+}
+
 int done(cudaError_t e, int path) {
     if (e != cudaSuccess) return QMM_ERR_CUDA;
     set_last_path(path);
@@ -212,11 +236,8 @@ size_t qattn_decode_workspace_bytes(int fmt, int dtype, int64_t B, int n_q_heads
     if (B <= 0 || B > (1 << 24) || n_q_heads <= 0 || n_q_heads > 65536 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
         !attn_dim_ok(head_dim) || max_len <= 0 || max_len > (1 << 30) || window < 0)
         return 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     AttnPlan p;
-    if (attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev), &p) != cudaSuccess) return 0;
-    return p.ws_bytes;
+    return plan_for(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p) == QMM_OK ? p.ws_bytes : 0;
 }
 
 int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs, const void* k_cache,
@@ -248,11 +269,8 @@ int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs
         return QMM_ERR_ACTIVATIONS_TOO_SMALL;
     if (!fits(out_elems, B, static_cast<int64_t>(n_q_heads) * head_dim, n_q_heads, head_dim, head_dim))
         return QMM_ERR_OUTPUT_TOO_SMALL;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
     AttnPlan p;
-    if (attn_plan(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, sm_count(dev), &p) != cudaSuccess)
-        return QMM_ERR_CUDA;
+    if (int r = plan_for(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p)) return r;
     if (p.ws_bytes) {
         if (!workspace) return QMM_ERR_NULL_POINTER;
         if (workspace_bytes < p.ws_bytes) return QMM_ERR_WORKSPACE_TOO_SMALL;

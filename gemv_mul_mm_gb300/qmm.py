@@ -8,7 +8,6 @@ raises; there is no CPU path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 from typing import Optional
@@ -296,18 +295,21 @@ def qmoe_ffn(kind, W_gu, gu_stride: int, W_down, down_stride: int, n_experts: in
     return Y
 
 
-def _torch():
-    """What the serving operators' bindings use of torch, looked up once: a call
-    on a decode step costs about as much on the host as on the GPU.
-
-    (torch, element types, raw stream of a device, current device, new tensor).
-    The raw stream, the device and the allocation go around torch's Python and
+def _calls():
+    """The bindings in C of the operators below (csrc/pycall.c), with the entry
+    points of the loaded library and what they use of torch: element types, the
+    raw stream of a device, the current device, a new tensor, the error check.
+    The stream, the device and the allocation go around torch's Python and
     dispatcher layers where this torch has the direct functions (an allocation
     then takes 0.8 us instead of 2 to 6)."""
-    global _T
-    if _T is None:
+    global _CALL
+    if _CALL is None:
         import torch
-        dtypes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        L = _lib()
+        try:
+            from gemv_mul_mm_gb300 import _pycall
+        except ImportError as e:
+            raise ImportError("_pycall.so not built; run __graft_entry__.build() first") from e
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
             def raw(device):
@@ -317,71 +319,15 @@ def _torch():
         if new is None:
             def new(shape, strides, dtype):
                 return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
-        _T = (torch, dtypes, raw, current, new)
-    return _T
+        entry = tuple(ctypes.cast(f, _P).value for f in
+                      (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes))
+        _pycall.setup(entry, (torch.float32, torch.float16, torch.bfloat16), torch.int32, torch.int64, torch.uint8, raw, current,
+                      new, _check)
+        _CALL = _pycall
+    return _CALL
 
 
-_T = None
-
-
-def _device(X, what: str) -> int:
-    """Index of X's GPU, which must be the current one (kernels launch there)."""
-    dev = X.get_device()
-    if dev < 0:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if dev != _T[3]():
-        raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
-    return dev
-
-
-def _act(X, what: str) -> int:
-    """Element type of an f32 / f16 / bf16 tensor."""
-    dt = (_T or _torch())[1].get(X.dtype)
-    if dt is None:
-        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {X.dtype}")
-    return dt
-
-
-def _rows(X, what: str):
-    """(T, H, D, elements reachable, token stride, head stride) of a (T, H, D)
-    tensor whose last dimension is contiguous."""
-    shape, stride = X.shape, X.stride()
-    if len(shape) != 3:
-        raise ValueError(f"{what} must have three dimensions (tokens, heads, dim), got {tuple(shape)}")
-    T, H, D = shape
-    ts, hs, ds = stride
-    if ds != 1 and D > 1:
-        raise ValueError(f"{what}'s last dimension must be contiguous")
-    return T, H, D, (T - 1) * ts + (H - 1) * hs + D if T and H and D else 0, ts, hs
-
-
-def _want(X, dtype, n, what: str, dev: int) -> int:
-    """Address of a contiguous `dtype` tensor of `n` elements on GPU `dev`."""
-    if X.dtype is not dtype or not X.is_contiguous() or (n >= 0 and X.numel() != n):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n >= 0 else ""))
-    if X.get_device() != dev:
-        raise ValueError(f"{what} is on {X.device}, not on cuda:{dev}")
-    return X.data_ptr()
-
-
-def _on(X, dev: int, what: str):
-    if X.get_device() != dev:
-        raise ValueError(f"{what} is on {X.device}, not on cuda:{dev}")
-
-
-def _pages(k_cache, v_cache, dev: int):
-    """(pages, page stride, bytes) of a cache given as two (pages, bytes) uint8 tensors."""
-    shape, stride = k_cache.shape, k_cache.stride()
-    if len(shape) != 2 or stride[1] != 1 or k_cache.element_size() != 1:
-        raise ValueError("k_cache must be a (pages, bytes per page) uint8 tensor with contiguous pages")
-    if v_cache.shape != shape or v_cache.stride() != stride or v_cache.dtype is not k_cache.dtype:
-        raise ValueError("v_cache must have k_cache's shape, strides and type")
-    _on(k_cache, dev, "k_cache")
-    _on(v_cache, dev, "v_cache")
-    n, nbytes = shape
-    # one page alone has no stride to speak of
-    ps = stride[0] if n > 1 else nbytes
-    return n, ps, (n - 1) * ps + nbytes if n else 0
+_CALL = None
 
 
 def _fmt(fmt) -> int:
@@ -422,23 +368,7 @@ def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=No
     each head in pairs (i, i + rot/2) ("half") or (2i, 2i + 1)
     ("interleaved"). positions: int32 (T,); turns: qrope_turns. X may be a
     view; out=X rotates in place. Returns out (X's type)."""
-    torch, _, raw, _, new = _T or _torch()
-    dt = _act(X, "X")
-    T, H, D, n, ts, hs = _rows(X, "X")
-    dev = _device(X, "X")
-    pos = _want(positions, torch.int32, T, "positions", dev)
-    tur = _want(turns, torch.int64, -1, "turns", dev)
-    if out is None:
-        out = new((T, H, D), (H * D, D, 1), X.dtype)
-        on, ots, ohs = T * H * D, H * D, D
-    else:
-        if out.shape != X.shape or out.dtype != X.dtype:
-            raise ValueError("out must have X's shape and type")
-        _on(out, dev, "out")
-        _, _, _, on, ots, ohs = _rows(out, "out")
-    _check(_lib().qrope(X.data_ptr(), dt, n, ts, hs, pos, tur, 2 * turns.numel(), ROPE_LAYOUTS[layout], mscale,
-                        out.data_ptr(), on, ots, ohs, T, H, D, raw(dev) if stream is None else stream), "qrope")
-    return out
+    return (_CALL or _calls()).qrope(X, positions, turns, ROPE_LAYOUTS[layout], mscale, out, stream)
 
 
 def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None, turns=None, layout: str = "half",
@@ -447,56 +377,21 @@ def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None
     (T,); -1 skips a token) of a paged cache of format "f16", "bf16" or "q8_0",
     rotating K first when positions and turns are given. k_cache, v_cache:
     (pages, bytes per page) uint8 tensors (qkv_cache)."""
-    torch, _, raw, _, _ = _T or _torch()
-    dt = _act(K, "K")
-    if V.dtype != K.dtype or V.shape != K.shape:
-        raise ValueError("V must have K's shape and type")
-    T, H, D, kn, kts, khs = _rows(K, "K")
-    _, _, _, vn, vts, vhs = _rows(V, "V")
-    dev = _device(K, "K")
-    _on(V, dev, "V")
-    slot = _want(slots, torch.int64, T, "slots", dev)
-    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
-    if (positions is None) != (turns is None):
-        raise ValueError("positions and turns go together")
-    pos = tur = rot = 0
-    if positions is not None:
-        pos = _want(positions, torch.int32, T, "positions", dev)
-        tur = _want(turns, torch.int64, -1, "turns", dev)
-        rot = 2 * turns.numel()
-    _check(_lib().qkv_store(_fmt(fmt), K.data_ptr(), kn, kts, khs, V.data_ptr(), vn, vts, vhs, dt, slot, pos, tur, rot,
-                            ROPE_LAYOUTS[layout], mscale, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps,
-                            page_size, T, H, D, raw(dev) if stream is None else stream), "qkv_store")
+    (_CALL or _calls()).qkv_store(_fmt(fmt), K, V, slots, k_cache, v_cache, page_size, positions, turns, ROPE_LAYOUTS[layout],
+                                  mscale, stream)
 
 
 def qkv_load(fmt, slots, k_cache, v_cache, page_size: int, n_kv_heads: int, head_dim: int, dtype=None, stream=None):
     """The keys and values in `slots` (int64 (T,); -1 gives zeros) as two (T,
     n_kv_heads, head_dim) tensors of `dtype` (float32 by default)."""
-    torch, dtypes, raw, _, new = _T or _torch()
-    dt = F32 if dtype is None else dtypes.get(dtype)
-    if dt is None:
-        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-    dev = _device(k_cache, "k_cache")
-    T = slots.numel()
-    slot = _want(slots, torch.int64, T, "slots", dev)
-    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
-    shape, strides = (T, n_kv_heads, head_dim), (n_kv_heads * head_dim, head_dim, 1)
-    K = new(shape, strides, dtype or torch.float32)
-    V = new(shape, strides, dtype or torch.float32)
-    _check(_lib().qkv_load(_fmt(fmt), slot, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps, page_size,
-                           K.data_ptr(), V.data_ptr(), dt, T * n_kv_heads * head_dim, T, n_kv_heads, head_dim,
-                           raw(dev) if stream is None else stream), "qkv_load")
-    return K, V
+    return (_CALL or _calls()).qkv_load(_fmt(fmt), slots, k_cache, v_cache, page_size, n_kv_heads, head_dim, dtype, stream)
 
 
 def qattn_decode_workspace_bytes(fmt, dtype, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
                                  window: int = 0) -> int:
-    return _lib().qattn_decode_workspace_bytes(_fmt(fmt), _torch()[1][dtype], batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
-
-
-@functools.lru_cache(maxsize=4096)
-def _attn_workspace(device: int, *sizes) -> int:
-    return _lib().qattn_decode_workspace_bytes(*sizes)
+    import torch
+    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dtype]
+    return _lib().qattn_decode_workspace_bytes(_fmt(fmt), dt, batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
 
 
 def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int, n_kv_heads: int,
@@ -510,42 +405,8 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
     uint8 tensor of qattn_decode_workspace_bytes(...)), allocated here with
     torch if None."""
-    torch, _, raw, _, new = _T or _torch()
-    dt = _act(q, "q")
-    B, H, D, qn, qbs, qhs = _rows(q, "q")
-    dev = _device(q, "q")
-    n_pages, ps, nbytes = _pages(k_cache, v_cache, dev)
-    tshape = block_table.shape
-    if block_table.dtype is not torch.int32 or len(tshape) != 2 or tshape[0] != B or \
-            (tshape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be an int32 tensor (sequences, pages) with contiguous rows")
-    _on(block_table, dev, "block_table")
-    lens = _want(seq_lens, torch.int32, B, "seq_lens", dev)
-    width, ts = tshape[1], block_table.stride(0)
-    if max_len is None:
-        max_len = width * page_size
-    if out is None:
-        out = new((B, H, D), (H * D, D, 1), q.dtype)
-        optr = out.data_ptr()
-    else:
-        optr = _want(out, q.dtype, B * H * D, "out", dev)
-    lse = new((B, H), (H, 1), torch.float32) if return_lse else None
-    L, f = _lib(), _fmt(fmt)
-    wptr = wn = 0
-    if workspace is None:
-        wn = _attn_workspace(dev, f, dt, B, H, n_kv_heads, D, max_len, window)
-        if wn:
-            workspace = new((wn,), (1,), torch.uint8)
-            wptr = workspace.data_ptr()
-    else:
-        _on(workspace, dev, "workspace")
-        wptr, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(L.qattn_decode(f, q.data_ptr(), dt, qn, qbs, qhs, k_cache.data_ptr(), v_cache.data_ptr(), nbytes, n_pages, ps,
-                          page_size, block_table.data_ptr(), (B - 1) * ts + width if B else 0, ts, width, lens, max_len,
-                          B, H, n_kv_heads, D, D ** -0.5 if scale is None else scale, window, softcap, optr, B * H * D,
-                          lse.data_ptr() if return_lse else 0, wptr, wn, raw(dev) if stream is None else stream),
-           "qattn_decode")
-    return (out, lse) if return_lse else out
+    return (_CALL or _calls()).qattn_decode(_fmt(fmt), q, k_cache, v_cache, block_table, seq_lens, page_size, n_kv_heads, scale,
+                                            window, softcap, max_len, out, return_lse, workspace, stream)
 
 
 def selftest_wait_timeout(cycles: int, stream=None):

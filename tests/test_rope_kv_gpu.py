@@ -245,6 +245,31 @@ def test_offsets_past_32_bits(Q):
     assert Q.check_device_error() == 0
 
 
+def test_binding_refuses_and_stays_usable(Q):
+    import torch
+    x = randn((4, 2, 64), "f16", 1)
+    pos, turns = torch.zeros(4, dtype=torch.int32, device="cuda"), turns_of(freqs(64))
+    kc, vc = Q.qkv_cache("f16", 2, 16, 2, 64)
+    slots = torch.arange(4, device="cuda")
+    for call, kind in (
+            (lambda: Q.qrope(x.double(), pos, turns), TypeError), (lambda: Q.qrope("x", pos, turns), TypeError),
+            (lambda: Q.qrope(x, pos.cpu(), turns), ValueError), (lambda: Q.qrope(x, pos[::2], turns), ValueError),
+            (lambda: Q.qrope(x, pos, turns.int()), ValueError), (lambda: Q.qrope(x, pos, turns, out=x.float()), ValueError),
+            (lambda: Q.qrope(x, pos, turns, layout="other"), KeyError), (lambda: Q.qrope(x, pos, turns, mscale="a"), TypeError),
+            (lambda: Q.qkv_store("f16", x, x, slots, kc, vc.cpu(), 16), ValueError),
+            (lambda: Q.qkv_store("f16", x, x, slots, kc, vc, 1 << 40), OverflowError),
+            (lambda: Q.qkv_load("f16", slots, kc, vc, 16, 2, 64, dtype=torch.int32), TypeError),
+            (lambda: Q.qkv_load("f16", slots, kc, vc, 16, -2, 64), ValueError),
+            (lambda: Q.qattn_decode("f16", x, kc, vc, torch.zeros((4, 1), dtype=torch.int32, device="cuda"), pos, 16, 2,
+                                    workspace=pos), ValueError)):
+        with pytest.raises(kind):
+            call()
+    with pytest.raises(Q.QmmError) as e:
+        Q.qkv_load("q8_0", slots, kc, vc, 16, 2, 80)
+    assert e.value.name == "QMM_ERR_COLS_NOT_BLOCK_ALIGNED"
+    assert torch.equal(Q.qrope(x, pos, turns), x)                     # position 0: no rotation
+
+
 def test_on_another_stream_and_in_a_graph(Q):
     import torch
     x = randn((9, 4, 64), "f16", 4)
