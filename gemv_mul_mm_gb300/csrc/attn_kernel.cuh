@@ -232,7 +232,8 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sm_q[8 * NT][D + 4];
     __shared__ float sm_m[kWarps][8 * NT], sm_l[kWarps][8 * NT], sm_scale[8 * NT];
-    __shared__ float sm_qsum[8 * NT][Q8 ? C : 1];
+    __shared__ __align__(8) float sm_qsum[Q8 ? C : 1][8 * NT];
+    __shared__ uint2 sm_qf[Q8 ? NT * NQ * MT : 1][32];
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     // block -> (sequence, key-value head, chunk of its query heads, split)
@@ -390,36 +391,46 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (i % 4 == 0) sm_qsum[h][c] = sum * -7.62939453125e-06f;
+            if (i % 4 == 0) sm_qsum[c][h] = sum * -7.62939453125e-06f;
         }
         __syncthreads();
     }
-    unsigned qf[NT][NQ][MT][2];
-    float qb[NT][Q8 ? C : 1][2];                      // of heads 2t, 2t + 1
+    // The fragments stay in registers, or with Q8_0, whose registers decide how
+    // many blocks fit an SM, in shared memory, where the block's warps share them.
+    uint2 qf[Q8 ? 1 : NT][Q8 ? 1 : NQ][Q8 ? 1 : MT];
     float sc[NT][2];                                  // score scale of heads 2t, 2t + 1, to log2 units unless capped
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const float f = NORM ? sm_scale[8 * n + g] : 1.f;
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+        for (int j = 0; j < MT; ++j) {
+            if (Q8 && j % kWarps != warp) continue;
+            unsigned w[NQ][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 // dims 2t, 2t + 1 (+ 8) of the 16, or with Q8_0 4t, 4t + 2 (+ 1)
                 const int d = 16 * j + (Q8 ? 4 * t + k : 2 * t + 8 * k);
                 float x0 = sm_q[8 * n + g][d] * f, x1 = sm_q[8 * n + g][d + (Q8 ? 2 : 1)] * f;
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) qf[n][q][j][k] = take16<BF>(x0, x1);
+                for (int q = 0; q < NQ; ++q) w[q][k] = take16<BF>(x0, x1);
             }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                if constexpr (Q8) sm_qf[(n * NQ + q) * MT + j][lane] = make_uint2(w[q][0], w[q][1]);
+                else qf[n][q][j] = make_uint2(w[q][0], w[q][1]);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             sc[n][k] = a.scale * (Q8 ? 16777216.f : 1.f) * (a.softcap > 0.f ? 1.f : kLog2e);
             if (NORM) sc[n][k] /= sm_scale[8 * n + 2 * t + k];
-            if constexpr (Q8) {
-#pragma unroll
-                for (int c = 0; c < C; ++c) qb[n][c][k] = sm_qsum[8 * n + 2 * t + k][c];
-            }
         }
     }
+    if constexpr (Q8) __syncthreads();
+    auto q_frag = [&](int n, int q, int j) {
+        if constexpr (Q8) return sm_qf[(n * NQ + q) * MT + j][lane];
+        else return qf[n][q][j];
+    };
 
     // Weights are 2^(score - ref) <= 2^kTop: f16 terms use the top of their
     // range. Before the first score, ref is kNone: every finite score exceeds it.
@@ -475,12 +486,15 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float acc[4] = {qb[n][c][0], qb[n][c][1], qb[n][c][0], qb[n][c][1]};
+                    const float2 qb = *reinterpret_cast<const float2*>(&sm_qsum[c][8 * n + 2 * t]);
+                    float acc[4] = {qb.x, qb.y, qb.x, qb.y};
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], qf[n][q][2 * c + j][0], qf[n][q][2 * c + j][1]);
+                        for (int q = 0; q < NQ; ++q) {
+                            const uint2 f = q_frag(n, q, 2 * c + j);
+                            mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], f.x, f.y);
+                        }
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
                         const float d = __half2float(kscale[i >> 1][c]);
@@ -506,7 +520,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) mma<BF>(acc[n][q], x[0], x[1], x[2], x[3], qf[n][q][j][0], qf[n][q][j][1]);
+                    for (int q = 0; q < NQ; ++q) mma<BF>(acc[n][q], x[0], x[1], x[2], x[3], q_frag(n, q, j).x, q_frag(n, q, j).y);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)

@@ -484,8 +484,9 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * The new token's own key is in the cache already (qkv_store first). Position
  * j is row j % page_size of page block_table[b][j / page_size]. A sequence of
  * length 0 gives zeros and lse = -inf. Whatever the cache holds outside the
- * range, NaN included, has no effect. Long sequences are split over the GPU
- * and joined in a fixed order: results are deterministic. Accumulation,
+ * range, NaN included, has no effect; an Inf or NaN inside it makes the heads
+ * that see it Inf or NaN. Long sequences are split over the GPU and joined in a
+ * fixed order: results are deterministic. Accumulation,
  * softmax and joins are fp32; with fp32 q the result is fp32-accurate, 16-bit
  * outputs are rounded once.
  *
