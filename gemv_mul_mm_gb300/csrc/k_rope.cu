@@ -8,7 +8,7 @@
 // Bound by reading X and writing Y. An item is two vectors of N elements of one
 // head (half layout: N elements of the first half and their partners;
 // interleaved: 2 N consecutive ones; past rot: up to 2 N copied). A block takes
-// a few tokens and up to four items a thread; it loads them all, computes each
+// a few tokens and one to four items a thread; it loads them all, computes each
 // (token, pair)'s cos and sin once into shared memory meanwhile (a thread that
 // computed its own spent as many instructions on them as on four heads), and
 // then rotates and stores.
@@ -20,7 +20,6 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;        // items per thread, loads in flight together
 constexpr int kAngles = 1024;    // (token, pair)s per block
 
 struct RopeShape {
@@ -30,7 +29,7 @@ struct RopeShape {
     int head_groups;
 };
 
-template <typename T, int N>
+template <typename T, int N, int ITEMS>
 __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeShape g) {
     grid_dep_launch();
     grid_dep_wait();
@@ -42,12 +41,12 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     const int pairs = a.rot / 2;
     const bool half = a.layout == QMM_ROPE_HALF;
 
-    Vec<T, N> v0[kItems], v1[kItems];
-    int unit[kItems], tok[kItems];
-    int64_t off_x[kItems], off_y[kItems];
+    Vec<T, N> v0[ITEMS], v1[ITEMS];
+    int unit[ITEMS], tok[ITEMS];
+    int64_t off_x[ITEMS], off_y[ITEMS];
     // item = (token, head, unit), units innermost; a thread's items are 256 apart
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
         const unsigned i = threadIdx.x + k * kThreads, th = i / static_cast<unsigned>(g.units);
         unit[k] = static_cast<int>(i - th * g.units);
         tok[k] = static_cast<int>(th / static_cast<unsigned>(heads));
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
         if (tok[k] >= tokens) break;
         const bool turn = unit[k] < g.rot_units;
         if (turn) {
@@ -121,18 +120,23 @@ template <typename T, int N> cudaError_t run(const RopeArgs& a, cudaStream_t s) 
     RopeShape g;
     g.rot_units = a.rot / (2 * N);
     g.units = g.rot_units + (in_place ? 0 : static_cast<int>((a.D - a.rot + 2 * N - 1) / (2 * N)));
-    // A block's items: four a thread where that leaves a block per SM, else one
+    // Items per thread, whose loads are in flight together: four where that still
+    // leaves twelve blocks per SM (four waves), two down to two blocks per SM, one
+    // below
     int dev = 0;
     cudaGetDevice(&dev);
-    const int64_t all = a.T * a.H * g.units;
-    const int items = all >= static_cast<int64_t>(sm_count(dev)) * kItems * kThreads ? kItems * kThreads : kThreads;
+    const int64_t per_sm = a.T * a.H * g.units / (static_cast<int64_t>(sm_count(dev)) * kThreads);
+    const int per_thread = per_sm >= 48 ? 4 : per_sm >= 4 ? 2 : 1;
+    const int items = per_thread * kThreads;
     g.heads = static_cast<int>(std::min<int64_t>(a.H, std::max(1, items / g.units)));
     g.head_groups = static_cast<int>((a.H + g.heads - 1) / g.heads);
-    // (units is at most 1024: one head always fits)
+    // (a head of more units than that, up to 1024, has a block of its own below)
     g.tokens = std::max(1, std::min(items / (g.heads * g.units), kAngles / (a.rot / 2)));
     const int64_t blocks = (a.T + g.tokens - 1) / g.tokens * g.head_groups;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_chained(k_rope<T, N>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, s, a, g);
+    auto go = [&](auto kernel) { return launch_chained(kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, s, a, g); };
+    const int need = g.tokens * g.heads * g.units;
+    return need <= kThreads ? go(k_rope<T, N, 1>) : need <= 2 * kThreads ? go(k_rope<T, N, 2>) : go(k_rope<T, N, 4>);
 }
 
 template <typename T> cudaError_t pick(const RopeArgs& a, cudaStream_t s) {
