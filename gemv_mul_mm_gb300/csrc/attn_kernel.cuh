@@ -256,6 +256,14 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         const int j = i * kThreads + threadIdx.x, h = j / D, d = j % D;
         qv[i] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
     }
+    // and the pages of this warp's first tiles, as they are without a window
+    const int32_t* table = a.table + b * a.table_stride;
+    int first_page[STAGES];
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+        const int64_t key = static_cast<int64_t>(split) * chunk + (warp + i * kWarps) * Lay::KT;
+        first_page[i] = table[imin64(key >> a.c.page_shift, a.table_width - 1)];
+    }
     const Range rg = range_of(a, b, chunk);
     if (rg.splits == 0) {                             // nothing to attend to (or a bad length)
         if (split == 0) {
@@ -271,7 +279,6 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     const int begin = rg.lo16 + split * chunk, end = min(begin + chunk, rg.len);
     const int shift = a.c.page_shift, page_mask = (1 << shift) - 1;
     const int page_lo = rg.lo >> shift, page_hi = (rg.len - 1) >> shift;
-    const int32_t* table = a.table + b * a.table_stride;
     const int64_t unit = a.c.unit();
     const uint8_t* kbase = a.c.k + kh * unit;
     const int64_t v_minus_k = a.c.v - a.c.k;
@@ -342,13 +349,16 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     int base = begin + warp * KT;
     int id[2];                                        // pages of the next tile to load
     int ahead = base;                                 // its first key
-    page_ids(ahead, id);
+    const bool known = rg.lo16 == 0 && !small_pages;
+    if (known) id[0] = first_page[0];
+    else page_ids(ahead, id);
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
         if (ahead < end) {
             load_tile(ahead, id, ring + i * Lay::STAGE);
             ahead += stride;
-            page_ids(ahead, id);
+            if (known) id[0] = first_page[i + 1];
+            else page_ids(ahead, id);
         }
         copies_commit();
     }

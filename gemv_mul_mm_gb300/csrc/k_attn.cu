@@ -20,41 +20,44 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     const Range r = range_of(a, bh / a.Hq, chunk);
     if (r.splits <= 1) return;
     __shared__ float sm[kJoinThreads * 4];
-    __shared__ float sl[kJoinThreads];
+    __shared__ float sm_m[kJoinThreads], sm_l[kJoinThreads];
     const int D = a.c.D, per = D / 4, groups = kJoinThreads / per;
     const int grp = threadIdx.x / per, v = threadIdx.x % per;
     const float2* ml = ws_ml(a, splits, bh, 0);
-    float m = -INFINITY;
-    for (int s = threadIdx.x % 32; s < r.splits; s += 32) m = fmaxf(m, ml[s].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
     if (grp < groups) {
         const float4* O = reinterpret_cast<const float4*>(ws_o(a, splits, bh, 0)) + v;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.f;
 #pragma unroll 4
         for (int s = grp; s < r.splits; s += groups) {
             const float2 p = ml[s];
             const float4 x = O[static_cast<int64_t>(s) * per];
-            const float f = p.x == -INFINITY ? 0.f : ex2(p.x - m);
-            l += p.y == 0.f ? 0.f : f * p.y;
-            acc.x = fmaf(f, x.x, acc.x);
-            acc.y = fmaf(f, x.y, acc.y);
-            acc.z = fmaf(f, x.z, acc.z);
-            acc.w = fmaf(f, x.w, acc.w);
+            const float top = fmaxf(m, p.x);
+            const float old = m == -INFINITY ? 0.f : ex2(m - top), f = p.x == -INFINITY ? 0.f : ex2(p.x - top);
+            m = top;
+            l = l * old + (p.y == 0.f ? 0.f : f * p.y);
+            acc.x = fmaf(f, x.x, acc.x * old);
+            acc.y = fmaf(f, x.y, acc.y * old);
+            acc.z = fmaf(f, x.z, acc.z * old);
+            acc.w = fmaf(f, x.w, acc.w * old);
         }
         reinterpret_cast<float4*>(sm)[grp * per + v] = acc;
-        if (v == 0) sl[grp] = l;
+        if (v == 0) {
+            sm_m[grp] = m;
+            sm_l[grp] = l;
+        }
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kJoinThreads) {
-        float o = 0.f, ll = 0.f;
+        float m = -INFINITY, o = 0.f, l = 0.f;
+        for (int i = 0; i < groups; ++i) m = fmaxf(m, sm_m[i]);
         for (int i = 0; i < groups; ++i) {
-            o += sm[i * D + d];
-            ll += sl[i];
+            const float f = sm_m[i] == -INFINITY ? 0.f : ex2(sm_m[i] - m);
+            o = fmaf(f, sm[i * D + d], o);
+            l += sm_l[i] == 0.f ? 0.f : f * sm_l[i];
         }
-        store_act(a.out, a.dtype, bh * D + d, o / ll);
-        if (a.lse && d == 0) a.lse[bh] = m * kLn2 + logf(ll);
+        store_act(a.out, a.dtype, bh * D + d, o / l);
+        if (a.lse && d == 0) a.lse[bh] = m * kLn2 + logf(l);
     }
 }
 
