@@ -28,7 +28,8 @@ static PyObject *dt_act[3];               /* torch.float32, float16, bfloat16: q
 static PyObject *dt_i32, *dt_i64, *dt_u8;
 static PyObject *fn_stream;               /* device index -> raw stream */
 static PyObject *fn_device;               /* () -> current device index */
-static PyObject *fn_new;                  /* (shape, strides, dtype) -> tensor on the current device */
+static PyObject *fn_new;                  /* (shape, strides, dtype) -> tensor on the current device and stream */
+static PyObject *fn_new_on;               /* (shape, strides, dtype, stream) -> tensor of that stream */
 static PyObject *fn_check;                /* (status, name) -> raises */
 static PyObject *s_data_ptr, *s_shape, *s_stride, *s_dtype, *s_get_device;
 
@@ -40,10 +41,10 @@ static int set_ref(PyObject **to, PyObject *o) {
 
 static PyObject *setup(PyObject *self, PyObject *args) {
     unsigned long long a[5];
-    PyObject *o[10];
+    PyObject *o[11];
     (void)self;
-    if (!PyArg_ParseTuple(args, "(KKKKK)(OOO)OOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &o[0], &o[1], &o[2], &o[3], &o[4],
-                          &o[5], &o[6], &o[7], &o[8], &o[9]))
+    if (!PyArg_ParseTuple(args, "(KKKKK)(OOO)OOOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &o[0], &o[1], &o[2], &o[3], &o[4],
+                          &o[5], &o[6], &o[7], &o[8], &o[9], &o[10]))
         return NULL;
     f_qrope = (__typeof__(f_qrope))(uintptr_t)a[0];
     f_qkv_store = (__typeof__(f_qkv_store))(uintptr_t)a[1];
@@ -57,7 +58,8 @@ static PyObject *setup(PyObject *self, PyObject *args) {
     set_ref(&fn_stream, o[6]);
     set_ref(&fn_device, o[7]);
     set_ref(&fn_new, o[8]);
-    set_ref(&fn_check, o[9]);
+    set_ref(&fn_new_on, o[9]);
+    set_ref(&fn_check, o[10]);
     Py_RETURN_NONE;
 }
 
@@ -216,13 +218,42 @@ static int read_cache(PyObject *ko, PyObject *vo, Cache *c) {
     return 0;
 }
 
+/* The stream of a call: the caller's handle, or the current one of `dev`. New
+ * tensors come from the pool of the stream that uses them: one of the current
+ * stream's could still be in use there, and a workspace would be handed out
+ * again there while the kernels of the other stream run. */
+typedef struct {
+    void *handle;
+    int other;                            /* not the current stream */
+} Stream;
+
+static int stream_of(PyObject *o, int dev, Stream *s) {
+    PyObject *d = PyLong_FromLong(dev);
+    if (!d) return -1;
+    PyObject *r = PyObject_CallOneArg(fn_stream, d);
+    Py_DECREF(d);
+    if (!r) return -1;
+    s->handle = PyLong_AsVoidPtr(r);
+    s->other = 0;
+    Py_DECREF(r);
+    if (o != Py_None && !PyErr_Occurred()) {
+        r = PyNumber_Long(o);
+        if (!r) return -1;
+        void *given = PyLong_AsVoidPtr(r);
+        Py_DECREF(r);
+        s->other = given != s->handle;
+        s->handle = given;
+    }
+    return PyErr_Occurred() ? -1 : 0;
+}
+
 /* A new contiguous tensor; *ptr its address. */
-static PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, void **ptr) {
+static PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, const Stream *s, void **ptr) {
     PyObject *sh = PyTuple_New(nd), *st = PyTuple_New(nd), *t = NULL, *p;
-    int64_t s = 1;
+    int64_t n = 1;
     if (!sh || !st) goto out;
     for (int i = nd - 1; i >= 0; --i) {
-        PyObject *a = PyLong_FromLongLong(shape[i]), *b = PyLong_FromLongLong(s);
+        PyObject *a = PyLong_FromLongLong(shape[i]), *b = PyLong_FromLongLong(n);
         if (!a || !b) {
             Py_XDECREF(a);
             Py_XDECREF(b);
@@ -230,9 +261,11 @@ static PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, void 
         }
         PyTuple_SET_ITEM(sh, i, a);
         PyTuple_SET_ITEM(st, i, b);
-        s *= shape[i] > 1 ? shape[i] : 1;
+        n *= shape[i] > 1 ? shape[i] : 1;
     }
-    {
+    if (s->other) {
+        t = PyObject_CallFunction(fn_new_on, "OOOK", sh, st, dtype, (unsigned long long)(uintptr_t)s->handle);
+    } else {
         PyObject *args[3] = {sh, st, dtype};
         t = PyObject_Vectorcall(fn_new, args, 3, NULL);
     }
@@ -249,23 +282,6 @@ out:
     Py_XDECREF(sh);
     Py_XDECREF(st);
     return t;
-}
-
-/* The stream: the caller's handle, or the current one of `dev`. */
-static int stream_of(PyObject *o, int dev, void **s) {
-    PyObject *r;
-    if (o == Py_None) {
-        PyObject *d = PyLong_FromLong(dev);
-        if (!d) return -1;
-        r = PyObject_CallOneArg(fn_stream, d);
-        Py_DECREF(d);
-    } else {
-        r = PyNumber_Long(o);
-    }
-    if (!r) return -1;
-    *s = PyLong_AsVoidPtr(r);
-    Py_DECREF(r);
-    return PyErr_Occurred() ? -1 : 0;
 }
 
 /* Raises for a status other than QMM_OK. */
@@ -299,7 +315,7 @@ static int nargs_are(Py_ssize_t n, Py_ssize_t want_n, const char *name) {
 static PyObject *py_qrope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Ten x, pos, turns, y;
     size_t xn, yn;
-    void *stream;
+    Stream stream;
     PyObject *out = a[5];
     (void)self;
     if (!nargs_are(n, 7, "qrope") || read_tensor(a[0], &x, "X")) return NULL;
@@ -311,7 +327,7 @@ static PyObject *py_qrope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const float mscale = (float)PyFloat_AsDouble(a[4]);
     if (PyErr_Occurred() || stream_of(a[6], x.dev, &stream)) return NULL;
     if (out == Py_None) {
-        out = new_tensor(3, x.shape, x.dtype, &y.ptr);
+        out = new_tensor(3, x.shape, x.dtype, &stream, &y.ptr);
         if (!out) return NULL;
         yn = (size_t)numel(&x);
         y.stride[0] = x.shape[1] * x.shape[2];
@@ -328,7 +344,7 @@ static PyObject *py_qrope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = f_qrope(x.ptr, dt, xn, x.stride[0], x.stride[1], pos.ptr, turns.ptr, (int)(2 * numel(&turns)), layout, mscale, y.ptr, yn,
-                 y.stride[0], y.stride[1], x.shape[0], x.shape[1], x.shape[2], stream);
+                 y.stride[0], y.stride[1], x.shape[0], x.shape[1], x.shape[2], stream.handle);
     Py_END_ALLOW_THREADS
     if (failed(rc, "qrope")) Py_CLEAR(out);
     return out;
@@ -339,7 +355,7 @@ static PyObject *py_qkv_store(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     Ten k, v, slots, pos, turns;
     Cache c;
     size_t kn, vn;
-    void *stream;
+    Stream stream;
     (void)self;
     if (!nargs_are(n, 12, "qkv_store") || read_tensor(a[1], &k, "K") || read_tensor(a[2], &v, "V")) return NULL;
     const int dt = act_of(k.dtype, "K");
@@ -369,7 +385,7 @@ static PyObject *py_qkv_store(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     Py_BEGIN_ALLOW_THREADS
     rc = f_qkv_store(fmt, k.ptr, kn, k.stride[0], k.stride[1], v.ptr, vn, v.stride[0], v.stride[1], dt, slots.ptr,
                      rope ? pos.ptr : NULL, rope ? turns.ptr : NULL, rope ? (int)(2 * numel(&turns)) : 0, layout, mscale, c.k, c.v,
-                     c.bytes, c.pages, c.stride, page, k.shape[0], (int)k.shape[1], (int)k.shape[2], stream);
+                     c.bytes, c.pages, c.stride, page, k.shape[0], (int)k.shape[1], (int)k.shape[2], stream.handle);
     Py_END_ALLOW_THREADS
     if (failed(rc, "qkv_store")) return NULL;
     Py_RETURN_NONE;
@@ -379,7 +395,8 @@ static PyObject *py_qkv_store(PyObject *self, PyObject *const *a, Py_ssize_t n) 
 static PyObject *py_qkv_load(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Ten slots;
     Cache c;
-    void *stream, *kp, *vp;
+    Stream stream;
+    void *kp, *vp;
     (void)self;
     if (!nargs_are(n, 9, "qkv_load") || read_cache(a[2], a[3], &c)) return NULL;
     PyObject *dtype = a[7] == Py_None ? dt_act[0] : a[7];
@@ -393,7 +410,7 @@ static PyObject *py_qkv_load(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, "n_kv_heads or head_dim out of range");
         return NULL;
     }
-    PyObject *k = new_tensor(3, shape, dtype, &kp), *v = k ? new_tensor(3, shape, dtype, &vp) : NULL;
+    PyObject *k = new_tensor(3, shape, dtype, &stream, &kp), *v = k ? new_tensor(3, shape, dtype, &stream, &vp) : NULL;
     if (!v) {
         Py_XDECREF(k);
         return NULL;
@@ -401,7 +418,7 @@ static PyObject *py_qkv_load(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = f_qkv_load(fmt, slots.ptr, c.k, c.v, c.bytes, c.pages, c.stride, page, kp, vp, dt, (size_t)(shape[0] * shape[1] * shape[2]),
-                    shape[0], (int)shape[1], (int)shape[2], stream);
+                    shape[0], (int)shape[1], (int)shape[2], stream.handle);
     Py_END_ALLOW_THREADS
     PyObject *r = failed(rc, "qkv_load") ? NULL : PyTuple_Pack(2, k, v);
     Py_DECREF(k);
@@ -415,7 +432,8 @@ static PyObject *py_qattn_decode(PyObject *self, PyObject *const *a, Py_ssize_t 
     Ten q, table, lens, t;
     Cache c;
     size_t qn;
-    void *stream, *optr, *lptr = NULL, *wptr = NULL;
+    Stream stream;
+    void *optr, *lptr = NULL, *wptr = NULL;
     PyObject *out = NULL, *lse = NULL, *ws = NULL, *r = NULL;
     (void)self;
     if (!nargs_are(n, 16, "qattn_decode") || read_tensor(a[1], &q, "q")) return NULL;
@@ -448,7 +466,7 @@ static PyObject *py_qattn_decode(PyObject *self, PyObject *const *a, Py_ssize_t 
         return NULL;
     }
     if (a[12] == Py_None) {
-        out = new_tensor(3, q.shape, q.dtype, &optr);
+        out = new_tensor(3, q.shape, q.dtype, &stream, &optr);
         if (!out) return NULL;
     } else {
         if (want(a[12], &t, q.dtype, B * H * D, q.dev, "out")) return NULL;
@@ -456,11 +474,11 @@ static PyObject *py_qattn_decode(PyObject *self, PyObject *const *a, Py_ssize_t 
         optr = t.ptr;
         Py_INCREF(out);
     }
-    if (with_lse && !(lse = new_tensor(2, q.shape, dt_act[0], &lptr))) goto done;
+    if (with_lse && !(lse = new_tensor(2, q.shape, dt_act[0], &stream, &lptr))) goto done;
     int64_t wn = 0;
     if (a[14] == Py_None) {
         wn = (int64_t)f_ws_bytes(fmt, dt, B, (int)H, kv, (int)D, (int)max_len, window);
-        if (wn && !(ws = new_tensor(1, &wn, dt_u8, &wptr))) goto done;
+        if (wn && !(ws = new_tensor(1, &wn, dt_u8, &stream, &wptr))) goto done;
     } else {
         if (read_tensor(a[14], &t, "workspace") || on(&t, q.dev, "workspace")) goto done;
         if (t.dtype != dt_u8 || !contiguous(&t)) {
@@ -475,7 +493,7 @@ static PyObject *py_qattn_decode(PyObject *self, PyObject *const *a, Py_ssize_t 
     rc = f_qattn_decode(fmt, q.ptr, dt, qn, q.stride[0], q.stride[1], c.k, c.v, c.bytes, c.pages, c.stride, page, table.ptr,
                         B ? (size_t)((B - 1) * table.stride[0] + width) : 0, table.stride[0], (int)width, lens.ptr, (int)max_len, B,
                         (int)H, kv, (int)D, a[8] == Py_None ? (float)(1.0 / __builtin_sqrt(D > 0 ? (double)D : 1.0)) : (float)scale,
-                        window, softcap, optr, (size_t)(B * H * D), lptr, wptr, (size_t)wn, stream);
+                        window, softcap, optr, (size_t)(B * H * D), lptr, wptr, (size_t)wn, stream.handle);
     Py_END_ALLOW_THREADS
     if (!failed(rc, "qattn_decode")) {
         if (with_lse) {

@@ -319,10 +319,16 @@ def _calls():
         if new is None:
             def new(shape, strides, dtype):
                 return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+        def new_on(shape, strides, dtype, handle):
+            other = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            with torch.cuda.stream(other):
+                return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
         entry = tuple(ctypes.cast(f, _P).value for f in
                       (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes))
         _pycall.setup(entry, (torch.float32, torch.float16, torch.bfloat16), torch.int32, torch.int64, torch.uint8, raw, current,
-                      new, _check)
+                      new, new_on, _check)
         _CALL = _pycall
     return _CALL
 

@@ -271,6 +271,29 @@ def test_streams_and_graphs(Q):
     assert Q.check_device_error() == 0
 
 
+def test_stream_given_by_handle_does_not_share_memory_with_the_current_one(Q):
+    """Outputs and workspaces of a call on another stream come from that
+    stream's memory: work on the current stream, which allocates and fills
+    blocks of the same sizes all the time, does not touch them."""
+    import torch
+    p = problem(Q, "f16", "f16", 128, 1, 8, 64, [30000, 300], 4)
+    want = call(Q, p)
+    need = Q.qattn_decode_workspace_bytes("f16", torch.float16, 2, 8, 1, 128, p["table"].shape[1] * 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(50):
+        got.append(call(Q, p, stream=side.cuda_stream))
+        for size in (need, want.numel() * 2):                         # what a freed block would be handed out to
+            torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    with torch.cuda.stream(side):                                     # and the default stream from another one
+        y = call(Q, p, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
 def test_back_to_back_calls_share_a_workspace_on_one_stream(Q):
     import torch
     p, r = (problem(Q, "f16", "f16", 128, 1, 8, 64, [n, 300], s) for n, s in ((9000, 1), (7000, 2)))
