@@ -162,7 +162,7 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, int64_t b, int chun
 }
 
 // Partial results in the workspace: O [B * Hq][splits][D], then (m, l) pairs
-// [B * Hq][splits]; m, the log2 of the unit of O and l.
+// [B * Hq][splits]; m, the score that O and l are relative to.
 __device__ __forceinline__ float* ws_o(const AttnArgs& a, int splits, int64_t bh, int s) {
     return static_cast<float*>(a.ws) + (bh * splits + s) * a.c.D;
 }
@@ -171,6 +171,14 @@ __device__ __forceinline__ float2* ws_ml(const AttnArgs& a, int splits, int64_t 
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Scores are kept in log2 units, scale and log2 e in one factor; capped ones in
+// natural units (the cap times log2 e, rounded, would scale all of them alike)
+// and their differences are multiplied by log2 e.
+__device__ __forceinline__ float unit_of(const AttnArgs& a) { return a.softcap > 0.f ? kLog2e : 1.f; }
+__device__ __forceinline__ float lse_of(const AttnArgs& a, float m, float l) {
+    return (a.softcap > 0.f ? m : m * kLn2) + logf(l);
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -279,8 +287,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     const int begin = rg.lo16 + split * chunk, end = min(begin + chunk, rg.len);
     const int shift = a.c.page_shift, page_mask = (1 << shift) - 1;
     const int page_lo = rg.lo >> shift, page_hi = (rg.len - 1) >> shift;
-    const int64_t unit = a.c.unit();
-    const uint8_t* kbase = a.c.k + kh * unit;
+    const uint8_t* kbase = a.c.k + kh * a.c.unit();
     const int64_t v_minus_k = a.c.v - a.c.k;
     bool bad = false;
 
@@ -445,6 +452,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     // Weights are 2^(score - ref) <= 2^kTop: f16 terms use the top of their
     // range. Before the first score, ref is kNone: every finite score exceeds it.
     constexpr float kTop = BF ? 0.f : 14.f, kNone = -3e38f;
+    const float unit = unit_of(a), top = a.softcap > 0.f ? kTop * kLn2 : kTop;
     float ref[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -542,23 +550,23 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 }
         }
 
-        // ---- scores, in log2 units
+        // ---- scores, less ref, in log2 units
         if constexpr (SLOW) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float x = sx[n][i] * sc[n][i & 1];
-                    if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x / a.softcap);
+                    if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
                     const int key = base + 8 * (i >> 1) + g;
                     if (key < rg.lo || key >= end) x = -INFINITY;
                     sx[n][i] = x;
                 }
         }
-        auto rel = [&](int n, int i) {                // score - ref
+        auto rel = [&](int n, int i) {
             // not fused: ref is a rounded score, and against the exact product the
             // rounding itself would be the difference once scores pass 2^24
-            return SLOW ? sx[n][i] - ref[n][i & 1] : __fmul_rn(sx[n][i], sc[n][i & 1]) - ref[n][i & 1];
+            return SLOW ? (sx[n][i] - ref[n][i & 1]) * unit : __fmul_rn(sx[n][i], sc[n][i & 1]) - ref[n][i & 1];
         };
         float y[NT][4];
         bool grew = false;
@@ -611,11 +619,11 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             float up = 1.f;                           // change of O's factor
             if constexpr (Q8) {
                 const unsigned w = as_u32(v_top);
-                const unsigned top = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
-                if (top > (as_u32(v_lim) & 0xffffu)) {
+                const unsigned big = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
+                if (big > (as_u32(v_lim) & 0xffffu)) {
                     // scales are below 2^(field - 14) by their exponent field;
                     // one step more, so that few tiles raise it again
-                    const int e = min(static_cast<int>(top >> 10) - 13, 16);
+                    const int e = min(static_cast<int>(big >> 10) - 13, 16);
                     const __half2 mul = __float2half2_rn(exp2f(static_cast<float>(max(-15, min(15, -e)))));
                     up = __low2float(mul) / __low2float(v_mul);
                     v_mul = mul;
@@ -631,8 +639,8 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    const float now = fmaxf(ref[n][k], mt - kTop);
-                    alpha[k] = ex2(ref[n][k] - now);
+                    const float now = fmaxf(ref[n][k], mt - top);
+                    alpha[k] = ex2((ref[n][k] - now) * unit);
                     ref[n][k] = now;
                     l[n][k] *= alpha[k];
                     alpha[k] *= up;
@@ -818,7 +826,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][h]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - mm);
+            const float f = sm_m[w][h] == -INFINITY ? 0.f : ex2((sm_m[w][h] - mm) * unit);
             ll += sm_l[w][h] == 0.f ? 0.f : f * sm_l[w][h];
             sm_m[w][h] = f;
         }
@@ -826,7 +834,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         if (h < nh) {
             const int64_t bh = b * a.Hq + h0 + h;
             if (rg.splits > 1) *ws_ml(a, splits, bh, split) = make_float2(mm, ll);
-            else if (a.lse) a.lse[bh] = mm * kLn2 + logf(ll);
+            else if (a.lse) a.lse[bh] = lse_of(a, mm, ll);
         }
     }
     __syncthreads();

@@ -10,7 +10,7 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s of one head of one sequence
+// o = sum_s e^(m_s - m) O_s / sum_s e^(m_s - m) l_s of one head of one sequence
 // per block, in split order within each of the block's lanes' groups
 // (deterministic). A group of D / 4 threads adds every GROUPS-th split.
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a, int splits, int chunk) {
@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     const int D = a.c.D, per = D / 4, groups = kJoinThreads / per;
     const int grp = threadIdx.x / per, v = threadIdx.x % per;
     const float2* ml = ws_ml(a, splits, bh, 0);
+    const float unit = unit_of(a);
     if (grp < groups) {
         const float4* O = reinterpret_cast<const float4*>(ws_o(a, splits, bh, 0)) + v;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
             const float2 p = ml[s];
             const float4 x = O[static_cast<int64_t>(s) * per];
             const float top = fmaxf(m, p.x);
-            const float old = m == -INFINITY ? 0.f : ex2(m - top), f = p.x == -INFINITY ? 0.f : ex2(p.x - top);
+            const float old = m == -INFINITY ? 0.f : ex2((m - top) * unit), f = p.x == -INFINITY ? 0.f : ex2((p.x - top) * unit);
             m = top;
             l = l * old + (p.y == 0.f ? 0.f : f * p.y);
             acc.x = fmaf(f, x.x, acc.x * old);
@@ -52,12 +53,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
         float m = -INFINITY, o = 0.f, l = 0.f;
         for (int i = 0; i < groups; ++i) m = fmaxf(m, sm_m[i]);
         for (int i = 0; i < groups; ++i) {
-            const float f = sm_m[i] == -INFINITY ? 0.f : ex2(sm_m[i] - m);
+            const float f = sm_m[i] == -INFINITY ? 0.f : ex2((sm_m[i] - m) * unit);
             o = fmaf(f, sm[i * D + d], o);
             l += sm_l[i] == 0.f ? 0.f : f * sm_l[i];
         }
         store_act(a.out, a.dtype, bh * D + d, o / l);
-        if (a.lse && d == 0) a.lse[bh] = m * kLn2 + logf(l);
+        if (a.lse && d == 0) a.lse[bh] = lse_of(a, m, l);
     }
 }
 
