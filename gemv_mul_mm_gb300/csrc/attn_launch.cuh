@@ -63,6 +63,7 @@ template <int FMT> cudaError_t launch_fmt(const Launch& l, int D, bool hi, int t
     case 64: return pick<FMT, 64>(l, hi, tiles);
     case 96: return pick<FMT, 96>(l, hi, tiles);
     case 128: return pick<FMT, 128>(l, hi, tiles);
+    case 192: return pick<FMT, 192>(l, hi, tiles);
     default: return pick<FMT, 256>(l, hi, tiles);
     }
 }

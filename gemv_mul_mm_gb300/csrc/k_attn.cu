@@ -73,12 +73,12 @@ cudaError_t launch_one(const Launch& l, int fmt, int D) {
 }  // namespace
 }  // namespace attn
 
-bool attn_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
+bool attn_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms, AttnPlan* p) {
     const int group = Hq / Hkv;
-    // Query heads per block: 16 halve the reads of a group of more than 8 (D = 256
-    // has no registers for them).
+    // Query heads per block: 16 halve the reads of a group of more than 8 (above
+    // dim 128 there are no registers for them).
     p->tiles = group > 8 && D <= 128 ? 2 : 1;
     p->head_chunks = (group + 8 * p->tiles - 1) / (8 * p->tiles);
     p->hi = attn::needs_hi(fmt, dtype);

@@ -15,7 +15,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int N = 8;
 
-
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

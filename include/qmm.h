@@ -503,7 +503,7 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  *   workspace    device scratch of the caller, 16-byte aligned, at least
  *                qattn_decode_workspace_bytes(...) bytes (may be NULL where
  *                that is 0); calls that overlap must not share it
- * head_dim is 64, 96, 128 or 256 (QMM_ERR_UNIMPLEMENTED otherwise).
+ * head_dim is 64, 96, 128, 192 or 256 (QMM_ERR_UNIMPLEMENTED otherwise).
  */
 QMM_API int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs,
                          const void* k_cache, const void* v_cache, size_t cache_bytes, int64_t n_pages,

@@ -90,6 +90,13 @@ def test_lengths_at_every_edge(Q, fmt, dt, D, Hkv, group, page):
     check(Q, problem(Q, fmt, dt, D, Hkv, group, page, EDGES, D + group))
 
 
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group,page,window", [(4, 16, 0), (11, 8, 0), (2, 32, 50)])
+def test_head_dim_192(Q, fmt, dt, group, page, window):
+    check(Q, problem(Q, fmt, dt, 192, 2, group, page, EDGES + [9000], group), window)
+
+
 @pytest.mark.parametrize("fmt,dt", [("f16", "f16"), ("bf16", "bf16"), ("q8_0", "f32")])
 @pytest.mark.parametrize("Hkv,group", [(1, 1), (3, 1), (5, 7), (2, 8), (1, 9), (2, 16), (1, 17), (1, 40)])
 def test_head_groups(Q, fmt, dt, Hkv, group):
