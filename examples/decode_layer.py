@@ -107,6 +107,7 @@ def run(steps=32, batch=4, fmt="q8_0", kind="Q4_0", **sizes):
     layer.prompt(x, lens)
     token = torch.randn((batch, layer.d_model), generator=gen, device="cuda").half()
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())   # the prompt and the token are still being made there
     with torch.cuda.stream(side):        # a first call outside the capture
         layer.step(token)
     torch.cuda.current_stream().wait_stream(side)
