@@ -100,8 +100,10 @@ class AttentionLayer:
 def run(steps=32, batch=4, fmt="q8_0", kind="Q4_0", **sizes):
     """(relative error of the last step against plain_step, microseconds per step)."""
     layer = AttentionLayer(kind, fmt, batch=batch, **sizes)
-    gen = torch.Generator(device="cuda").manual_seed(3)
     prompt = 200 if layer.max_len > 400 else layer.max_len // 4
+    if prompt < 1 or steps < 1 or prompt + 1 + steps > layer.max_len:   # a step of its own comes before the replayed ones
+        raise ValueError(f"prompts of up to {prompt} tokens and 1 + {steps} steps do not fit {layer.max_len} tokens")
+    gen = torch.Generator(device="cuda").manual_seed(3)
     x = torch.randn((batch, prompt, layer.d_model), generator=gen, device="cuda").half()
     lens = torch.randint(1, prompt + 1, (batch,), generator=gen, device="cuda", dtype=torch.int32)
     layer.prompt(x, lens)

@@ -100,3 +100,16 @@ def test_the_first_step_waits_for_what_it_reads(example):
     made = max(i for i, e in enumerate(log[:first]) if e[1] == "main")   # prompt, token, lengths
     assert ("wait for main", "side") in log[made:first]
     assert ("wait for side", "main") in log[first:log.index(("step", "main"))]   # and the capture for the step
+
+
+@pytest.mark.parametrize("steps,sizes", [(824, {}), (100, dict(max_len=128)), (1, dict(max_len=3)), (0, {}), (-1, {})])
+def test_steps_past_the_cache_are_refused(example, steps, sizes):
+    """Positions beyond the page table would index it out of range."""
+    with pytest.raises(ValueError):
+        example.run(steps=steps, **sizes)
+    assert not any(e[0] in ("prompt", "step", "replay") for e in example.rec.log)
+
+
+def test_steps_up_to_the_cache_run(example):
+    example.run(steps=823)
+    assert sum(e[0] == "replay" for e in example.rec.log) == 823
