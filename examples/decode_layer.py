@@ -5,8 +5,8 @@ cache write, attention of the new tokens, output projection.
     python examples/decode_layer.py [--steps 32] [--batch 4] [--fmt q8_0] [--kind Q4_0]
 
 runs a batch of sequences of different lengths for some steps, replaying one
-CUDA graph per step, checks the last step against a plain 64-bit computation,
-and prints the time of a step.
+CUDA graph per step, checks the cache and the last step against a plain 64-bit
+computation, and prints the time of a step.
 """
 from __future__ import annotations
 
@@ -76,17 +76,46 @@ class AttentionLayer:
         return qmm.qgemm(self.kind, self.w_out, o.view(self.batch, -1), self.d_model, self.q_heads * self.dim, self.batch,
                          weights_const=True)
 
+    def plain_heads(self, x):
+        """heads(x) of x (n, d_model) in 64 bits from the weights, rounded to f16 as there."""
+        w = qmm.qdequant(self.kind, self.w_qkv, self.rows, self.d_model).double()
+        y = (x.double() @ w.T).half().double().view(x.shape[0], -1, self.dim)
+        h, k = self.q_heads, self.kv_heads
+        return y[:, :h], y[:, h:h + k], y[:, h + k:]
+
+    def plain_rotation(self, x, positions):
+        """x (n, heads, dim) rotated at positions (n,), in 64 bits."""
+        turns = self.turns.cpu().numpy().view("uint64").astype("float64") / 2.0 ** 64
+        a = positions.double()[:, None, None] * torch.from_numpy(turns * 2 * math.pi).cuda()
+        c, s = a.cos() * self.mscale, a.sin() * self.mscale
+        x1, x2 = x.chunk(2, -1)
+        return torch.cat([x1 * c - x2 * s, x2 * c + x1 * s], -1)
+
+    def check_cache(self, x, lens, token, steps):
+        """Raises unless prompts x of lens tokens and `steps` steps on token left the
+        lengths and the rows that they should have: each head's key and value
+        against the weights' 64-bit products, rotated in 64 bits. Of a row's norm the product may be off
+        by 4e-3 and its f16 rounding by 2^-11, twice, the cache by its
+        format's rounding (Q8_0: half a code, amax / 254, in each of 32 values)."""
+        if not torch.equal(self.lens, lens + steps):
+            raise RuntimeError(f"lengths are {self.lens.tolist()}, not {(lens + steps).tolist()}")
+        bound = 4e-3 + 2 * 2.0 ** -11 + {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "q8_0": 32 ** 0.5 / 254 * (1 + 2.0 ** -9)}[self.fmt]
+        for b, n in enumerate(lens.tolist()):
+            at = torch.arange(n + steps, device="cuda")
+            _, k, v = self.plain_heads(torch.cat([x[b, :n], token[b].expand(steps, -1)]))
+            slots = self.slots(at.expand(self.batch, -1)).view(self.batch, -1)[b].contiguous()
+            got = qmm.qkv_load(self.fmt, slots, self.k_cache, self.v_cache, self.page, self.kv_heads, self.dim)
+            for name, have, want in (("key", got[0], self.plain_rotation(k, at)), ("value", got[1], v)):
+                off = (have.double() - want).norm(dim=-1) / want.norm(dim=-1)
+                if not bool((off <= bound).all()):
+                    raise RuntimeError(f"sequence {b}: a cached {name} is off by {float(off.max()):.1e} of its norm")
+
     def plain_step(self, x):
         """What step(x) returned, recomputed in 64 bits from the weights and the
-        cache as it now is; activations between operators are f16, as there."""
-        w = [qmm.qdequant(self.kind, t, r, c).double() for t, r, c in
-             ((self.w_qkv, self.rows, self.d_model), (self.w_out, self.d_model, self.q_heads * self.dim))]
-        y = (x.double() @ w[0].T).half().double().view(self.batch, -1, self.dim)[:, :self.q_heads]
-        turns = self.turns.cpu().numpy().view("uint64").astype("float64") / 2.0 ** 64
-        a = (self.lens - 1).double()[:, None, None] * torch.from_numpy(turns * 2 * math.pi).cuda()
-        c, s = a.cos() * self.mscale, a.sin() * self.mscale
-        q1, q2 = y.chunk(2, -1)
-        q = torch.cat([q1 * c - q2 * s, q2 * c + q1 * s], -1).half().double()
+        cache as it now is (check_cache says whether it is right); activations
+        between operators are f16, as there."""
+        w_out = qmm.qdequant(self.kind, self.w_out, self.d_model, self.q_heads * self.dim).double()
+        q = self.plain_rotation(self.plain_heads(x)[0], self.lens - 1).half().double()
         out = []
         for b, n in enumerate(self.lens.tolist()):
             at = self.slots(torch.arange(n, device="cuda").expand(self.batch, n)).view(self.batch, n)[b].contiguous()
@@ -94,7 +123,7 @@ class AttentionLayer:
             qb = q[b].view(self.kv_heads, -1, self.dim)
             p = torch.softmax(torch.einsum("hgd,nhd->hgn", qb, k) * self.dim ** -0.5, -1)
             out.append(torch.einsum("hgn,nhd->hgd", p, v).reshape(-1))
-        return torch.stack(out).half().double() @ w[1].T
+        return torch.stack(out).half().double() @ w_out.T
 
 
 def run(steps=32, batch=4, fmt="q8_0", kind="Q4_0", **sizes):
@@ -124,6 +153,7 @@ def run(steps=32, batch=4, fmt="q8_0", kind="Q4_0", **sizes):
     end.synchronize()
     if qmm.check_device_error():
         raise RuntimeError("a device error was latched")
+    layer.check_cache(x, lens, token, 1 + steps)
     want = layer.plain_step(token)
     return float((y.double() - want).norm() / want.norm()), begin.elapsed_time(end) * 1e3 / steps
 
