@@ -639,7 +639,13 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    const float now = fmaxf(ref[n][k], mt - top);
+                    // From 2^24 on floats lie 2 and more apart and mt - top may
+                    // round down, the largest weight past f16's range. There the
+                    // maximum itself is the reference: weights lie that far apart
+                    // too, and the largest is 1.
+                    float now = mt - top;
+                    if ((mt - now) * unit > kTop + 1.f) now = mt;
+                    now = fmaxf(ref[n][k], now);
                     alpha[k] = ex2((ref[n][k] - now) * unit);
                     ref[n][k] = now;
                     l[n][k] *= alpha[k];

@@ -1,0 +1,80 @@
+"""qattn_decode where fp32 arithmetic itself gets coarse: scores past 2^24, over
+every cache format and activation type, capped or not."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import kv_util as U
+from tests.test_attn_decode_gpu import Q, call, check, problem  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(Q, fmt, p, K, V):
+    """Writes K and V (n, heads, dim) to the first sequence's positions."""
+    import torch
+    j = np.arange(K.shape[0])
+    slots = torch.from_numpy(p["host"][0][0, j // p["page"]].astype(np.int64) * p["page"] + j % p["page"]).cuda()
+    Q.qkv_store(fmt, K, V, slots, p["kc"], p["vc"], p["page"])
+    pg, row = slots // p["page"], slots % p["page"]
+    return tuple(U.cache_values(fmt, c, p["page"], p["Hkv"], p["D"])[pg, :, row] for c in (p["kc"], p["vc"]))
+
+
+def equal_keys(Q, fmt, dt, n=70, D=128, k=1.5, q=1.0):
+    """One sequence whose keys are all the same, so that every score is and the
+    weights are 1 / n whatever the scores."""
+    import torch
+    p = problem(Q, fmt, dt, D, 1, 2, 16, [n], 3)
+    p["q"].fill_(q)
+    V = torch.randn((n, 1, D), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    return (p, *rows(Q, fmt, p, torch.full((n, 1, D), k, device="cuda"), V))
+
+
+def check_equal(Q, p, K, V, score, **kw):
+    """The mean of V, and the lse. Equal weights: what is left of the tolerance of
+    kv_util.attend is the weights' terms and the sums; the lse follows the
+    score's own error, its sum's D / 16 steps of up to 3 terms and three roundings."""
+    import torch
+    out, lse = call(Q, p, return_lse=True, **kw)
+    n, acc = V.shape[0], p["dt"]
+    want, mag = V[:, 0].mean(0), V[:, 0].abs().mean(0)
+    rel = (3 * n / 16 + 16) * 2.0 ** -23 + (2.0 ** -20 if acc == "f32" else 2.0 ** -16)
+    tol = mag * rel + U.UNIT[acc] * want.abs() + U.TINY[acc]
+    assert bool(torch.isfinite(out).all()), f"score {score:.3e}: not finite"
+    assert bool(((out[0].double() - want).abs() <= tol).all()), f"score {score:.3e}"
+    ltol = abs(score) * (3 * p["D"] / 16 + 12) * 2.0 ** -23 + 2.0 ** -20
+    assert bool(((lse.double() - (score + math.log(n))).abs() <= ltol).all()), f"score {score:.3e}"
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_scores_past_the_integers_of_fp32(Q, fmt, dt):
+    """From 2^24 (in log2 units) on, a score less 14 is not a float any more: the
+    reference that weights are taken from must not round below it."""
+    p, K, V = equal_keys(Q, fmt, dt)
+    dot = float((p["q"][0, 0].double() * K[0, 0]).sum())
+    for e in range(22, 31):
+        for f in (1.0, 1.21, 1.5, 1.87):
+            for sign in (1, -1):
+                score = sign * 2.0 ** e * f * math.log(2)
+                scale = float(np.float32(score / dot))
+                check_equal(Q, p, K, V, scale * dot, scale=scale)
+
+
+@pytest.mark.parametrize("fmt,dt", [("f16", "f16"), ("q8_0", "f16"), ("q8_0", "f32"), ("f16", "f32")])
+def test_large_activations_at_the_usual_scale(Q, fmt, dt):
+    p, K, V = equal_keys(Q, fmt, dt, k=4000.0, q=4000.0)
+    check_equal(Q, p, K, V, float((p["q"][0, 0].double() * K[0, 0]).sum()) * 128 ** -0.5)
+
+
+@pytest.mark.parametrize("fmt,dt", [("f16", "f16"), ("q8_0", "f32"), ("f16", "f32"), ("bf16", "bf16")])
+def test_large_softcaps(Q, fmt, dt):
+    p, K, V = equal_keys(Q, fmt, dt)
+    dot = float((p["q"][0, 0].double() * K[0, 0]).sum())
+    for cap in (3e7, 1.4e8, 2.0 ** 28 * 1.3, 7e8, 3e9):
+        for sign in (1, -1):
+            scale = float(np.float32(sign * 4 * cap / dot))
+            cap32 = float(np.float32(cap))
+            check_equal(Q, p, K, V, cap32 * math.tanh(scale * dot / cap32), scale=scale, softcap=cap32)
+
