@@ -463,8 +463,8 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
     }
-    // Q8_0: V's scales are below v_lim = 2^E and are multiplied by v_mul = 2^k,
-    // k = -E within f16's range; O carries that factor
+    // Q8_0: V's scales, of either sign, are below v_lim = 2^E in magnitude and are
+    // multiplied by v_mul = 2^k, k = -E within f16's range; O carries that factor
     __half2 v_lim = __float2half2_rn(0.f), v_mul = __float2half2_rn(1.f);
 
     // matrix mi of an ldmatrix: lanes 8 mi .. 8 mi + 7 give its rows
@@ -611,7 +611,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                     for (int c = 0; c < C; ++c) vd[i][c] &= keep;
                 }
 #pragma unroll
-                for (int c = 0; c < C; ++c) v_top = __hmax2(v_top, as_half2(vd[i][c]));
+                for (int c = 0; c < C; ++c) v_top = __hmax2(v_top, __habs2(as_half2(vd[i][c])));
             }
             grew |= !__hbleu2(v_top, v_lim);
         }

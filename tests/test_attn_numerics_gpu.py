@@ -1,5 +1,6 @@
 """qattn_decode where fp32 arithmetic itself gets coarse: scores past 2^24, over
-every cache format and activation type, capped or not."""
+every cache format and activation type, capped or not; cache scales of either
+sign."""
 import math
 
 import numpy as np
@@ -78,3 +79,29 @@ def test_large_softcaps(Q, fmt, dt):
             cap32 = float(np.float32(cap))
             check_equal(Q, p, K, V, cap32 * math.tanh(scale * dot / cap32), scale=scale, softcap=cap32)
 
+
+def negate_blocks(cache, page, heads, dim, seed, share):
+    """A share of a q8_0 cache's blocks as (-scale) * (-code): the same values."""
+    import torch
+    u = cache.view(cache.shape[0], heads, -1)
+    codes = u[:, :, :page * dim].view(torch.int8).view(-1, heads, page, dim // 32, 32)
+    scales = u[:, :, page * dim:].view(torch.float16).view(-1, heads, page, dim // 32)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    flip = torch.rand(scales.shape, generator=g, device="cuda") < share
+    codes.copy_(torch.where(flip[..., None], -codes, codes))
+    scales.copy_(torch.where(flip, -scales, scales))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,group", [(64, 4), (96, 12), (128, 3), (192, 2), (256, 8)])
+@pytest.mark.parametrize("size,share", [(1.0, 0.5), (3000.0, 0.5), (3000.0, 1.0), (1e-3, 1.0)])
+def test_negative_scales(Q, dt, D, group, size, share):
+    """A block's value is scale * code whatever the scale's sign (a cache may
+    come from elsewhere: qkv_store writes none below zero)."""
+    import torch
+    p = problem(Q, "q8_0", dt, D, 2, group, 16, [333, 40, 0, 1, 3000], D, garbage=False)
+    v = p["vc"].view(p["vc"].shape[0], 2, -1)[:, :, 16 * D:].view(torch.float16)
+    v.copy_((v.float() * size).half())
+    for c, s in ((p["kc"], 1), (p["vc"], 2)):
+        negate_blocks(c, 16, 2, D, s, share)
+    check(Q, p)
