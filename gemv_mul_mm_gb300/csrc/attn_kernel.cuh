@@ -35,12 +35,16 @@
 // range: fp32 / bf16 q rows are scaled by a power of two that puts their
 // largest magnitude in [2^9, 2^10), and weights are held as 2^14 e^{s - m}.
 //
-// Q8_0 codes enter exactly. K: the biased code u = c + 128 in the low byte is
-// the f16 subnormal u 2^-24; the block's product starts at -128 2^-24 sum q to
-// take the bias out, and K's block scale multiplies the fp32 partial sum of the
-// 32 dims. The bias costs a factor of two in the sum's magnitude, no more,
-// because |u| < 256 against |c| < 128; in the second product, whose sums over
-// thousands of keys cancel, codes enter without bias (1024 + u minus 1152).
+// Q8_0 codes enter exactly, as the f16 integers they are (u = c + 128 in the low
+// byte of 1024, less 1152). K's block scale multiplies the fp32 partial sum of
+// the 32 dims. The MMA cuts its sum off 24 bits below the largest term, so that
+// nothing large may stand in it that the result does not hold: the biased codes
+// themselves, with 128 sum q taken off at the start, are a subtraction fewer,
+// but where one channel of a block stands out the other codes are small, and
+// scores came out 10 to 20 times as far off as an fp32 sum with a channel of 50
+// times the others, 100 to 300 times with one of 500. (Nor were they faster: 64 x
+// 8192 tokens, f16 q, 202 us against 194.) The small terms of q are summed first,
+// for the same reason.
 // V's block scale d multiplies the two terms of p: t1 = rn(ph d), then
 // t2 = rn(pl d + (ph d - t1)), where the bracket is exact in one fma. A power
 // of two, from the running largest exponent of V's scales, keeps d near 1.
@@ -122,12 +126,6 @@ __device__ __forceinline__ void codes_f16(unsigned x, unsigned& p0, unsigned& p1
     const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
     p0 = *reinterpret_cast<const unsigned*>(&r0);
     p1 = *reinterpret_cast<const unsigned*>(&r1);
-}
-
-// The same pairs as f16 subnormals (c + 128) 2^-24, exactly.
-__device__ __forceinline__ void codes_sub(unsigned x, unsigned& p0, unsigned& p1) {
-    p0 = (x & 0x00ff00ffu) ^ 0x00800080u;
-    p1 = __byte_perm(x, 0u, 0x4341) ^ 0x00800080u;
 }
 
 __device__ __forceinline__ __half2 as_half2(unsigned x) { return *reinterpret_cast<const __half2*>(&x); }
@@ -240,7 +238,6 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sm_q[8 * NT][D + 4];
     __shared__ float sm_m[kWarps][8 * NT], sm_l[kWarps][8 * NT], sm_scale[8 * NT];
-    __shared__ __align__(8) float sm_qsum[Q8 ? C : 1][8 * NT];
     __shared__ uint2 sm_qf[Q8 ? NT * NQ * MT : 1][32];
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
@@ -391,27 +388,6 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         }
         __syncthreads();
     }
-    if constexpr (Q8) {
-        // -128 2^-24 times the sum of the q terms of each 32-dim block, four lanes
-        // to a block
-        for (int i = threadIdx.x; i < 8 * NT * C * 4; i += kThreads) {
-            const int h = i / (4 * C), c = i / 4 % C;
-            const float f = NORM ? sm_scale[h] : 1.f;
-            float sum = 0.f;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                const float x = sm_q[h][32 * c + 4 * d + i % 4] * f;
-                float rest = x, none = 0.f;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) take16<false>(rest, none);
-                sum += x - rest;
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (i % 4 == 0) sm_qsum[c][h] = sum * -7.62939453125e-06f;
-        }
-        __syncthreads();
-    }
     // The fragments stay in registers, or with Q8_0, whose registers decide how
     // many blocks fit an SM, in shared memory, where the block's warps share them.
     uint2 qf[Q8 ? 1 : NT][Q8 ? 1 : NQ][Q8 ? 1 : MT];
@@ -439,7 +415,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            sc[n][k] = a.scale * (Q8 ? 16777216.f : 1.f) * (a.softcap > 0.f ? 1.f : kLog2e);
+            sc[n][k] = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
             if (NORM) sc[n][k] /= sm_scale[8 * n + 2 * t + k];
         }
     }
@@ -499,17 +475,16 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
                 unsigned x[2][4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    codes_sub(w[2 * j], x[j][0], x[j][2]);
-                    codes_sub(w[2 * j + 1], x[j][1], x[j][3]);
+                    codes_f16(w[2 * j], x[j][0], x[j][2]);
+                    codes_f16(w[2 * j + 1], x[j][1], x[j][3]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float2 qb = *reinterpret_cast<const float2*>(&sm_qsum[c][8 * n + 2 * t]);
-                    float acc[4] = {qb.x, qb.y, qb.x, qb.y};
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int q = NQ - 1; q >= 0; --q)
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
+                        for (int j = 0; j < 2; ++j) {
                             const uint2 f = q_frag(n, q, 2 * c + j);
                             mma<BF>(acc, x[j][0], x[j][1], x[j][2], x[j][3], f.x, f.y);
                         }

@@ -1,6 +1,6 @@
 """qattn_decode where fp32 arithmetic itself gets coarse: scores past 2^24, over
-every cache format and activation type, capped or not; cache scales of either
-sign."""
+every cache format and activation type, capped or not; query rows of any
+magnitude, cache scales of either sign, key channels far above the others."""
 import math
 
 import numpy as np
@@ -105,3 +105,49 @@ def test_negative_scales(Q, dt, D, group, size, share):
     for c, s in ((p["kc"], 1), (p["vc"], 2)):
         negate_blocks(c, 16, 2, D, s, share)
     check(Q, p)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8_0"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_enormous_queries(Q, fmt, dt):
+    """Query rows near the end of fp32's range over small keys: finite scores,
+    1e29 apart, so that one key takes all."""
+    import torch
+    p = problem(Q, fmt, dt, 64, 1, 2, 16, [100], 3)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    K, V = rows(Q, fmt, p, 1e-4 * torch.randn((100, 1, 64), generator=g, device="cuda"), torch.randn((100, 1, 64), generator=g, device="cuda"))
+    for size in (2.0 ** 100, 2.0 ** 112, 2.0 ** 118, 2.0 ** 122):
+        r = dict(p, q=(p["q"].double() * size).to(p["q"].dtype))
+        out, lse = call(Q, r, return_lse=True)
+        s = torch.einsum("hd,nd->hn", r["q"][0].double(), K[:, 0]) * 0.125
+        best = V[s.argmax(-1), 0]
+        tol = 2.0 ** -22 + U.UNIT[dt]
+        assert bool(((out[0].double() - best).abs() <= tol * best.abs() + 1e-30).all()), f"q of {size:.1e}"
+        assert bool(((lse[0].double() / s.amax(-1) - 1).abs() < 1e-5).all()), f"q of {size:.1e}"
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("outlier", [1.0, 50.0, 500.0])
+def test_key_channels_above_the_others(Q, dt, D, outlier):
+    """A channel of K far above the others, where q is small, leaves small codes
+    elsewhere in its block. The score is the fp32 sum of its terms all the same.
+    One key a sequence: its lse is the score. Summed one after another in fp32, the terms
+    give an error of a quarter of 2^-23 of S = sum |q k| (rms over many scores);
+    1 is allowed."""
+    import torch
+    n = 96
+    p = problem(Q, "q8_0", dt, D, 1, 8, 16, [1] * n, 5)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    K = torch.randn((n, 1, D), generator=g, device="cuda")
+    K[..., 7] *= outlier
+    slots = torch.from_numpy(p["host"][0][:, 0].astype(np.int64) * 16).cuda()
+    Q.qkv_store("q8_0", K, K, slots, p["kc"], p["vc"], 16)
+    K = U.cache_values("q8_0", p["kc"], 16, 1, D)[slots // 16, 0, 0]
+    q = 300.0 * torch.randn(p["q"].shape, generator=g, device="cuda")
+    q[..., 7] *= 1e-3 if outlier > 1 else 1.0
+    p["q"] = q.to(p["q"].dtype)
+    _, lse = call(Q, p, return_lse=True)
+    terms = p["q"].double() * K[:, None] * D ** -0.5
+    err = (lse.double() - terms.sum(-1)) / terms.abs().sum(-1)
+    assert float(err.square().mean().sqrt()) <= 2.0 ** -23
