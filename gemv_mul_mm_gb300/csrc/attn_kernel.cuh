@@ -426,8 +426,10 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
     };
 
     // Weights are 2^(score - ref) <= 2^kTop: f16 terms use the top of their
-    // range. Before the first score, ref is kNone: every finite score exceeds it.
-    constexpr float kTop = BF ? 0.f : 14.f, kNone = -3e38f;
+    // range. Before the first score, ref is kNone, the lowest float (with an
+    // infinity a masked score would be NaN): a score of just that value leaves
+    // ref alone and is told from none by l.
+    constexpr float kTop = BF ? 0.f : 14.f, kNone = -3.402823466e38f;
     const float unit = unit_of(a), top = a.softcap > 0.f ? kTop * kLn2 : kTop;
     float ref[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
@@ -784,7 +786,7 @@ __device__ __forceinline__ void attn_block(const AttnArgs& a, int splits, int ch
             l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], 8);
             l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], 16);
             if (g == 0) {
-                sm_m[warp][8 * n + 2 * t + k] = ref[n][k] == kNone ? -INFINITY : ref[n][k];
+                sm_m[warp][8 * n + 2 * t + k] = l[n][k] == 0.f ? -INFINITY : ref[n][k];
                 sm_l[warp][8 * n + 2 * t + k] = bad ? NAN : l[n][k];
             }
         }

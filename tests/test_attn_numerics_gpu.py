@@ -1,5 +1,6 @@
 """qattn_decode where fp32 arithmetic itself gets coarse: scores past 2^24, over
-every cache format and activation type, capped or not; query rows of any
+every cache format and activation type, capped or not, and near the lowest
+float; query rows of any
 magnitude, cache scales of either sign, key channels far above the others."""
 import math
 
@@ -151,3 +152,13 @@ def test_key_channels_above_the_others(Q, dt, D, outlier):
     terms = p["q"].double() * K[:, None] * D ** -0.5
     err = (lse.double() - terms.sum(-1)) / terms.abs().sum(-1)
     assert float(err.square().mean().sqrt()) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("fmt,dt", [("f16", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32"), ("q8_0", "f32")])
+def test_scores_near_the_lowest_float(Q, fmt, dt):
+    """Finite scores are real ones down to the lowest float (in log2 units)."""
+    p, K, V = equal_keys(Q, fmt, dt, D=64, k=1.0)
+    dot = float((p["q"][0, 0].double() * K[0, 0]).sum())
+    for log2_score in (-1e38, -2.9e38, -3.1e38, -3.39e38):
+        scale = float(np.float32(log2_score * math.log(2) / dot))
+        check_equal(Q, p, K, V, scale * dot, scale=scale)
