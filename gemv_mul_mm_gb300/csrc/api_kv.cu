@@ -78,6 +78,16 @@ int plan_for(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len,
     return QMM_OK;
 }
 
+// The same for sizes that are not checked yet; false where qattn_decode would
+// refuse them.
+bool plan_of(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, AttnPlan* p) {
+    if ((fmt != QMM_KV_F16 && fmt != QMM_KV_BF16 && fmt != QMM_KV_Q8_0) || !dtype_ok(dtype)) return false;
+    if (B <= 0 || B > (1 << 24) || Hq <= 0 || Hq > 65536 || Hkv <= 0 || Hq % Hkv || !attn_dim_ok(D) || max_len <= 0 ||
+        max_len > (1 << 30) || window < 0)
+        return false;
+    return plan_for(fmt, dtype, B, Hq, Hkv, D, max_len, window, p) == QMM_OK;
+}
+
 int done(cudaError_t e, int path) {
     if (e != cudaSuccess) return QMM_ERR_CUDA;
     set_last_path(path);
@@ -232,12 +242,13 @@ int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const void* v_c
 
 size_t qattn_decode_workspace_bytes(int fmt, int dtype, int64_t B, int n_q_heads, int n_kv_heads, int head_dim,
                                     int max_len, int window) {
-    if ((fmt != QMM_KV_F16 && fmt != QMM_KV_BF16 && fmt != QMM_KV_Q8_0) || !dtype_ok(dtype)) return 0;
-    if (B <= 0 || B > (1 << 24) || n_q_heads <= 0 || n_q_heads > 65536 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
-        !attn_dim_ok(head_dim) || max_len <= 0 || max_len > (1 << 30) || window < 0)
-        return 0;
     AttnPlan p;
-    return plan_for(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p) == QMM_OK ? p.ws_bytes : 0;
+    return plan_of(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p) ? p.ws_bytes : 0;
+}
+
+int qattn_decode_splits(int fmt, int dtype, int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int max_len, int window) {
+    AttnPlan p;
+    return plan_of(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p) ? p.splits : 0;
 }
 
 int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs, const void* k_cache,
@@ -271,7 +282,7 @@ int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs
         return QMM_ERR_OUTPUT_TOO_SMALL;
     AttnPlan p;
     if (int r = plan_for(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p)) return r;
-    if (p.ws_bytes) {
+    if (p.splits > 1) {
         if (!workspace) return QMM_ERR_NULL_POINTER;
         if (workspace_bytes < p.ws_bytes) return QMM_ERR_WORKSPACE_TOO_SMALL;
     }

@@ -115,9 +115,13 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     // 16384 keys are 1.2e-5 of the result, little against a 16-bit output's own
     // rounding, and more are not taken.
     const int64_t least = p->hi ? 1 : (steps + 255) / 256;
+    // More than 64 blocks per SM are not made (only sequences of a million
+    // keys and batches that nearly fill the memory would take them): the workspace
+    // has a bound that grows with the sizes, though the count itself does not.
+    const int64_t blocks = static_cast<int64_t>(64) * sms;
     int64_t best = least;
     double best_cost = cost(best, (steps + best - 1) / best);
-    const int64_t most = std::max(least, std::min<int64_t>(steps, 512));
+    const int64_t most = std::max(least, std::min<int64_t>({steps, 512, blocks / items}));
     for (int i = 0; i < 18; ++i) {
         const int64_t s = i < 9 ? int64_t(2) << i : (i - 8) * sms / items;
         if (s < 2 || s <= least || s > most) continue;
@@ -131,7 +135,11 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     const int64_t per = (steps + best - 1) / best;
     p->chunk = static_cast<int>(per * step);
     p->splits = static_cast<int>(best);
-    p->ws_bytes = best > 1 ? static_cast<size_t>(B) * Hq * best * (D * 4 + 8) : 0;
+    // Partial results at most: those of the most splits that this batch and any
+    // smaller one, these lengths and any shorter ones, can have.
+    const int64_t heads = B * Hq, any = std::max(least, std::min<int64_t>(steps, 512));
+    const int64_t parts = std::min(heads * any, std::max(heads * least, (blocks * group + p->head_chunks - 1) / p->head_chunks));
+    p->ws_bytes = any > 1 ? static_cast<size_t>(parts) * (D * 4 + 8) : 0;
     return cudaSuccess;
 }
 

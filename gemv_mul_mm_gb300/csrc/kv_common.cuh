@@ -216,7 +216,7 @@ struct AttnPlan {
     int tiles;                     // 8-head tiles of a head group
     int head_chunks;               // head groups per key-value head
     bool hi;                       // the kernel with more terms
-    size_t ws_bytes;
+    size_t ws_bytes;               // what a split call asks for: no less than smaller sizes need
 };
 bool attn_dim_ok(int D);
 cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int max_len, int window, int sms, AttnPlan* p);

@@ -23,6 +23,7 @@ static __typeof__(&qkv_store) f_qkv_store;
 static __typeof__(&qkv_load) f_qkv_load;
 static __typeof__(&qattn_decode) f_qattn_decode;
 static __typeof__(&qattn_decode_workspace_bytes) f_ws_bytes;
+static __typeof__(&qattn_decode_splits) f_splits;
 
 static PyObject *dt_act[3];               /* torch.float32, float16, bfloat16: qmm_dtype order */
 static PyObject *dt_i32, *dt_i64, *dt_u8;
@@ -40,17 +41,18 @@ static int set_ref(PyObject **to, PyObject *o) {
 }
 
 static PyObject *setup(PyObject *self, PyObject *args) {
-    unsigned long long a[5];
+    unsigned long long a[6];
     PyObject *o[11];
     (void)self;
-    if (!PyArg_ParseTuple(args, "(KKKKK)(OOO)OOOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &o[0], &o[1], &o[2], &o[3], &o[4],
-                          &o[5], &o[6], &o[7], &o[8], &o[9], &o[10]))
+    if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &a[5], &o[0], &o[1], &o[2], &o[3],
+                          &o[4], &o[5], &o[6], &o[7], &o[8], &o[9], &o[10]))
         return NULL;
     f_qrope = (__typeof__(f_qrope))(uintptr_t)a[0];
     f_qkv_store = (__typeof__(f_qkv_store))(uintptr_t)a[1];
     f_qkv_load = (__typeof__(f_qkv_load))(uintptr_t)a[2];
     f_qattn_decode = (__typeof__(f_qattn_decode))(uintptr_t)a[3];
     f_ws_bytes = (__typeof__(f_ws_bytes))(uintptr_t)a[4];
+    f_splits = (__typeof__(f_splits))(uintptr_t)a[5];
     for (int i = 0; i < 3; ++i) set_ref(&dt_act[i], o[i]);
     set_ref(&dt_i32, o[3]);
     set_ref(&dt_i64, o[4]);
@@ -477,7 +479,8 @@ static PyObject *py_qattn_decode(PyObject *self, PyObject *const *a, Py_ssize_t 
     if (with_lse && !(lse = new_tensor(2, q.shape, dt_act[0], &stream, &lptr))) goto done;
     int64_t wn = 0;
     if (a[14] == Py_None) {
-        wn = (int64_t)f_ws_bytes(fmt, dt, B, (int)H, kv, (int)D, (int)max_len, window);
+        if (f_splits(fmt, dt, B, (int)H, kv, (int)D, (int)max_len, window) > 1)
+            wn = (int64_t)f_ws_bytes(fmt, dt, B, (int)H, kv, (int)D, (int)max_len, window);
         if (wn && !(ws = new_tensor(1, &wn, dt_u8, &stream, &wptr))) goto done;
     } else {
         if (read_tensor(a[14], &t, "workspace") || on(&t, q.dev, "workspace")) goto done;

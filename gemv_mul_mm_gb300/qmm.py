@@ -93,6 +93,7 @@ def _lib():
                                    _I64, _I, _I, _I, f32, _I, f32, _P, _SZ, _P, _P, _SZ, _P]
         L.qattn_decode_workspace_bytes.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
         L.qattn_decode_workspace_bytes.restype = _SZ
+        L.qattn_decode_splits.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
         L.qmm_check_device_error.argtypes = [_P]
         L.qmm_selftest_wait_timeout.argtypes = [_I64, _P]
         L.qmm_set_path.argtypes = [_I]
@@ -326,7 +327,7 @@ def _calls():
                 return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
         entry = tuple(ctypes.cast(f, _P).value for f in
-                      (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes))
+                      (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes, L.qattn_decode_splits))
         _pycall.setup(entry, (torch.float32, torch.float16, torch.bfloat16), torch.int32, torch.int64, torch.uint8, raw, current,
                       new, new_on, _check)
         _CALL = _pycall
@@ -395,9 +396,19 @@ def qkv_load(fmt, slots, k_cache, v_cache, page_size: int, n_kv_heads: int, head
 
 def qattn_decode_workspace_bytes(fmt, dtype, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
                                  window: int = 0) -> int:
+    """Scratch bytes of qattn_decode on the current device; what the largest batch
+    and max_len ask for serves every smaller call."""
     import torch
     dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dtype]
     return _lib().qattn_decode_workspace_bytes(_fmt(fmt), dt, batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
+
+
+def qattn_decode_splits(fmt, dtype, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
+                        window: int = 0) -> int:
+    """Parts that qattn_decode splits sequences of max_len into; with 1 it uses no workspace."""
+    import torch
+    dt = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dtype]
+    return _lib().qattn_decode_splits(_fmt(fmt), dt, batch, n_q_heads, n_kv_heads, head_dim, max_len, window)
 
 
 def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int, n_kv_heads: int,
@@ -409,8 +420,8 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     head_dim ** -0.5; max_len (a bound on seq_lens) to what the table holds; a
     tighter one splits short batches better. Returns out (q's type), and lse
     (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
-    uint8 tensor of qattn_decode_workspace_bytes(...)), allocated here with
-    torch if None."""
+    uint8 tensor of qattn_decode_workspace_bytes(...) or more, of larger
+    sizes for instance), allocated here with torch if None."""
     return (_CALL or _calls()).qattn_decode(_fmt(fmt), q, k_cache, v_cache, block_table, seq_lens, page_size, n_kv_heads, scale,
                                             window, softcap, max_len, out, return_lse, workspace, stream)
 

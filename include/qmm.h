@@ -502,7 +502,8 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  *                [B][n_q_heads] or NULL
  *   workspace    device scratch of the caller, 16-byte aligned, at least
  *                qattn_decode_workspace_bytes(...) bytes (may be NULL where
- *                that is 0); calls that overlap must not share it
+ *                that is 0 or qattn_decode_splits is 1); calls that overlap
+ *                must not share it
  * head_dim is 64, 96, 128, 192 or 256 (QMM_ERR_UNIMPLEMENTED otherwise).
  */
 QMM_API int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs, int64_t q_hs,
@@ -513,10 +514,16 @@ QMM_API int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int6
                          void* out, size_t out_elems, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream);
 
-/* Scratch bytes qattn_decode needs on the current device (0: none, or an
- * argument it refuses). */
+/* Scratch bytes qattn_decode asks for on the current device (0: none, or an
+ * argument it refuses). They do not shrink as B, max_len or window (0 counting
+ * as the longest) grow: one workspace of the largest serves every smaller call. */
 QMM_API size_t qattn_decode_workspace_bytes(int fmt, int dtype, int64_t B, int n_q_heads, int n_kv_heads, int head_dim,
                                             int max_len, int window);
+
+/* Parts that qattn_decode splits sequences of max_len into on the current
+ * device; with 1 it uses no workspace. 0: an argument it refuses. */
+QMM_API int qattn_decode_splits(int fmt, int dtype, int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
+                                int window);
 
 /*
  * qmm_check_device_error -- synchronize `stream`, then read and clear the
