@@ -1,6 +1,8 @@
 // api_kv.cu -- the C ABI of the rotary, cache and attention operators
 // (include/qmm.h): argument validation and dispatch.
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "kv_common.cuh"
 
@@ -18,6 +20,39 @@ constexpr int64_t kBig = int64_t(1) << 40;
 bool fits(size_t elems, int64_t rows, int64_t rs, int64_t cols, int64_t cs, int64_t last) {
     const __int128 need = static_cast<__int128>(rows - 1) * rs + static_cast<__int128>(cols - 1) * cs + last;
     return need <= static_cast<__int128>(elems);
+}
+
+// Whether some |o + t * ts| < D with |t| < T (t = 0 not counted with `apart`).
+bool comes_near(int64_t o, int64_t T, int64_t ts, int64_t D, bool apart) {
+    const int64_t at = ts ? std::min(std::max(-o / ts, 1 - T), T - 1) : T > 1;
+    for (int64_t t = std::max(at - 1, 1 - T); t <= std::min(at + 1, T - 1); ++t)
+        if (!(apart && t == 0) && std::llabs(o + t * ts) < D) return true;
+    return false;
+}
+
+// Whether two rows of Y (t, h), D elements at t * ts + h * hs, share an element.
+bool rows_meet(int64_t T, int64_t ts, int64_t H, int64_t hs, int64_t D) {
+    if ((H == 1 || hs >= D) && (T == 1 || ts >= (H - 1) * hs + D)) return false;   // the usual order
+    if ((T == 1 || ts >= D) && (H == 1 || hs >= (T - 1) * ts + D)) return false;
+    for (int64_t h = 0; h < H; ++h)
+        if (comes_near(h * hs, T, ts, D, h == 0)) return true;
+    return false;
+}
+
+// Whether Y may be written while X is read: Y is X, or they share no element.
+// Where their ranges meet and their token strides differ that is not looked into.
+bool apart_or_same(const RopeArgs& a, int64_t size) {
+    const int64_t x0 = reinterpret_cast<intptr_t>(a.X) / size, y0 = reinterpret_cast<intptr_t>(a.Y) / size;
+    const int64_t xn = (a.T - 1) * a.x_ts + (a.H - 1) * a.x_hs + a.D, yn = (a.T - 1) * a.y_ts + (a.H - 1) * a.y_hs + a.D;
+    if (x0 + xn <= y0 || y0 + yn <= x0) return true;
+    const bool same_ts = a.T == 1 || a.x_ts == a.y_ts, same_hs = a.H == 1 || a.x_hs == a.y_hs;
+    if (a.X == a.Y && same_ts && same_hs) return true;
+    if (!same_ts || (!same_hs && a.H > 1024)) return false;
+    const int64_t lo = same_hs ? 1 - a.H : 0;        // same_hs: h is a difference of heads
+    for (int64_t h = lo; h < a.H; ++h)
+        for (int64_t g = 0; g < (same_hs ? 1 : a.H); ++g)
+            if (comes_near(y0 - x0 + h * a.y_hs - g * a.x_hs, a.T, a.x_ts, a.D, false)) return false;
+    return true;
 }
 
 // The rotary arguments shared by qrope and qkv_store.
@@ -175,6 +210,7 @@ int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, 
     a.T = T;
     a.H = H;
     a.D = D;
+    if (rows_meet(T, y_ts, H, y_hs, D) || !apart_or_same(a, esize(dtype))) return QMM_ERR_BAD_ARGUMENT;
     return done(launch_rope(a, static_cast<cudaStream_t>(stream)), 8);
 }
 

@@ -432,9 +432,10 @@ QMM_API int qrope_turns(double base, int rot_dim, int scaling, double factor, do
  * copied. fp32 arithmetic, one rounding at the store. The gradient of the
  * input is the same call on the output's gradient with negated positions.
  *
- *   X, Y        device, dtype, element (t, h, d) at t * ts + h * hs + d; Y may
- *               be X with the same strides (in place), and must not overlap it
- *               otherwise; x_elems, y_elems their sizes
+ *   X, Y        device, dtype, element (t, h, d) at t * ts + h * hs + d; x_elems,
+ *               y_elems their sizes. Y may be X with the same strides (in place).
+ *               Otherwise they share no element, nor do two rows of Y
+ *               (QMM_ERR_BAD_ARGUMENT); Y between rows of X has X's token stride
  *   positions   device int32 [T], any sign;  turns  device [rot_dim / 2]
  */
 QMM_API int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, const int32_t* positions,
