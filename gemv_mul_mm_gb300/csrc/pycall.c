@@ -311,6 +311,14 @@ static int nargs_are(Py_ssize_t n, Py_ssize_t want_n, const char *name) {
     return 0;
 }
 
+/* Reads a table of qrope_turns. */
+static int want_turns(PyObject *o, Ten *t, int dev) {
+    if (want(o, t, dt_i64, -1, dev, "turns")) return -1;
+    if (numel(t) <= INT32_MAX / 2) return 0;
+    PyErr_SetString(PyExc_ValueError, "turns has too many elements");
+    return -1;
+}
+
 /* ---- the operators */
 
 /* (X, positions, turns, layout, mscale, out or None, stream or None) */
@@ -318,12 +326,12 @@ static PyObject *py_qrope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Ten x, pos, turns, y;
     size_t xn, yn;
     Stream stream;
-    PyObject *out = a[5];
     (void)self;
     if (!nargs_are(n, 7, "qrope") || read_tensor(a[0], &x, "X")) return NULL;
+    PyObject *out = a[5];
     const int dt = act_of(x.dtype, "X");
     if (dt < 0 || rows_of(&x, "X", &xn) || on_current(&x, "X") ||
-        want(a[1], &pos, dt_i32, x.shape[0], x.dev, "positions") || want(a[2], &turns, dt_i64, -1, x.dev, "turns"))
+        want(a[1], &pos, dt_i32, x.shape[0], x.dev, "positions") || want_turns(a[2], &turns, x.dev))
         return NULL;
     const int layout = as_int(a[3]);
     const float mscale = (float)PyFloat_AsDouble(a[4]);
@@ -378,7 +386,7 @@ static PyObject *py_qkv_store(PyObject *self, PyObject *const *a, Py_ssize_t n) 
         PyErr_SetString(PyExc_ValueError, "positions and turns go together");
         return NULL;
     }
-    if (rope && (want(a[7], &pos, dt_i32, k.shape[0], k.dev, "positions") || want(a[8], &turns, dt_i64, -1, k.dev, "turns")))
+    if (rope && (want(a[7], &pos, dt_i32, k.shape[0], k.dev, "positions") || want_turns(a[8], &turns, k.dev)))
         return NULL;
     const int fmt = as_int(a[0]), page = as_int(a[6]), layout = as_int(a[9]);
     const float mscale = (float)PyFloat_AsDouble(a[10]);
