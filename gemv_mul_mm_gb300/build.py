@@ -2,8 +2,10 @@
 
 Each .cu translation unit compiles in parallel into an object, then one
 link step makes the shared library. csrc/pycall.c, the CPython bindings of the
-serving operators, becomes the extension module _pycall.so. Used by ``__graft_entry__.build()`` and
-by the Python binding when the library is missing or stale.
+serving operators, becomes an extension module named for this Python's ABI;
+without Python's headers the library is built all the same. Used by
+``__graft_entry__.build()`` and by the Python binding when the library is
+missing or stale.
 """
 from __future__ import annotations
 
@@ -14,13 +16,14 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
 PYCALL_SRC = os.path.join(CSRC, "pycall.c")
-PYCALL = os.path.join(HERE, "_pycall.so")
+PYCALL = os.path.join(HERE, "_pycall" + sysconfig.get_config_var("EXT_SUFFIX"))
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -60,15 +63,20 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
-def build_pycall(force: bool = False) -> str:
+def build_pycall(force: bool = False) -> Optional[str]:
+    """The extension module, or None where Python's headers or a C compiler are
+    missing (qmm then says so when one of its operators is called)."""
     deps = [PYCALL_SRC, os.path.join(ROOT, "include", "qmm.h")]
     if not force and os.path.exists(PYCALL) and all(os.path.getmtime(f) <= os.path.getmtime(PYCALL) for f in deps):
         return PYCALL
     cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
-    if cc is None:
-        raise RuntimeError("no C compiler found")
+    include = sysconfig.get_paths()["include"]
+    missing = "a C compiler" if cc is None else "" if os.path.exists(os.path.join(include, "Python.h")) else "Python.h"
+    if missing:
+        sys.stderr.write(f"{missing} not found: built without the Python bindings of qrope, qkv_store, qkv_load and qattn_decode\n")
+        return None
     tmp = PYCALL + ".tmp"
-    cmd = [cc, "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+    cmd = [cc, "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", include,
            "-I", os.path.join(ROOT, "include"), PYCALL_SRC, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -78,7 +86,12 @@ def build_pycall(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    lib = build_lib(force, verbose_ptxas)
     build_pycall(force)
+    return lib
+
+
+def build_lib(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -310,7 +310,7 @@ def _calls():
         try:
             from gemv_mul_mm_gb300 import _pycall
         except ImportError as e:
-            raise ImportError("_pycall.so not built; run __graft_entry__.build() first") from e
+            raise ImportError("_pycall not built for this Python; run __graft_entry__.build() where Python.h and a C compiler are") from e
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
             def raw(device):
