@@ -39,19 +39,21 @@ bool rows_meet(int64_t T, int64_t ts, int64_t H, int64_t hs, int64_t D) {
     return false;
 }
 
-// Whether Y may be written while X is read: Y is X, or they share no element.
-// Where their ranges meet and their token strides differ that is not looked into.
-bool apart_or_same(const RopeArgs& a, int64_t size) {
-    const int64_t x0 = reinterpret_cast<intptr_t>(a.X) / size, y0 = reinterpret_cast<intptr_t>(a.Y) / size;
-    const int64_t xn = (a.T - 1) * a.x_ts + (a.H - 1) * a.x_hs + a.D, yn = (a.T - 1) * a.y_ts + (a.H - 1) * a.y_hs + a.D;
+// Whether rows of Y may be written while those of X are read, T x H rows of D
+// elements each: Y is X, or they share no element. Where their ranges meet and
+// their token strides differ that is not looked into.
+bool apart_or_same(const void* X, int64_t x_ts, int64_t x_hs, const void* Y, int64_t y_ts, int64_t y_hs, int64_t T, int64_t H,
+                   int64_t D, int64_t size) {
+    const int64_t x0 = reinterpret_cast<intptr_t>(X) / size, y0 = reinterpret_cast<intptr_t>(Y) / size;
+    const int64_t xn = (T - 1) * x_ts + (H - 1) * x_hs + D, yn = (T - 1) * y_ts + (H - 1) * y_hs + D;
     if (x0 + xn <= y0 || y0 + yn <= x0) return true;
-    const bool same_ts = a.T == 1 || a.x_ts == a.y_ts, same_hs = a.H == 1 || a.x_hs == a.y_hs;
-    if (a.X == a.Y && same_ts && same_hs) return true;
-    if (!same_ts || (!same_hs && a.H > 1024)) return false;
-    const int64_t lo = same_hs ? 1 - a.H : 0;        // same_hs: h is a difference of heads
-    for (int64_t h = lo; h < a.H; ++h)
-        for (int64_t g = 0; g < (same_hs ? 1 : a.H); ++g)
-            if (comes_near(y0 - x0 + h * a.y_hs - g * a.x_hs, a.T, a.x_ts, a.D, false)) return false;
+    const bool same_ts = T == 1 || x_ts == y_ts, same_hs = H == 1 || x_hs == y_hs;
+    if (X == Y && same_ts && same_hs) return true;
+    if (!same_ts || (!same_hs && H > 1024)) return false;
+    const int64_t lo = same_hs ? 1 - H : 0;          // same_hs: h is a difference of heads
+    for (int64_t h = lo; h < H; ++h)
+        for (int64_t g = 0; g < (same_hs ? 1 : H); ++g)
+            if (comes_near(y0 - x0 + h * y_hs - g * x_hs, T, x_ts, D, false)) return false;
     return true;
 }
 
@@ -194,6 +196,8 @@ int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, 
     if (int r = check_rope(positions, turns, rot_dim, layout, mscale, D)) return r;
     if (!fits(x_elems, T, x_ts, H, x_hs, D)) return QMM_ERR_ACTIVATIONS_TOO_SMALL;
     if (!fits(y_elems, T, y_ts, H, y_hs, D)) return QMM_ERR_OUTPUT_TOO_SMALL;
+    if (rows_meet(T, y_ts, H, y_hs, D) || !apart_or_same(X, x_ts, x_hs, Y, y_ts, y_hs, T, H, D, esize(dtype)))
+        return QMM_ERR_BAD_ARGUMENT;
     RopeArgs a;
     a.X = X;
     a.Y = Y;
@@ -210,7 +214,6 @@ int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, 
     a.T = T;
     a.H = H;
     a.D = D;
-    if (rows_meet(T, y_ts, H, y_hs, D) || !apart_or_same(a, esize(dtype))) return QMM_ERR_BAD_ARGUMENT;
     return done(launch_rope(a, static_cast<cudaStream_t>(stream)), 8);
 }
 
@@ -316,6 +319,9 @@ int qattn_decode(int fmt, const void* q, int dtype, size_t q_elems, int64_t q_bs
         return QMM_ERR_ACTIVATIONS_TOO_SMALL;
     if (!fits(out_elems, B, static_cast<int64_t>(n_q_heads) * head_dim, n_q_heads, head_dim, head_dim))
         return QMM_ERR_OUTPUT_TOO_SMALL;
+    if (!apart_or_same(q, q_bs, q_hs, out, static_cast<int64_t>(n_q_heads) * head_dim, head_dim, B, n_q_heads, head_dim,
+                       esize(dtype)))
+        return QMM_ERR_BAD_ARGUMENT;
     AttnPlan p;
     if (int r = plan_for(fmt, dtype, B, n_q_heads, n_kv_heads, head_dim, max_len, window, &p)) return r;
     if (p.splits > 1) {

@@ -499,7 +499,8 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  *                heads and latches QMM_ERR_BAD_SLOT.
  *   max_len      host bound on seq_lens, at most table_width * page_size
  *   window       0: the whole sequence
- *   out          device, dtype, [B][n_q_heads][head_dim]; lse  fp32
+ *   out          device, dtype, [B][n_q_heads][head_dim]: q itself where that
+ *                is contiguous, or apart from it (QMM_ERR_BAD_ARGUMENT); lse  fp32
  *                [B][n_q_heads] or NULL
  *   workspace    device scratch of the caller, 16-byte aligned, at least
  *                qattn_decode_workspace_bytes(...) bytes (may be NULL where
