@@ -40,11 +40,11 @@ template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_
 // Depth of a warp's ring and blocks per SM, measured on 64 sequences of 8192
 // tokens (GB/s over the measured copy bandwidth). f16 and bf16 fill the memory
 // system with three stages and two blocks per SM (1.00; 0.96 with tiles of 32
-// keys in two stages). q8_0 is bound by instructions and takes as many blocks
-// as registers and shared memory hold: four with two stages (0.84 with f16 and
-// 0.77 with fp32 activations, against 0.81 and 0.73 for three with three
-// stages), at dim 256 and with 16 heads two (dim 256: 0.81, against 0.71 with
-// three stages, where only one fits).
+// keys in two stages). q8_0 issues on 62 % of its cycles and waits on its own
+// results the rest, so that it takes as many blocks as registers and shared
+// memory hold: four with two stages (0.83 to 0.88 with f16 and 0.76 with fp32
+// activations; three with three stages were 0.03 to 0.04 less), at dim 256 and
+// with 16 heads two (dim 256: 0.82; 0.71 with three stages, where only one fits).
 template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
     if constexpr (FMT != QMM_KV_Q8_0) return go_with<FMT, D, HI, NT, 3, 2>(l);
     else if constexpr (D <= 128 && NT == 1) return go_with<FMT, D, HI, NT, 2, 4>(l);

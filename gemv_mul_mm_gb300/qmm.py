@@ -374,7 +374,8 @@ def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=No
     """Rotary positions on X (T, H, D): the first 2 * turns.numel() values of
     each head in pairs (i, i + rot/2) ("half") or (2i, 2i + 1)
     ("interleaved"). positions: int32 (T,); turns: qrope_turns. X may be a
-    view; out=X rotates in place. Returns out (X's type)."""
+    view; out=X rotates in place (any other overlap is refused). Returns out
+    (X's type)."""
     return (_CALL or _calls()).qrope(X, positions, turns, ROPE_LAYOUTS[layout], mscale, out, stream)
 
 
@@ -417,11 +418,12 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     """Attention of one new token per sequence, q (B, n_q_heads, head_dim), over
     the paged cache: block_table int32 (B, pages), seq_lens int32 (B,) counting
     the new token, whose key is stored already. scale defaults to
-    head_dim ** -0.5; max_len (a bound on seq_lens) to what the table holds; a
-    tighter one splits short batches better. Returns out (q's type), and lse
+    head_dim ** -0.5; max_len (a bound on seq_lens) to what the table holds. The
+    sequences are split by that bound: one several times the lengths costs up
+    to five times the time. Returns out (q's type), and lse
     (fp32, (B, n_q_heads)) if asked. The scratch comes from `workspace` (a CUDA
     uint8 tensor of qattn_decode_workspace_bytes(...) or more, of larger
-    sizes for instance), allocated here with torch if None."""
+    sizes for instance), allocated here with torch if None. out may be q."""
     return (_CALL or _calls()).qattn_decode(_fmt(fmt), q, k_cache, v_cache, block_table, seq_lens, page_size, n_kv_heads, scale,
                                             window, softcap, max_len, out, return_lse, workspace, stream)
 

@@ -382,7 +382,9 @@ QMM_API size_t qmoe_ffn_workspace_bytes(int64_t T, int top_k, int64_t d_model, i
  * rows of head_dim values (head_dim a multiple of 32):
  *   QMM_KV_F16 / QMM_KV_BF16  the values, [page_size][head_dim]
  *   QMM_KV_Q8_0               int8 codes [page_size][head_dim], then f16 scales
- *                             [page_size][head_dim / 32]; value = scale * code.
+ *                             [page_size][head_dim / 32]; value = scale * code
+ *                             (a scale of either sign; qkv_store writes none
+ *                             below zero).
  *                             The bytes per token are those of Q8_0 blocks.
  * Slot s of the cache is row s % page_size of page s / page_size.
  */
@@ -487,9 +489,16 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * length 0 gives zeros and lse = -inf. Whatever the cache holds outside the
  * range, NaN included, has no effect; an Inf or NaN inside it makes the heads
  * that see it Inf or NaN. Long sequences are split over the GPU and joined in a
- * fixed order: results are deterministic. Accumulation,
- * softmax and joins are fp32; with fp32 q the result is fp32-accurate, 16-bit
- * outputs are rounded once.
+ * fixed order: results are deterministic.
+ *
+ * Accuracy. Scores, the softmax's maximum and sum, and outputs are held in fp32;
+ * q and the weights enter the products as sums of 16-bit terms. With fp32 q (or q
+ * of another 16-bit type than the cache's; f16 for Q8_0) those carry 22 bits or
+ * more and the result is as near as a plain fp32 computation's. With q of the
+ * cache's type the weights carry 22 bits (16 over bf16), and sums over up to 16384
+ * keys are cut off, not rounded, to 24: 2^-16 and less of the result, before the
+ * output's one rounding to 16 bits. Scores in log2 units (times 1.4427) have to
+ * be finite floats, and |scale| times the largest |q| of a row below 2^136.
  *
  *   q            device, dtype, element (b, h, d) at b * q_bs + h * q_hs + d
  *   block_table  device int32, row b at b * table_stride, table_width page ids;
@@ -497,7 +506,10 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  *   seq_lens     device int32 [B], 0 .. max_len. A length outside that range,
  *                or a page id outside the cache, gives NaN in that sequence's
  *                heads and latches QMM_ERR_BAD_SLOT.
- *   max_len      host bound on seq_lens, at most table_width * page_size
+ *   max_len      host bound on seq_lens, at most table_width * page_size. The
+ *                split goes by it, not by the lengths: under a bound far above
+ *                them most of the GPU idles (one sequence of 6900 tokens, 8 heads
+ *                of 128, f16: 11 us under a bound of 6900, 60 us under 131072)
  *   window       0: the whole sequence
  *   out          device, dtype, [B][n_q_heads][head_dim]: q itself where that
  *                is contiguous, or apart from it (QMM_ERR_BAD_ARGUMENT); lse  fp32
