@@ -96,10 +96,13 @@ class AttentionLayer:
         lengths and the rows that they should have: each head's key and value
         against the weights' 64-bit products, rotated in 64 bits. Of a row's norm the product may be off
         by 4e-3 and its f16 rounding by 2^-11, twice, the cache by its
-        format's rounding (Q8_0: half a code, amax / 254, in each of 32 values)."""
+        format's rounding (Q8_0: half a code, amax / 254, in each of 32 values; Q4_0: half a
+        code, amax / 16, in 31 values, and where -8 has no opposite a whole one, of a
+        value that counts for more in the norm)."""
         if not torch.equal(self.lens, lens + steps):
             raise RuntimeError(f"lengths are {self.lens.tolist()}, not {(lens + steps).tolist()}")
-        bound = 4e-3 + 2 * 2.0 ** -11 + {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "q8_0": 32 ** 0.5 / 254 * (1 + 2.0 ** -9)}[self.fmt]
+        bound = 4e-3 + 2 * 2.0 ** -11 + {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "q8_0": 32 ** 0.5 / 254 * (1 + 2.0 ** -9),
+                                        "q4_0": 31 ** 0.5 / 16 * (1 + 2.0 ** -8)}[self.fmt]
         for b, n in enumerate(lens.tolist()):
             at = torch.arange(n + steps, device="cuda")
             _, k, v = self.plain_heads(torch.cat([x[b, :n], token[b].expand(steps, -1)]))

@@ -1,8 +1,8 @@
 """Builds libqmm.so in-tree with nvcc for sm_103a (no cmake).
 
 Each .cu translation unit compiles in parallel into an object, then one
-link step makes the shared library. csrc/pycall.c, the CPython bindings of the
-serving operators, becomes an extension module named for this Python's ABI;
+link step makes the shared library. csrc/pycall*.c, the CPython bindings of the
+serving operators, become an extension module named for this Python's ABI;
 without Python's headers the library is built all the same. Used by
 ``__graft_entry__.build()`` and by the Python binding when the library is
 missing or stale.
@@ -23,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
 PYCALL_SRC = os.path.join(CSRC, "pycall.c")
+PYCALL_LAYER_SRC = os.path.join(CSRC, "pycall_layer.c")
 PYCALL = os.path.join(HERE, "_pycall" + sysconfig.get_config_var("EXT_SUFFIX"))
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -66,21 +67,21 @@ def _compile(src: str, extra) -> str:
 def build_pycall(force: bool = False) -> Optional[str]:
     """The extension module, or None where Python's headers or a C compiler are
     missing (qmm then says so when one of its operators is called)."""
-    deps = [PYCALL_SRC, os.path.join(ROOT, "include", "qmm.h")]
+    deps = [PYCALL_SRC, PYCALL_LAYER_SRC, os.path.join(CSRC, "pycall.h"), os.path.join(ROOT, "include", "qmm.h")]
     if not force and os.path.exists(PYCALL) and all(os.path.getmtime(f) <= os.path.getmtime(PYCALL) for f in deps):
         return PYCALL
     cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
     include = sysconfig.get_paths()["include"]
     missing = "a C compiler" if cc is None else "" if os.path.exists(os.path.join(include, "Python.h")) else "Python.h"
     if missing:
-        sys.stderr.write(f"{missing} not found: built without the Python bindings of qrope, qkv_store, qkv_load and qattn_decode\n")
+        sys.stderr.write(f"{missing} not found: built without the Python bindings of qrope, qkv_store, qkv_load, qattn_decode, qrmsnorm and qmoe_route\n")
         return None
     tmp = PYCALL + ".tmp"
     cmd = [cc, "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", include,
-           "-I", os.path.join(ROOT, "include"), PYCALL_SRC, "-o", tmp]
+           "-I", os.path.join(ROOT, "include"), "-I", CSRC, PYCALL_SRC, PYCALL_LAYER_SRC, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed for pycall.c:\n{r.stderr}")
+        raise RuntimeError(f"{cc} failed for the bindings:\n{r.stderr}")
     os.replace(tmp, PYCALL)
     return PYCALL
 

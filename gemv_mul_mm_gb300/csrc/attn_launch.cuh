@@ -1,5 +1,5 @@
 // attn_launch.cuh -- the kernel choice of one cache format (included by one
-// translation unit per format).
+// translation unit per format; that of q4_0 defines QMM_ATTN_Q4).
 #pragma once
 
 #include <atomic>
@@ -10,11 +10,9 @@ namespace qmm {
 namespace attn {
 
 // Shared memory beyond 48 KB has to be allowed once per kernel and device; the
-// resident blocks are looked up at the same time.
-template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
-    constexpr int bytes = Layout<FMT, D, NT, STAGES>::BYTES, kDevices = 64;
-    auto kernel = k_attn<FMT, D, HI, NT, STAGES, MINB>;
-    static std::atomic<int> fits[kDevices];
+// resident blocks are looked up at the same time (`fits`, one of each kernel).
+constexpr int kDevices = 64;
+template <typename K> cudaError_t launch_kernel(const Launch& l, K kernel, int bytes, std::atomic<int> (&fits)[kDevices]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -37,6 +35,21 @@ template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_
                           l.p.head_chunks);
 }
 
+#ifdef QMM_ATTN_Q4
+template <int D, bool HI, int NT, int SUB, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
+    static std::atomic<int> fits[kDevices];
+    return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB>, Layout4<D, NT, SUB, STAGES>::BYTES, fits);
+}
+
+template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
+    return go_with<D, HI, NT, 2, 2, D <= 128 && NT == 1 ? 3 : 2>(l);
+}
+#else
+template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
+    static std::atomic<int> fits[kDevices];
+    return launch_kernel(l, k_attn<FMT, D, HI, NT, STAGES, MINB>, Layout<FMT, D, NT, STAGES>::BYTES, fits);
+}
+
 // Depth of a warp's ring and blocks per SM, measured on 64 sequences of 8192
 // tokens (GB/s over the measured copy bandwidth). f16 and bf16 fill the memory
 // system with three stages and two blocks per SM (1.00; 0.96 with tiles of 32
@@ -50,6 +63,7 @@ template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
     else if constexpr (D <= 128 && NT == 1) return go_with<FMT, D, HI, NT, 2, 4>(l);
     else return go_with<FMT, D, HI, NT, 2, 2>(l);
 }
+#endif
 
 template <int FMT, int D> cudaError_t pick(const Launch& l, bool hi, int tiles) {
     if constexpr (D <= 128) {

@@ -66,6 +66,7 @@ cudaError_t launch_one(const Launch& l, int fmt, int D) {
     switch (fmt) {
     case QMM_KV_F16: return launch_fmt<QMM_KV_F16>(l, D, l.p.hi, l.p.tiles);
     case QMM_KV_BF16: return launch_fmt<QMM_KV_BF16>(l, D, l.p.hi, l.p.tiles);
+    case QMM_KV_Q4_0: return launch_fmt<QMM_KV_Q4_0>(l, D, l.p.hi, l.p.tiles);
     default: return launch_fmt<QMM_KV_Q8_0>(l, D, l.p.hi, l.p.tiles);
     }
 }
@@ -90,7 +91,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     if (e != cudaSuccess) return e;
     const int64_t items = B * Hkv * p->head_chunks;
     const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + 15) : max_len;
-    constexpr int64_t step = attn::kWarps * 16;
+    const int64_t step = attn::kWarps * (fmt == QMM_KV_Q4_0 ? 32 : 16);   // keys that a block's warps take at once
     const int64_t steps = (keys + step - 1) / step;
     // The split count n with the least expected time, in steps of 64 keys (an SM
     // takes 0.5 to 0.7 us for one, and q8_0 a quarter more for each block
@@ -100,11 +101,12 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     // blocks, or are powers of two. Lengths are known on the device only: a
     // batch is taken to be anything between its bound and half of it. A
     // smaller count wins within 3 %.
+    const bool blocks_hide = fmt == QMM_KV_Q8_0 || fmt == QMM_KV_Q4_0;   // bound by latencies that other blocks hide
     auto busiest = [&](double blocks, int64_t per) {
         const double load = blocks / sms, waves = std::ceil(load / resident);
-        const double idle = fmt == QMM_KV_Q8_0 && load < resident ? resident - std::ceil(load) : 0.0;
+        const double idle = blocks_hide && load < resident ? resident - std::ceil(load) : 0.0;
         return (load <= resident ? std::ceil(load) : load + 0.5) * (1.0 + 0.25 * idle) * static_cast<double>(per) + 8.0 +
-               (fmt == QMM_KV_Q8_0 || resident == 1 ? 8.0 : 2.0) * (waves - 1);
+               (blocks_hide || resident == 1 ? 8.0 : 2.0) * (waves - 1);
     };
     auto cost = [&](int64_t n, int64_t per) {
         const double full = busiest(static_cast<double>(items) * n, per);
@@ -114,7 +116,8 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     // Without HI the MMAs sum a block's keys, cutting off bits (see the kernel):
     // 16384 keys are 1.2e-5 of the result, little against a 16-bit output's own
     // rounding, and more are not taken.
-    const int64_t least = p->hi ? 1 : (steps + 255) / 256;
+    // Over q4_0 they are summed with rounding.
+    const int64_t least = p->hi || fmt == QMM_KV_Q4_0 ? 1 : (steps + 255) / 256;
     // More than 64 blocks per SM are not made (only sequences of a million
     // keys and batches that nearly fill the memory would take them): the workspace
     // has a bound that grows with the sizes, though the count itself does not.

@@ -7,81 +7,16 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "kv_common.cuh"
+#include "quant.cuh"
 
 namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int N = 8;
-
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// a / 127 rounded once, for 0 <= a < 2^128 away from subnormal quotients (which
-// f16 rounds to 0): the product with the rounded reciprocal, corrected once by
-// its exact remainder (Markstein's scheme).
-__device__ __forceinline__ float over_127(float a) {
-    constexpr float r = 1.f / 127.f;
-    const float q = a * r;
-    return fmaf(fmaf(-q, 127.f, a), r, q);
-}
-
-// Q8_0: d = f16(max |x| / 127), code = rint(x / d) in [-127, 127], each division
-// rounded once; a block of zeros (or whose d underflows) has d = 0 and codes
-// 0. A block that holds an Inf or NaN, or whose d overflows f16, gets d = NaN
-// and reads back as NaN, so that a bad activation stays visible.
-//
-// x / d is first taken as x * (1 / d), off by less than 2^-15 at |x / d| <= 128:
-// only quotients that near to half an integer can round the other way, and
-// only lanes that hold one divide (once in some thousand values). Adding 1.5 *
-// 2^23 rounds to an integer and leaves its low byte in the low byte.
-__device__ __forceinline__ void quant8(const float (&x)[N], uint2& codes, __half& d) {
-    float amax = fabsf(x[0]);
-#pragma unroll
-    for (int j = 1; j < N; ++j) amax = max_nan(amax, fabsf(x[j]));
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    d = __float2half_rn(over_127(amax));
-    const float df = __half2float(d);
-    if (!(df < INFINITY)) d = __ushort_as_half(0x7fff);
-    codes = make_uint2(0u, 0u);
-    if (!(df > 0.f && df < INFINITY)) return;
-    constexpr float kRound = 12582912.f;
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df));
-    float q[N];
-    float off = 0.f;                     // the largest distance of a quotient from its integer
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float2 v = make_float2(x[j], x[j + 1]), rr = make_float2(r, r);
-        const float2 n = fma2(v, rr, make_float2(kRound, kRound));
-        const float2 m = fma2(n, make_float2(-1.f, -1.f), make_float2(kRound, kRound));   // minus the integer
-        const float2 e = fma2(v, rr, m);
-        off = fmaxf(fmaxf(off, fabsf(e.x)), fabsf(e.y));
-        q[j] = n.x;
-        q[j + 1] = n.y;
-    }
-    // a subnormal d is coarse: quotients reach 190 and are clamped
-    if (off > 0.49996f || df < 6.103515625e-05f) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) q[j] = fmaxf(-127.f, fminf(127.f, rintf(__fdiv_rn(x[j], df)))) + kRound;
-    }
-    unsigned w[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const unsigned a = __byte_perm(__float_as_uint(q[4 * k]), __float_as_uint(q[4 * k + 1]), 0x0040);
-        const unsigned b = __byte_perm(__float_as_uint(q[4 * k + 2]), __float_as_uint(q[4 * k + 3]), 0x0040);
-        w[k] = __byte_perm(a, b, 0x5410);
-    }
-    codes = make_uint2(w[0], w[1]);
-}
+constexpr int N = kQuantN;
 
 // Where a thread's eight elements of a row go: the same place in every head's
-// unit. All 32 lanes of a warp call put8 together (quant8 shuffles); lanes with
+// unit. All 32 lanes of a warp call put8 together (quant8 and quant4 shuffle); lanes with
 // `writes` false write nothing.
 template <int FMT>
 __device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t row, int e, const float (&x)[N], bool writes) {
@@ -93,6 +28,14 @@ __device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t ro
         *reinterpret_cast<uint2*>(unit + row * c.D + e) = codes;
         if (e % 32 == 0)
             reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
+    } else if constexpr (FMT == QMM_KV_Q4_0) {
+        unsigned codes;
+        __half d;
+        quant4(x, codes, d);
+        if (!writes) return;
+        *reinterpret_cast<unsigned*>(unit + row * (c.D / 2) + e / 2) = codes;
+        if (e % 32 == 0)
+            reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D / 2) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
     } else {
         if (!writes) return;
         using T = typename std::conditional<FMT == QMM_KV_F16, __half, __nv_bfloat16>::type;
@@ -315,7 +258,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_load(KvLoadArgs a, int64_t thre
     const int64_t row = slot & ((1ll << a.c.page_shift) - 1);
     const int64_t unit = a.c.unit();
     const uint8_t* base = (is_v ? a.c.v : a.c.k) + (slot >> a.c.page_shift) * a.c.page_stride;
-    const int64_t at = row * a.c.D + e, scale_at = (static_cast<int64_t>(a.c.D) << a.c.page_shift) + (row * (a.c.D / 32) + e / 32) * 2;
+    const int64_t row_bytes = kv_code_bytes(FMT, a.c.D);
+    const int64_t at = FMT == QMM_KV_Q4_0 ? row * row_bytes + e / 2 : row * a.c.D + e;
+    const int64_t scale_at = (row_bytes << a.c.page_shift) + (row * (a.c.D / 32) + e / 32) * 2;   // Q8_0, Q4_0
 #pragma unroll 1
     for (int h = h0; h < h1; h += kB) {
         using S = typename std::conditional<FMT == QMM_KV_BF16, __nv_bfloat16, __half>::type;
@@ -327,6 +272,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_load(KvLoadArgs a, int64_t thre
             const uint8_t* p = base + min(h + k, h1 - 1) * unit;
             if constexpr (FMT == QMM_KV_Q8_0) {
                 w[k] = *reinterpret_cast<const uint2*>(p + at);
+                d[k] = *reinterpret_cast<const __half*>(p + scale_at);
+            } else if constexpr (FMT == QMM_KV_Q4_0) {
+                w[k].x = *reinterpret_cast<const unsigned*>(p + at);
                 d[k] = *reinterpret_cast<const __half*>(p + scale_at);
             } else {
                 v[k].load(reinterpret_cast<const S*>(p) + at);
@@ -343,6 +291,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_load(KvLoadArgs a, int64_t thre
 #pragma unroll
                 for (int j = 0; j < N; ++j)
                     f[j] = df * (__uint_as_float(__byte_perm(u[j / 4], 0x4b000000u, 0x7440 + j % 4)) - 8388736.f);
+            } else if constexpr (FMT == QMM_KV_Q4_0) {
+                // code + 8 in the low bits of 2^23, less 2^23 + 8: exact
+                const float df = __half2float(d[k]);
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = df * (__uint_as_float((w[k].x >> (4 * j) & 15u) | 0x4b000000u) - 8388616.f);
             } else {
                 v[k].get(f);
             }
@@ -393,6 +346,7 @@ template <typename T> cudaError_t store(const KvStoreArgs& a, cudaStream_t s) {
     switch (a.c.fmt) {
     case QMM_KV_F16: return pick(std::integral_constant<int, QMM_KV_F16>{});
     case QMM_KV_BF16: return pick(std::integral_constant<int, QMM_KV_BF16>{});
+    case QMM_KV_Q4_0: return pick(std::integral_constant<int, QMM_KV_Q4_0>{});
     default: return pick(std::integral_constant<int, QMM_KV_Q8_0>{});
     }
 }
@@ -406,6 +360,7 @@ template <typename T> cudaError_t load(const KvLoadArgs& a, cudaStream_t s) {
     switch (a.c.fmt) {
     case QMM_KV_F16: return go(k_kv_load<T, QMM_KV_F16>);
     case QMM_KV_BF16: return go(k_kv_load<T, QMM_KV_BF16>);
+    case QMM_KV_Q4_0: return go(k_kv_load<T, QMM_KV_Q4_0>);
     default: return go(k_kv_load<T, QMM_KV_Q8_0>);
     }
 }

@@ -1,0 +1,389 @@
+// k_norm.cu -- qrmsnorm: RMS norm of rows, with the residual's addition before it.
+//
+//   h = x + r,  r' = h,  y = h / sqrt(mean(h^2) + eps) * (w + o)
+//
+// Bound by reading x and r and writing r' and y once each: a row stays in
+// registers between the sum of squares and the product. A thread holds
+// vectors of N elements (eight, or one where a row's size, strides or addresses
+// do not allow 16-byte accesses); short rows take part of a warp each, long ones
+// a block each, and rows that no block can hold are read twice.
+#include <algorithm>
+
+#include "layer_common.cuh"
+#include "quant.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kWide = 256;       // threads of a block of short rows
+
+__device__ __forceinline__ float warp_sum(float v, int width) {
+    for (int o = width / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// N elements as they lie in memory, of a type known at run time (a branch that
+// a whole grid takes alike).
+template <int N> struct Raw;
+template <> struct Raw<8> {
+    uint4 a, b;
+    template <bool ALIGNED> __device__ __forceinline__ void load(const void* p, int64_t i, int dt) {
+        if constexpr (ALIGNED) {
+            if (dt == QMM_F32) {
+                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+                a = q[0];
+                b = q[1];
+            } else {
+                a = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(p) + i);
+            }
+        } else {
+            unsigned* u = &a.x;
+            if (dt == QMM_F32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) (j < 4 ? u[j] : (&b.x)[j - 4]) = static_cast<const unsigned*>(p)[i + j];
+            } else {
+                const unsigned short* q = static_cast<const unsigned short*>(p) + i;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] = q[2 * j] | static_cast<unsigned>(q[2 * j + 1]) << 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8], int dt) const {
+        const unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (dt == QMM_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+        } else if (dt == QMM_F16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                x[2 * j] = f.x;
+                x[2 * j + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+};
+template <> struct Raw<1> {
+    float v;
+    template <bool ALIGNED> __device__ __forceinline__ void load(const void* p, int64_t i, int dt) {
+        v = dt == QMM_F32   ? static_cast<const float*>(p)[i]
+            : dt == QMM_F16 ? __half2float(static_cast<const __half*>(p)[i])
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    }
+    __device__ __forceinline__ void get(float (&x)[1], int) const { x[0] = v; }
+};
+
+template <int N, bool ALIGNED>
+__device__ __forceinline__ void put(void* p, int64_t i, int dt, const float (&x)[N]) {
+    if constexpr (ALIGNED && N > 1) {
+        if (dt == QMM_F32) {
+            Vec<float, N> v;
+            v.set(x);
+            v.store(static_cast<float*>(p) + i);
+        } else if (dt == QMM_F16) {
+            Vec<__half, N> v;
+            v.set(x);
+            v.store(static_cast<__half*>(p) + i);
+        } else {
+            Vec<__nv_bfloat16, N> v;
+            v.set(x);
+            v.store(static_cast<__nv_bfloat16*>(p) + i);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (dt == QMM_F32) static_cast<float*>(p)[i + j] = x[j];
+            else if (dt == QMM_F16) static_cast<__half*>(p)[i + j] = __float2half_rn(x[j]);
+            else static_cast<__nv_bfloat16*>(p)[i + j] = __float2bfloat16_rn(x[j]);
+        }
+    }
+}
+
+// Eight elements a lane as Q8_0 blocks: a warp's 256 elements are 272 bytes, put
+// together in shared memory and written in the widest accesses their address
+// allows. `to`: the bytes of the warp's first block; lanes from `lanes` on hold nothing.
+__device__ __forceinline__ void put_q8(uint8_t* to, uint8_t* stage, int lane, int lanes, const float (&x)[8]) {
+    uint2 codes;
+    __half d;
+    quant8(x, codes, d);
+    unsigned short* s = reinterpret_cast<unsigned short*>(stage + lane / 4 * 34);
+    if (lane % 4 == 0) s[0] = __half_as_ushort(d);
+    s += 1 + lane % 4 * 4;
+    s[0] = static_cast<unsigned short>(codes.x);
+    s[1] = static_cast<unsigned short>(codes.x >> 16);
+    s[2] = static_cast<unsigned short>(codes.y);
+    s[3] = static_cast<unsigned short>(codes.y >> 16);
+    __syncwarp();
+    const int bytes = lanes / 4 * 34;
+    if (reinterpret_cast<uintptr_t>(to) % 16 == 0 && bytes % 16 == 0) {
+        for (int i = lane; i < bytes / 16; i += 32) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(stage)[i];
+    } else {
+        for (int i = lane; i < bytes / 2; i += 32)
+            reinterpret_cast<unsigned short*>(to)[i] = reinterpret_cast<const unsigned short*>(stage)[i];
+    }
+    __syncwarp();
+}
+
+struct Row {
+    int64_t x, r, ro, y;
+};
+__device__ __forceinline__ Row row_of(const NormArgs& a, int64_t row) {
+    int64_t t = row;
+    int h = 0;
+    if (a.H > 1) div_mod(row, static_cast<int>(a.H), t, h);
+    return {t * a.x_ts + h * a.x_hs, t * a.r_ts + h * a.r_hs, t * a.ro_ts + h * a.ro_hs, t * a.y_ts + h * a.y_hs};
+}
+
+// y = (h * inv) * (w + o)
+template <int N, bool ALIGNED> __device__ __forceinline__ void weights(const NormArgs& a, int64_t e, float (&w)[N]) {
+    if (!a.W) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = 1.f;
+        return;
+    }
+    if constexpr (ALIGNED && N > 1) {
+        Vec<float, N> v;
+        v.load(a.W + e);
+        v.get(w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = a.W[e + j];
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] += a.w_off;
+}
+
+// A row in `group` threads of a warp (a power of two), ITEMS vectors a thread.
+template <int N, bool ALIGNED, int ITEMS>
+__global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ NormArgs a, int group, int64_t rows) {
+    grid_dep_launch();
+    grid_dep_wait();
+    __shared__ __align__(16) uint8_t stage[N == 8 ? kWide / 32 : 1][272];
+    const int lane = threadIdx.x % 32, in = lane % group;
+    const int64_t warp = blockIdx.x * static_cast<int64_t>(kWide / 32) + threadIdx.x / 32;
+    const int per = 32 / group;
+    const int64_t row = warp * per + lane / group;
+    const bool live = row < rows;
+    const Row at = row_of(a, live ? row : rows - 1);
+    Raw<N> x[ITEMS], r[ITEMS];
+    const bool res = a.R != nullptr;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * group + in) * N;
+        if (e < a.D) {
+            x[k].template load<ALIGNED>(a.X, at.x + e, a.x_dt);
+            if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+        }
+    }
+    float h[ITEMS][N], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * group + in) * N;
+        if (e < a.D) {
+            x[k].get(h[k], a.x_dt);
+            if (res) {
+                float f[N];
+                r[k].get(f, a.r_dt);
+#pragma unroll
+                for (int j = 0; j < N; ++j) h[k][j] += f[j];
+                if (a.RO && live) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+        }
+    }
+    const float inv = rsqrtf(warp_sum(ss, group) / static_cast<float>(a.D) + a.eps);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * group + in) * N;
+        const bool mine = e < a.D;
+        float w[N];
+        if (mine) {
+            weights<N, ALIGNED>(a, e, w);
+#pragma unroll
+            for (int j = 0; j < N; ++j) h[k][j] = h[k][j] * inv * w[j];
+        }
+        if constexpr (N == 8) {
+            if (a.y_fmt == QMM_NORM_Q8_0) {          // one row a warp
+                const int left = (static_cast<int>(a.D) - k * 256) / 8;
+                if (left <= 0) continue;
+                uint8_t* to = static_cast<uint8_t*>(a.Y) + at.y + k * 272;
+                if (!mine)
+                    for (int j = 0; j < N; ++j) h[k][j] = 0.f;
+                put_q8(to, stage[threadIdx.x / 32], lane, live ? min(32, left) : 0, h[k]);
+                continue;
+            }
+        }
+        if (mine && live) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h[k]);
+    }
+}
+
+// A row a block.
+template <int N, bool ALIGNED, int ITEMS>
+__global__ void __launch_bounds__(1024) k_norm_block(const __grid_constant__ NormArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    __shared__ __align__(16) uint8_t stage[N == 8 ? 32 : 1][272];
+    __shared__ float part[32];
+    const int lane = threadIdx.x % 32, wid = threadIdx.x / 32, threads = static_cast<int>(blockDim.x);
+    const Row at = row_of(a, blockIdx.x);
+    Raw<N> x[ITEMS], r[ITEMS];
+    const bool res = a.R != nullptr;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        if (e < a.D) {
+            x[k].template load<ALIGNED>(a.X, at.x + e, a.x_dt);
+            if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+        }
+    }
+    float h[ITEMS][N], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        if (e < a.D) {
+            x[k].get(h[k], a.x_dt);
+            if (res) {
+                float f[N];
+                r[k].get(f, a.r_dt);
+#pragma unroll
+                for (int j = 0; j < N; ++j) h[k][j] += f[j];
+                if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+        }
+    }
+    ss = warp_sum(ss, 32);
+    if (lane == 0) part[wid] = ss;
+    __syncthreads();
+    ss = warp_sum(lane < threads / 32 ? part[lane] : 0.f, 32);
+    const float inv = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        const bool mine = e < a.D;
+        if (mine) {
+            float w[N];
+            weights<N, ALIGNED>(a, e, w);
+#pragma unroll
+            for (int j = 0; j < N; ++j) h[k][j] = h[k][j] * inv * w[j];
+        }
+        if constexpr (N == 8) {
+            if (a.y_fmt == QMM_NORM_Q8_0) {
+                const int first = (k * threads + wid * 32) * 8, left = (static_cast<int>(a.D) - first) / 8;
+                if (left <= 0) continue;
+                uint8_t* to = static_cast<uint8_t*>(a.Y) + at.y + first / 32 * 34;
+                if (!mine)
+                    for (int j = 0; j < N; ++j) h[k][j] = 0.f;
+                put_q8(to, stage[wid], lane, min(32, left), h[k]);
+                continue;
+            }
+        }
+        if (mine) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h[k]);
+    }
+}
+
+// Rows too long for a block's registers: x and r are read again for the product
+// (r' may be r or x, so that it is written with y).
+template <int N, bool ALIGNED>
+__global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ NormArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    __shared__ __align__(16) uint8_t stage[N == 8 ? 32 : 1][272];
+    __shared__ float part[32];
+    const int lane = threadIdx.x % 32, wid = threadIdx.x / 32, threads = static_cast<int>(blockDim.x);
+    const Row at = row_of(a, blockIdx.x);
+    const bool res = a.R != nullptr;
+    auto sum_of = [&](int64_t e, float (&h)[N]) {
+        Raw<N> x, r;
+        x.template load<ALIGNED>(a.X, at.x + e, a.x_dt);
+        if (res) r.template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+        x.get(h, a.x_dt);
+        if (res) {
+            float f[N];
+            r.get(f, a.r_dt);
+#pragma unroll
+            for (int j = 0; j < N; ++j) h[j] += f[j];
+        }
+    };
+    float ss = 0.f;
+    for (int64_t e = threadIdx.x * N; e < a.D; e += threads * N) {
+        float h[N];
+        sum_of(e, h);
+#pragma unroll
+        for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
+    }
+    ss = warp_sum(ss, 32);
+    if (lane == 0) part[wid] = ss;
+    __syncthreads();
+    ss = warp_sum(lane < threads / 32 ? part[lane] : 0.f, 32);
+    const float inv = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
+    // a warp's lanes stay together: they share blocks of the 8-bit output
+    for (int64_t first = wid * 32 * N; first < a.D; first += threads * N) {
+        const int64_t e = first + lane * N;
+        const bool mine = e < a.D;
+        float h[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[j] = 0.f;
+        if (mine) {
+            sum_of(e, h);
+            if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h);
+            float w[N];
+            weights<N, ALIGNED>(a, e, w);
+#pragma unroll
+            for (int j = 0; j < N; ++j) h[j] = h[j] * inv * w[j];
+        }
+        if constexpr (N == 8) {
+            if (a.y_fmt == QMM_NORM_Q8_0) {
+                put_q8(static_cast<uint8_t*>(a.Y) + at.y + first / 32 * 34, stage[wid], lane,
+                       static_cast<int>(imin64(32, (a.D - first) / 8)), h);
+                continue;
+            }
+        }
+        if (mine) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h);
+    }
+}
+
+template <int N, bool ALIGNED> cudaError_t run(const NormArgs& a, cudaStream_t s) {
+    const int64_t rows = a.T * a.H, vecs = (a.D + N - 1) / N;
+    if (rows > 0x7fffffff) return cudaErrorInvalidValue;
+    if (vecs <= 64) {
+        const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
+        int group = q8 ? 32 : 1;
+        while (group < 32 && group < vecs) group *= 2;
+        const int64_t per_block = kWide / group, blocks = (rows + per_block - 1) / per_block;
+        auto go = [&](auto k) { return launch_chained(k, dim3(static_cast<unsigned>(blocks)), kWide, 0, s, a, group, rows); };
+        return vecs <= 32 ? go(k_norm_warp<N, ALIGNED, 1>) : go(k_norm_warp<N, ALIGNED, 2>);
+    }
+    const dim3 grid(static_cast<unsigned>(rows));
+    auto threads = [&](int items) { return static_cast<int>((vecs + items * 32 - 1) / (items * 32)) * 32; };
+    auto go = [&](auto k, int items) { return launch_chained(k, grid, threads(items), 0, s, a); };
+    if (vecs <= 512) return go(k_norm_block<N, ALIGNED, 1>, 1);
+    if (vecs <= 1024) return go(k_norm_block<N, ALIGNED, 2>, 2);
+    if (vecs <= 4096) return go(k_norm_block<N, ALIGNED, 4>, 4);
+    return launch_chained(k_norm_long<N, ALIGNED>, grid, 1024, 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+    auto size = [](int dt) { return static_cast<int64_t>(dt == QMM_F32 ? 4 : 2); };
+    const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
+    auto ok = [&](const void* p, int64_t ts, int64_t hs, int64_t sz) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.T == 1 || ts * sz % 16 == 0) && (a.H == 1 || hs * sz % 16 == 0);
+    };
+    const bool vec = a.D % 8 == 0 && ok(a.X, a.x_ts, a.x_hs, size(a.x_dt)) && (!a.R || ok(a.R, a.r_ts, a.r_hs, size(a.r_dt))) &&
+                     (!a.RO || ok(a.RO, a.ro_ts, a.ro_hs, size(a.r_dt))) && ok(a.W, 0, 0, 4) &&
+                     (q8 || ok(a.Y, a.y_ts, a.y_hs, size(a.y_fmt)));
+    if (vec) return run<8, true>(a, s);
+    return q8 ? run<8, false>(a, s) : run<1, false>(a, s);
+}
+
+}  // namespace qmm

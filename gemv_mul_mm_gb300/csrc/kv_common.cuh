@@ -11,10 +11,18 @@ namespace qmm {
 // p * page_stride; in it each head has one contiguous unit:
 //   f16 / bf16   [page_size][D] values
 //   q8_0         [page_size][D] int8 codes, then [page_size][D / 32] f16 scales
+//   q4_0         [page_size][D / 2] bytes of two 4-bit codes plus 8, then the scales
 // (value = scale * code). Codes and scales apart keep every vector access
-// aligned; the bytes per row are those of 34-byte Q8_0 blocks.
+// aligned; the bytes per row are those of 34-byte Q8_0 and 18-byte Q4_0 blocks.
+__host__ __device__ constexpr bool kv_fmt_ok(int fmt) {
+    return fmt == QMM_KV_F16 || fmt == QMM_KV_BF16 || fmt == QMM_KV_Q8_0 || fmt == QMM_KV_Q4_0;
+}
+// Bytes of a row's codes or values, without scales.
+__host__ __device__ constexpr int64_t kv_code_bytes(int fmt, int64_t D) {
+    return fmt == QMM_KV_Q8_0 ? D : fmt == QMM_KV_Q4_0 ? D / 2 : 2 * D;
+}
 __host__ __device__ __forceinline__ size_t kv_row_bytes(int fmt, int64_t D) {
-    return static_cast<size_t>(fmt == QMM_KV_Q8_0 ? D + D / 16 : 2 * D);
+    return static_cast<size_t>(kv_code_bytes(fmt, D) + (fmt == QMM_KV_Q8_0 || fmt == QMM_KV_Q4_0 ? D / 16 : 0));
 }
 
 struct KvCache {

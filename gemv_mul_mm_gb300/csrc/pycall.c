@@ -1,6 +1,6 @@
 /*
  * pycall.c -- CPython bindings of the rotary, cache and attention operators
- * (include/qmm.h), used by qmm.py.
+ * (include/qmm.h), used by qmm.py, and what those of pycall_layer.c share with them.
  *
  * A call on a decode step costs more on the host than on the GPU: through
  * ctypes and Python-level checks qrope took 7.6 us and qattn_decode 15 us, of
@@ -9,12 +9,7 @@
  * through their Python attributes, and what else is needed of torch (element
  * types, the current stream, an allocator) is handed over once by setup().
  */
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <stdint.h>
-
-#include "qmm.h"
+#include "pycall.h"
 
 /* ---- what setup() hands over */
 
@@ -25,8 +20,7 @@ static __typeof__(&qattn_decode) f_qattn_decode;
 static __typeof__(&qattn_decode_workspace_bytes) f_ws_bytes;
 static __typeof__(&qattn_decode_splits) f_splits;
 
-static PyObject *dt_act[3];               /* torch.float32, float16, bfloat16: qmm_dtype order */
-static PyObject *dt_i32, *dt_i64, *dt_u8;
+PyObject *dt_act[3], *dt_i32, *dt_i64, *dt_u8;
 static PyObject *fn_stream;               /* device index -> raw stream */
 static PyObject *fn_device;               /* () -> current device index */
 static PyObject *fn_new;                  /* (shape, strides, dtype) -> tensor on the current device and stream */
@@ -41,10 +35,10 @@ static int set_ref(PyObject **to, PyObject *o) {
 }
 
 static PyObject *setup(PyObject *self, PyObject *args) {
-    unsigned long long a[6];
+    unsigned long long a[8];
     PyObject *o[11];
     (void)self;
-    if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &a[5], &o[0], &o[1], &o[2], &o[3],
+    if (!PyArg_ParseTuple(args, "(KKKKKKKK)(OOO)OOOOOOOO", &a[0], &a[1], &a[2], &a[3], &a[4], &a[5], &a[6], &a[7], &o[0], &o[1], &o[2], &o[3],
                           &o[4], &o[5], &o[6], &o[7], &o[8], &o[9], &o[10]))
         return NULL;
     f_qrope = (__typeof__(f_qrope))(uintptr_t)a[0];
@@ -53,6 +47,8 @@ static PyObject *setup(PyObject *self, PyObject *args) {
     f_qattn_decode = (__typeof__(f_qattn_decode))(uintptr_t)a[3];
     f_ws_bytes = (__typeof__(f_ws_bytes))(uintptr_t)a[4];
     f_splits = (__typeof__(f_splits))(uintptr_t)a[5];
+    f_qrmsnorm = (__typeof__(f_qrmsnorm))(uintptr_t)a[6];
+    f_qmoe_route = (__typeof__(f_qmoe_route))(uintptr_t)a[7];
     for (int i = 0; i < 3; ++i) set_ref(&dt_act[i], o[i]);
     set_ref(&dt_i32, o[3]);
     set_ref(&dt_i64, o[4]);
@@ -66,13 +62,6 @@ static PyObject *setup(PyObject *self, PyObject *args) {
 }
 
 /* ---- tensors */
-
-typedef struct {
-    void *ptr;
-    PyObject *dtype;                      /* borrowed: element types live as long as torch */
-    int nd, dev;
-    int64_t shape[4], stride[4];
-} Ten;
 
 /* A Python int from a call, or -1 with an exception. */
 static int64_t as_i64(PyObject *o) {
@@ -94,7 +83,7 @@ static int read_dims(PyObject *t, int64_t *to, const char *what) {
     return PyErr_Occurred() ? -1 : n;
 }
 
-static int read_tensor(PyObject *o, Ten *t, const char *what) {
+int read_tensor(PyObject *o, Ten *t, const char *what) {
     PyObject *p = PyObject_CallMethodNoArgs(o, s_data_ptr);
     if (!p) {
         if (PyErr_ExceptionMatches(PyExc_AttributeError)) PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
@@ -111,16 +100,14 @@ static int read_tensor(PyObject *o, Ten *t, const char *what) {
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* The qmm_dtype of an f32 / f16 / bf16 element type, or -1 with an exception. */
-static int act_of(PyObject *dtype, const char *what) {
+int act_of(PyObject *dtype, const char *what) {
     for (int i = 0; i < 3; ++i)
         if (dtype == dt_act[i]) return i;
     PyErr_Format(PyExc_TypeError, "%s must be float32, float16 or bfloat16, got %R", what, dtype);
     return -1;
 }
 
-/* Kernels launch on the current device: the first tensor has to be there. */
-static int on_current(const Ten *t, const char *what) {
+int on_current(const Ten *t, const char *what) {
     if (t->dev < 0) {
         PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", what);
         return -1;
@@ -134,7 +121,7 @@ static int on_current(const Ten *t, const char *what) {
     return 0;
 }
 
-static int on(const Ten *t, int dev, const char *what) {
+int on(const Ten *t, int dev, const char *what) {
     if (t->dev == dev) return 0;
     PyErr_Format(PyExc_ValueError, "%s is on device %d, not on cuda:%d", what, t->dev, dev);
     return -1;
@@ -156,14 +143,14 @@ static int rows_of(const Ten *t, const char *what, size_t *n) {
     return 0;
 }
 
-static int same_shape(const Ten *a, const Ten *b) {
+int same_shape(const Ten *a, const Ten *b) {
     if (a->nd != b->nd) return 0;
     for (int i = 0; i < a->nd; ++i)
         if (a->shape[i] != b->shape[i]) return 0;
     return 1;
 }
 
-static int64_t numel(const Ten *t) {
+int64_t numel(const Ten *t) {
     int64_t n = 1;
     for (int i = 0; i < t->nd; ++i) n *= t->shape[i];
     return n;
@@ -181,8 +168,7 @@ static int contiguous(const Ten *t) {
     return 1;
 }
 
-/* Reads a contiguous tensor of `dtype` and `n` elements (-1: any) on `dev`. */
-static int want(PyObject *o, Ten *t, PyObject *dtype, int64_t n, int dev, const char *what) {
+int want(PyObject *o, Ten *t, PyObject *dtype, int64_t n, int dev, const char *what) {
     if (read_tensor(o, t, what)) return -1;
     if (t->dtype != dtype || !contiguous(t) || (n >= 0 && numel(t) != n)) {
         if (n >= 0) PyErr_Format(PyExc_ValueError, "%s must be a contiguous %R tensor of %lld elements", what, dtype, (long long)n);
@@ -220,16 +206,7 @@ static int read_cache(PyObject *ko, PyObject *vo, Cache *c) {
     return 0;
 }
 
-/* The stream of a call: the caller's handle, or the current one of `dev`. New
- * tensors come from the pool of the stream that uses them: one of the current
- * stream's could still be in use there, and a workspace would be handed out
- * again there while the kernels of the other stream run. */
-typedef struct {
-    void *handle;
-    int other;                            /* not the current stream */
-} Stream;
-
-static int stream_of(PyObject *o, int dev, Stream *s) {
+int stream_of(PyObject *o, int dev, Stream *s) {
     PyObject *d = PyLong_FromLong(dev);
     if (!d) return -1;
     PyObject *r = PyObject_CallOneArg(fn_stream, d);
@@ -249,8 +226,7 @@ static int stream_of(PyObject *o, int dev, Stream *s) {
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* A new contiguous tensor; *ptr its address. */
-static PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, const Stream *s, void **ptr) {
+PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, const Stream *s, void **ptr) {
     PyObject *sh = PyTuple_New(nd), *st = PyTuple_New(nd), *t = NULL, *p;
     int64_t n = 1;
     if (!sh || !st) goto out;
@@ -286,8 +262,7 @@ out:
     return t;
 }
 
-/* Raises for a status other than QMM_OK. */
-static int failed(int rc, const char *name) {
+int failed(int rc, const char *name) {
     if (rc == QMM_OK) return 0;
     PyObject *r = PyObject_CallFunction(fn_check, "is", rc, name);
     Py_XDECREF(r);
@@ -295,8 +270,7 @@ static int failed(int rc, const char *name) {
     return 1;
 }
 
-/* A C int, or -1 with an exception. */
-static int as_int(PyObject *o) {
+int as_int(PyObject *o) {
     const long v = PyLong_AsLong(o);
     if (v < INT32_MIN || v > INT32_MAX) {
         PyErr_SetString(PyExc_OverflowError, "integer argument out of range");
@@ -305,7 +279,7 @@ static int as_int(PyObject *o) {
     return (int)v;
 }
 
-static int nargs_are(Py_ssize_t n, Py_ssize_t want_n, const char *name) {
+int nargs_are(Py_ssize_t n, Py_ssize_t want_n, const char *name) {
     if (n == want_n && f_qrope) return 1;
     PyErr_Format(PyExc_TypeError, "%s: %zd arguments, or setup() not called", name, n);
     return 0;
@@ -538,5 +512,7 @@ PyMODINIT_FUNC PyInit__pycall(void) {
     s_dtype = PyUnicode_InternFromString("dtype");
     s_get_device = PyUnicode_InternFromString("get_device");
     if (!s_data_ptr || !s_shape || !s_stride || !s_dtype || !s_get_device) return NULL;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddFunctions(m, layer_methods)) Py_CLEAR(m);
+    return m;
 }

@@ -20,8 +20,9 @@ KINDS = ["Q8_0", "Q4_0", "Q5_0", "Q4_K", "Q5_K", "Q6_K",
          "Q2_K", "Q3_K", "IQ4_NL", "IQ4_XS", "MXFP4", "Q4_1", "Q5_1", "Q8_1"]
 KIND_ID = {k: i for i, k in enumerate(KINDS)}
 F32, F16, BF16 = 0, 1, 2
-KV_FORMATS = {"f16": 0, "bf16": 1, "q8_0": 2}
+KV_FORMATS = {"f16": 0, "bf16": 1, "q8_0": 2, "q4_0": 4}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 
 STATUS = {
@@ -36,7 +37,7 @@ STATUS = {
 STATUS_ID = {v: k for k, v in STATUS.items()}
 
 PATH_AUTO, PATH_GENERIC, PATH_GEMV, PATH_TC, PATH_DEQUANT, PATH_GROUPED, PATH_MOE, PATH_REPACKED = range(8)
-PATH_ROPE, PATH_KV_STORE, PATH_KV_LOAD, PATH_ATTN = range(8, 12)
+PATH_ROPE, PATH_KV_STORE, PATH_KV_LOAD, PATH_ATTN, PATH_NORM, PATH_ROUTE = range(8, 14)
 FLAG_WEIGHTS_CONST = 1
 FLAG_Y_F16 = 2
 FLAG_Y_BF16 = 4
@@ -94,6 +95,9 @@ def _lib():
         L.qattn_decode_workspace_bytes.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
         L.qattn_decode_workspace_bytes.restype = _SZ
         L.qattn_decode_splits.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
+        L.qrmsnorm.argtypes = [_P, _I, _SZ, _I64, _I64, _P, _I, _SZ, _I64, _I64, _P, _SZ, _I64, _I64, _P, _SZ, f32, f32, _P, _I,
+                               _SZ, _I64, _I64, _I64, _I64, _I64, _P]
+        L.qmoe_route.argtypes = [_P, _I, _SZ, _I64, _P, _I, _I, _I, _I, _I, _I, f32, _P, _P, _SZ, _I64, _I, _P]
         L.qmm_check_device_error.argtypes = [_P]
         L.qmm_selftest_wait_timeout.argtypes = [_I64, _P]
         L.qmm_set_path.argtypes = [_I]
@@ -297,7 +301,7 @@ def qmoe_ffn(kind, W_gu, gu_stride: int, W_down, down_stride: int, n_experts: in
 
 
 def _calls():
-    """The bindings in C of the operators below (csrc/pycall.c), with the entry
+    """The bindings in C of the operators below (csrc/pycall*.c), with the entry
     points of the loaded library and what they use of torch: element types, the
     raw stream of a device, the current device, a new tensor, the error check.
     The stream, the device and the allocation go around torch's Python and
@@ -327,7 +331,8 @@ def _calls():
                 return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
         entry = tuple(ctypes.cast(f, _P).value for f in
-                      (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes, L.qattn_decode_splits))
+                      (L.qrope, L.qkv_store, L.qkv_load, L.qattn_decode, L.qattn_decode_workspace_bytes, L.qattn_decode_splits,
+                       L.qrmsnorm, L.qmoe_route))
         _pycall.setup(entry, (torch.float32, torch.float16, torch.bfloat16), torch.int32, torch.int64, torch.uint8, raw, current,
                       new, new_on, _check)
         _CALL = _pycall
@@ -382,7 +387,7 @@ def qrope(X, positions, turns, layout: str = "half", mscale: float = 1.0, out=No
 def qkv_store(fmt, K, V, slots, k_cache, v_cache, page_size: int, positions=None, turns=None, layout: str = "half",
               mscale: float = 1.0, stream=None):
     """Writes K and V (T, n_kv_heads, head_dim; views allowed) to `slots` (int64
-    (T,); -1 skips a token) of a paged cache of format "f16", "bf16" or "q8_0",
+    (T,); -1 skips a token) of a paged cache of format "f16", "bf16", "q8_0" or "q4_0",
     rotating K first when positions and turns are given. k_cache, v_cache:
     (pages, bytes per page) uint8 tensors (qkv_cache)."""
     (_CALL or _calls()).qkv_store(_fmt(fmt), K, V, slots, k_cache, v_cache, page_size, positions, turns, ROPE_LAYOUTS[layout],
@@ -426,6 +431,34 @@ def qattn_decode(fmt, q, k_cache, v_cache, block_table, seq_lens, page_size: int
     sizes for instance), allocated here with torch if None. out may be q."""
     return (_CALL or _calls()).qattn_decode(_fmt(fmt), q, k_cache, v_cache, block_table, seq_lens, page_size, n_kv_heads, scale,
                                             window, softcap, max_len, out, return_lse, workspace, stream)
+
+
+def qrmsnorm(X, weight=None, eps: float = 1e-6, residual=None, residual_out=None, out=None, out_dtype=None,
+             weight_offset: float = 0.0, stream=None):
+    """RMS norm of the rows of X (T, D) or (T, H, D; views allowed), of X + residual
+    where there is one: y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset). The
+    sum h goes to residual_out, to residual itself by default. weight: fp32 (D,).
+    Returns out: X's shape, of out_dtype (X's type by default), or with "q8_0"
+    uint8 rows of Q8_0 blocks (D / 32 * 34 bytes), as qdequant and qgemm read them.
+    out=X norms in place."""
+    if out_dtype is None:
+        out_dtype = X.dtype if out is None else out.dtype
+        if str(out_dtype) == "torch.uint8":
+            out_dtype = "q8_0"
+    return (_CALL or _calls()).qrmsnorm(X, weight, eps, residual, residual_out, out, True if out_dtype == "q8_0" else out_dtype,
+                                        weight_offset, stream)
+
+
+def qmoe_route(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1, group_top: int = 1,
+               renorm: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The top_k experts of each token and their weights, (ids int32, weights fp32),
+    both (T, top_k), from the router's logits (T, n_experts). Experts are chosen by
+    score plus bias (fp32 (n_experts,)), among those of the top_groups groups whose
+    group_top largest sum to most; weights are the scores, divided by their sum if
+    renorm, times scale. Equal values go to the lower index. What qmoe_ffn takes;
+    qgemm_grouped takes ids.flatten()."""
+    return (_CALL or _calls()).qmoe_route(logits, top_k, SCORES[score], bias, groups, top_groups, group_top, renorm, scale, ids,
+                                          weights, stream)
 
 
 def selftest_wait_timeout(cycles: int, stream=None):

@@ -386,9 +386,15 @@ QMM_API size_t qmoe_ffn_workspace_bytes(int64_t T, int top_k, int64_t d_model, i
  *                             (a scale of either sign; qkv_store writes none
  *                             below zero).
  *                             The bytes per token are those of Q8_0 blocks.
+ *   QMM_KV_Q4_0               4-bit codes plus 8, [page_size][head_dim / 2] bytes
+ *                             (elements 2 j in the low and 2 j + 1 in the high half
+ *                             of byte j), then f16 scales [page_size][head_dim / 32];
+ *                             value = scale * code, code in [-8, 7], a scale
+ *                             of either sign. The bytes per token are those of
+ *                             Q4_0 blocks.
  * Slot s of the cache is row s % page_size of page s / page_size.
  */
-typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8_0 = 2 } qmm_kv_format;
+typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8_0 = 2, QMM_KV_Q4_0 = 4 } qmm_kv_format;   /* (3 is none) */
 
 /* Bytes of one page of keys (or of values); 0 for a format, page size, head
  * count or head dim the cache does not take. Host only, no CUDA call. */
@@ -451,7 +457,9 @@ QMM_API int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_
  * fp32 value beyond the f16 range becomes Inf). QMM_KV_Q8_0 quantises each 32
  * consecutive values: d = f16(max |x| / 127), code = x / d rounded to nearest,
  * in [-127, 127]; d = 0 gives codes 0; a block holding an Inf or NaN, or whose
- * d overflows f16, gets d = NaN, so that it reads back as NaN.
+ * d overflows f16, gets d = NaN, so that it reads back as NaN. QMM_KV_Q4_0 the
+ * same with d = f16(m / -8) for the value m of largest magnitude (the first of
+ * them) and codes in [-8, 7].
  *
  *   K, V     device, dtype, element (t, h, d) at t * ts + h * hs + d; sizes in
  *            elements
@@ -497,7 +505,8 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * more and the result is as near as a plain fp32 computation's. With q of the
  * cache's type the weights carry 22 bits (16 over bf16), and sums over up to 16384
  * keys are cut off, not rounded, to 24: 2^-16 and less of the result, before the
- * output's one rounding to 16 bits. Scores in log2 units (times 1.4427) have to
+ * output's one rounding to 16 bits (over Q4_0 f16 q counts as the cache's type).
+ * Scores in log2 units (times 1.4427) have to
  * be finite floats, and |scale| times the largest |q| of a row below 2^136.
  *
  *   q            device, dtype, element (b, h, d) at b * q_bs + h * q_hs + d
@@ -540,6 +549,75 @@ QMM_API int qattn_decode_splits(int fmt, int dtype, int64_t B, int n_q_heads, in
                                 int window);
 
 /*
+ * qrmsnorm -- RMS norm of T x H rows of D values, with the residual's addition
+ * before it. For each row, in fp32:
+ *
+ *   h = x + residual             (h = x without a residual)
+ *   residual_out = h             (rounded to the residual's type, if asked for)
+ *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
+ *
+ * The norm takes h before it is rounded for residual_out. H = 1 norms tokens; more
+ * norm each head of a projection's rows. A row whose sum of squares passes
+ * the fp32 range (values of about 2^60 and more) gives zeros, one that holds an
+ * Inf or NaN gives NaN.
+ *
+ *   X             device, x_dtype, element (t, h, d) at t * x_ts + h * x_hs + d
+ *   residual      device, r_dtype, the same at r_ts, r_hs, or NULL
+ *   residual_out  device, r_dtype, at ro_ts, ro_hs, or NULL; may be residual, or X
+ *                 where that has its type, with the same strides
+ *   weight        device fp32 [D], or NULL for ones (weight_offset is then not read)
+ *   Y             device, element (t, h, d) at t * y_ts + h * y_hs + d of y_fmt:
+ *                 QMM_F32, QMM_F16 or QMM_BF16 (rounded once); or
+ *                 QMM_NORM_Q8_0: rows of D / 32 Q8_0 blocks (D a multiple of 32), as
+ *                 qdequant and the products' weights have them, rounded as
+ *                 QMM_KV_Q8_0 is by qkv_store; y_ts, y_hs and y_elems then count
+ *                 bytes (strides even). Y may be X (QMM_F32 and so on of X's type) with
+ *                 the same strides.
+ * Otherwise no output shares memory with another or with an input, nor do two
+ * rows of an output (QMM_ERR_BAD_ARGUMENT). D is at most 2^20, T * H below 2^31.
+ */
+enum { QMM_NORM_Q8_0 = 16 };
+QMM_API int qrmsnorm(const void* X, int x_dtype, size_t x_elems, int64_t x_ts, int64_t x_hs, const void* residual,
+                     int r_dtype, size_t r_elems, int64_t r_ts, int64_t r_hs, void* residual_out, size_t ro_elems,
+                     int64_t ro_ts, int64_t ro_hs, const float* weight, size_t weight_elems, float weight_offset,
+                     float eps, void* Y, int y_fmt, size_t y_elems, int64_t y_ts, int64_t y_hs, int64_t T, int64_t H,
+                     int64_t D, void* stream);
+
+/* Scores of qmoe_route. */
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+
+/*
+ * qmoe_route -- the experts of each token and their weights, as qmoe_ffn and
+ * qgemm_grouped take them. For a token with logits x:
+ *
+ *   s_e = e^{x_e} / sum e^x  (softmax)  or  1 / (1 + e^{-x_e})  (sigmoid)
+ *   c_e = s_e + bias_e                  (c = s without a bias)
+ *   n_groups > 1: a group's value is the sum of its group_top (1 or 2) largest c;
+ *     the experts of the top_groups best groups stay
+ *   ids: the top_k largest c of those that stay, the largest first
+ *   w_j = s_{ids_j}, divided by their sum if renorm, times scale
+ *
+ * Equal values go to the lower index. They are compared as real numbers, not as
+ * fp32 has them: where fp32's rounding could decide (in a few rows of a thousand),
+ * the row is computed in 64 bits. Without a bias, groups of group_top 2 aside,
+ * the logits themselves are compared. A NaN logit or bias counts as the largest
+ * value; weights are NaN where the formula is (softmax: all of the token's). Logits
+ * of -Inf have s = 0, a row of only those all s = 0; a bias of -Inf puts an
+ * expert behind all others. Where the chosen scores are all zero renormalised
+ * weights are zero. Ids are always distinct and in range.
+ *
+ *   logits    device, dtype, token t's n_experts values at t * stride
+ *   bias      device fp32 [n_experts], or NULL
+ *   ids, weights  device int32 / fp32 [T][top_k]; out_elems the size of each
+ * n_experts is at most 1024, top_k and n_groups at most 32 (QMM_ERR_UNIMPLEMENTED);
+ * n_groups divides n_experts, group_top is at most a group's experts and top_k at
+ * most the experts that stay (QMM_ERR_BAD_ARGUMENT).
+ */
+QMM_API int qmoe_route(const void* logits, int dtype, size_t elems, int64_t stride, const float* bias, int score,
+                       int n_groups, int top_groups, int group_top, int top_k, int renorm, float scale, int32_t* ids,
+                       float* weights, size_t out_elems, int64_t T, int n_experts, void* stream);
+
+/*
  * qmm_check_device_error -- synchronize `stream`, then read and clear the
  * device-side error latch of the current device. Returns QMM_OK,
  * QMM_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel ran out; that kernel's
@@ -570,7 +648,8 @@ QMM_API int qmm_set_path(int path);
 /* Which kernel family the most recent successful call on this host thread
  * launched: 1 generic, 2 streaming GEMV, 3 tensor-core GEMM, 4 dequant,
  * 5 grouped GEMV, 6 MoE layer, 7 repacked (split-K) GEMV, 8 rotary, 9 cache
- * store, 10 cache load, 11 decode attention; 0 before any call. */
+ * store, 10 cache load, 11 decode attention, 12 RMS norm, 13 routing; 0 before
+ * any call. */
 QMM_API int qmm_last_path(void);
 
 /* Number of kernels this library has launched since load (all threads). */
