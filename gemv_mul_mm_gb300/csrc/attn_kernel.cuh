@@ -73,7 +73,8 @@ template <> struct Terms<QMM_KV_Q8_0, false> { static constexpr int q = 1, p = 2
 template <> struct Terms<QMM_KV_Q8_0, true> { static constexpr int q = 2, p = 2; };    // bf16, fp32 q
 
 __host__ __device__ constexpr bool needs_hi(int fmt, int dtype) {
-    return fmt == QMM_KV_BF16 ? dtype != QMM_BF16 : dtype != QMM_F16;
+    // (over q4_0 bf16 rows are scaled by a power of two and are f16 values then)
+    return fmt == QMM_KV_BF16 ? dtype != QMM_BF16 : fmt == QMM_KV_Q4_0 ? dtype == QMM_F32 : dtype != QMM_F16;
 }
 
 // d += a b
@@ -144,7 +145,7 @@ __device__ __forceinline__ void store_act(void* p, int dtype, int64_t i, float v
 }
 
 // The range of one sequence: keys [lo, len), split in chunks that start at lo
-// rounded down to 16. A length outside [0, max_len] is an error.
+// rounded down to a tile (16 keys, 32 over q4_0). A length outside [0, max_len] is an error.
 struct Range {
     int lo, lo16, len, splits;
     bool bad;
@@ -155,7 +156,7 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, int64_t b, int chun
     r.bad = r.len < 0 || r.len > a.max_len;
     if (r.bad) r.len = 0;
     r.lo = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
-    r.lo16 = r.lo & ~15;
+    r.lo16 = r.lo & (a.c.fmt == QMM_KV_Q4_0 ? ~31 : ~15);
     r.splits = (r.len - r.lo16 + chunk - 1) / chunk;
     return r;
 }

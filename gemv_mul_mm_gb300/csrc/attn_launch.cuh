@@ -41,8 +41,13 @@ template <int D, bool HI, int NT, int SUB, int STAGES, int MINB> cudaError_t go_
     return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB>, Layout4<D, NT, SUB, STAGES>::BYTES, fits);
 }
 
+// Keys per tile, depth of the ring and blocks per SM, measured on 64 sequences of 8192
+// tokens and on one of 131072 (f16 activations, 8 heads of 128). Instructions bound the
+// kernel (62 % of the issue slots, 0.57 of the copy bandwidth): tiles of 32 keys take
+// 156 and 45 us, of 16 keys 184, of 64 206 us; four blocks, for which registers
+// spill, 154 and 51; three stages 157 and 57 us. Dim 64 fits four blocks (97 us, 109 with three).
 template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
-    return go_with<D, HI, NT, 2, 2, D <= 128 && NT == 1 ? 3 : 2>(l);
+    return go_with<D, HI, NT, 2, 2, (D > 128 || NT == 2 ? 2 : D == 64 ? 4 : 3)>(l);
 }
 #else
 template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {

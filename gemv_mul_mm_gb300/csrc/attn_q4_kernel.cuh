@@ -40,17 +40,23 @@ template <int D, int NT, int SUB, int STAGES> struct Layout4 {
     static constexpr int BYTES = kWarps * RING > JOIN ? kWarps * RING : JOIN;
 };
 
+// (x & mask) | bits in one instruction.
+__device__ __forceinline__ unsigned and_or(unsigned x, unsigned mask, unsigned bits) {
+    unsigned r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
+
 // Eight codes as four f16 pairs, (0, 4), (1, 5), (2, 6), (3, 7), exactly.
 __device__ __forceinline__ void codes4_f16(unsigned w, unsigned (&p)[4]) {
-    const __half2 one = __half2half2(__ushort_as_half(0x6408));       // 1032
+    const __half2 m1032 = __half2half2(__ushort_as_half(0xe408));     // -1032
     const __half2 r16 = __half2half2(__ushort_as_half(0x2c00));       // 1 / 16
     const __half2 m72 = __half2half2(__ushort_as_half(0xd480));       // -72
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        p[2 * i] = as_u32(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), one));
-        p[2 * i + 1] = as_u32(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), r16, m72));
-        w >>= 8;
-    }
+    const unsigned v = w >> 8;
+    p[0] = as_u32(__hadd2(as_half2(and_or(w, 0x000f000fu, 0x64006400u)), m1032));
+    p[1] = as_u32(__hfma2(as_half2(and_or(w, 0x00f000f0u, 0x64006400u)), r16, m72));
+    p[2] = as_u32(__hadd2(as_half2(and_or(v, 0x000f000fu, 0x64006400u)), m1032));
+    p[3] = as_u32(__hfma2(as_half2(and_or(v, 0x00f000f0u, 0x64006400u)), r16, m72));
 }
 
 template <int D, bool HI, int NT, int SUB, int STAGES>
@@ -109,12 +115,13 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     // Pages of a 16-key half: one, or with pages of 8 one for each eight keys.
     // Keys outside the range name a page inside it, so that every address is that of
     // a page the sequence owns.
-    const bool small_pages = shift < 4;
+    const bool small_pages = shift < 4, one_page = (1 << shift) >= KT;
     auto page_id = [&](int key) { return table[max(page_lo, min(key >> shift, page_hi))]; };
     auto page_ids = [&](int base, int (&id)[SUB][2]) {
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-            id[u][0] = page_id(base + 16 * u);
+            if (u && one_page) id[u][0] = id[0][0];
+            else id[u][0] = page_id(base + 16 * u);
             if (small_pages) id[u][1] = page_id(base + 16 * u + 8);
         }
     };
@@ -127,35 +134,62 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     };
     const uint32_t ring = smem_addr(smem) + warp * Lay::RING;
     constexpr int CPR = ROW / 16;                     // 16-byte pieces of a row
-    auto load_tile = [&](int base, const int (&id)[SUB][2], uint32_t stage) {
+    // A whole tile inside one page, as most are: its rows are contiguous, and so are its scales.
+    const uint32_t dst_lane = lane / CPR * RS + lane % CPR * 16;
+    constexpr int SP = KT * C / 8;                    // pieces of K's scales, and of V's
+    const uint8_t* const k_lane = kbase + lane * 16;
+    const uint8_t* const s_lane = k_lane + (ROW << shift) + (lane >= SP ? v_minus_k - SP * 16 : 0);
+    const int64_t page_stride = a.c.page_stride;
+    auto load_whole = [&](int base, int id, uint32_t stage) {
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.c.n_pages)) {
+            bad = true;
+            id = 0;
+        }
+        const int64_t at = static_cast<int64_t>(static_cast<unsigned>(id)) * page_stride;
+        const int row = base & page_mask;
+        const uint8_t *k = k_lane + at + row * ROW, *v = k + v_minus_k, *sc = s_lane + at + row * (2 * C);
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-            const int first = base + 16 * u;
-            const uint8_t* page[2];
-            page[0] = page_at(id[u][0]);
-            page[1] = small_pages ? page_at(id[u][1]) : page[0];
-            const int row0 = first & page_mask, row1 = (first + 8) & page_mask;
+        for (int i = 0; i < KT * CPR / 32; ++i) {
+            const int q = 32 * i + lane;
+            const uint32_t dst = stage + (32 % CPR == 0 ? dst_lane + i * (32 / CPR) * RS : q / CPR * RS + q % CPR * 16);
+            copy16(dst, k + i * 512);
+            copy16(dst + Lay::V0, v + i * 512);
+        }
+#pragma unroll
+        for (int i = 0; i < (2 * SP + 31) / 32; ++i) {
+            const int q = 32 * i + lane;
+            if (2 * SP % 32 && q >= 2 * SP) break;
+            if constexpr (SP % 32 == 0) copy16(stage + Lay::S0 + q * 16, sc + (i >= SP / 32 ? v_minus_k - SP * 16 : 0) + i * 512);
+            else if constexpr (2 * SP <= 32) copy16(stage + Lay::S0 + q * 16, sc);
+            else copy16(stage + Lay::S0 + q * 16, k_lane + at + (ROW << shift) + row * (2 * C) + (q >= SP ? v_minus_k - SP * 16 : 0) + i * 512);
+        }
+    };
+    // Rows outside the range are copied like the others: they are masked by their
+    // key (K) and have weights and scales of zero (V), and codes are never NaN.
+    auto load_tile = [&](int base, const int (&id)[SUB][2], uint32_t stage) {
+        if (one_page) {
+            load_whole(base, id[0][0], stage);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {               // pages of 16 or 8 keys
+            const int first = base + 16 * u, row0 = first & page_mask, row1 = (first + 8) & page_mask;
+            const uint8_t* page0 = page_at(id[u][0]);
+            const uint8_t* page1 = small_pages ? page_at(id[u][1]) : page0;
             if (lane < 4 * C) {                       // scales: C pieces per eight keys, of K then of V
-                const int col = lane % C;
-                const uint8_t* p = (lane / C & 1 ? page[1] + row1 * (2 * C) : page[0] + row0 * (2 * C)) + (ROW << shift) + col * 16;
-                const uint32_t dst = stage + Lay::S0 + u * 32 * C + lane % (2 * C) * 16;
-                copy16(lane < 2 * C ? dst : dst + Lay::SV, lane < 2 * C ? p : p + v_minus_k);
+                const uint8_t* p = (lane / C & 1 ? page1 + row1 * (2 * C) : page0 + row0 * (2 * C)) + (ROW << shift) + lane % C * 16;
+                copy16(stage + Lay::S0 + u * 32 * C + lane % (2 * C) * 16 + (lane < 2 * C ? 0 : Lay::SV), lane < 2 * C ? p : p + v_minus_k);
             }
-            const bool partial = first < rg.lo || first + 16 > end;
+            const uint8_t* k0 = page0 + row0 * ROW + lane * 16;
+            const uint8_t* k1 = page1 + (row1 - 8) * ROW + lane * 16;
 #pragma unroll
             for (int i = 0; i < (ROW + 31) / 32; ++i) {
                 const int q = 32 * i + lane, row = q / CPR;
                 if (ROW % 32 && q >= ROW) break;
-                const uint32_t dst = stage + (16 * u + row) * RS + q % CPR * 16;
-                const uint8_t* src = (row < 8 ? page[0] + row0 * ROW : page[1] + (row1 - 8) * ROW) + q * 16;
-                if (partial) {                        // rows outside the range become zeros
-                    const int n = first + row >= rg.lo && first + row < end ? 16 : 0;
-                    copy16_or_zero(dst, src, n);
-                    copy16_or_zero(dst + Lay::V0, src + v_minus_k, n);
-                } else {
-                    copy16(dst, src);
-                    copy16(dst + Lay::V0, src + v_minus_k);
-                }
+                const uint32_t dst = stage + 16 * u * RS + (32 % CPR == 0 ? dst_lane + i * (32 / CPR) * RS : row * RS + q % CPR * 16);
+                const uint8_t* src = ((ROW / 2) % 32 == 0 ? 32 * i >= ROW / 2 : row >= 8) ? k1 : k0;
+                copy16(dst, src + i * 512);
+                copy16(dst + Lay::V0, src + v_minus_k + i * 512);
             }
         }
     };
@@ -181,7 +215,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
         sm_q[j / D][j % D] = qv[i];
     }
     __syncthreads();
-    if (HI) {                                         // f16 terms of fp32 / bf16 rows
+    {                                                 // rows scaled into the middle of f16's range
         for (int h = warp; h < 8 * NT; h += kWarps) {
             float m = 0.f;
             for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(sm_q[h][d]));
@@ -197,7 +231,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     float sc[NT][2];                                  // score scale of heads 2t, 2t + 1, to log2 units unless capped
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float f = HI ? sm_scale[8 * n + g] : 1.f;
+        const float f = sm_scale[8 * n + g];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             if (j % kWarps != warp) continue;
@@ -216,7 +250,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             sc[n][k] = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-            if (HI) sc[n][k] /= sm_scale[8 * n + 2 * t + k];
+            sc[n][k] /= sm_scale[8 * n + 2 * t + k];
         }
     }
     __syncthreads();
@@ -235,9 +269,11 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
             for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
     }
     // V's scales, of either sign, are multiplied by a power of two that keeps them
-    // at 1 or below (2, of scales from 2^15 on), one for each 32-dim block: a block
-    // of small scales keeps its bits beside one of large ones. O carries the factor.
+    // below 2 (the weights' terms below 2^15), one for each 32-dim block: a block of small
+    // scales keeps its bits beside one of large ones. O carries the factor. Scales
+    // between 2^-8 and 2 need none, and none is applied where all are 1.
     __half2 v_mul[C];
+    bool v_scaled = true;
 #pragma unroll
     for (int c = 0; c < C; ++c) v_mul[c] = __float2half2_rn(32768.f);
 
@@ -254,41 +290,50 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
         const uint8_t* scales = smem + (stage - smem_base) + Lay::S0;
         // ---- S^T = K Q^T
         float sx[SUB][NT][4];
+        __half kscale[SUB][2][C];                     // of keys g, g + 8
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
             constexpr int B = C % 4 == 0 ? 8 : C % 2 == 0 ? 4 : 2;
             using SVec = typename VecOf<B>::type;
-            __half kscale[2][C];                      // of keys g, g + 8
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 2 * C / B; ++k) {
                     const SVec x = reinterpret_cast<const SVec*>(scales + (16 * u + g + 8 * i) * (2 * C))[k];
 #pragma unroll
-                    for (int j = 0; j < B / 2; ++j) kscale[i][k * (B / 2) + j] = reinterpret_cast<const __half*>(&x)[j];
+                    for (int j = 0; j < B / 2; ++j) kscale[u][i][k * (B / 2) + j] = reinterpret_cast<const __half*>(&x)[j];
                 }
+        }
 #pragma unroll
-            for (int c2 = 0; c2 < C; c2 += 2) {
-                unsigned w[4];
-                ldsm4(w, stage + u * 16 * RS + (c2 + 1 < C ? m_lane : m_row) + 16 * c2);
+        for (int c2 = 0; c2 < C; c2 += 2) {
+            unsigned w[SUB][4];
 #pragma unroll
-                for (int c = c2; c < c2 + 2 && c < C; ++c) {
+            for (int u = 0; u < SUB; ++u) ldsm4(w[u], stage + u * 16 * RS + (c2 + 1 < C ? m_lane : m_row) + 16 * c2);
+#pragma unroll
+            for (int c = c2; c < c2 + 2 && c < C; ++c) {
+                uint2 f[NT][NQ][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) f[n][q][j] = sm_qf[(n * NQ + q) * MT + 2 * c + j][lane];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
                     unsigned x0[4], x1[4];            // keys g, g + 8
-                    codes4_f16(w[2 * (c - c2)], x0);
-                    codes4_f16(w[2 * (c - c2) + 1], x1);
+                    codes4_f16(w[u][2 * (c - c2)], x0);
+                    codes4_f16(w[u][2 * (c - c2) + 1], x1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int q = NQ - 1; q >= 0; --q)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint2 f = sm_qf[(n * NQ + q) * MT + 2 * c + j][lane];
-                                mma<false>(acc, x0[2 * j], x1[2 * j], x0[2 * j + 1], x1[2 * j + 1], f.x, f.y);
-                            }
+                            for (int j = 0; j < 2; ++j)
+                                mma<false>(acc, x0[2 * j], x1[2 * j], x0[2 * j + 1], x1[2 * j + 1], f[n][q][j].x, f[n][q][j].y);
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
-                            const float d = __half2float(kscale[i >> 1][c]);
+                            const float d = __half2float(kscale[u][i >> 1][c]);
                             const float2 x = fma2(make_float2(d, d), make_float2(acc[i], acc[i + 1]),
                                                   c == 0 ? make_float2(0.f, 0.f) : make_float2(sx[u][n][i], sx[u][n][i + 1]));
                             sx[u][n][i] = x.x;
@@ -318,7 +363,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
             return SLOW ? (sx[u][n][i] - ref[n][i & 1]) * unit : __fmul_rn(sx[u][n][i], sc[n][i & 1]) - ref[n][i & 1];
         };
         float y[SUB][NT][4];
-        bool grew = false;
+        float most = -INFINITY;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -326,8 +371,9 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     y[u][n][i] = rel(u, n, i);
-                    grew |= y[u][n][i] > kTop;
+                    most = fmaxf(most, y[u][n][i]);
                 }
+        const bool grew = most > kTop;
         // V scales of keys (2t, 2t + 1) and (2t + 8, 2t + 9) as stored
         auto v_scales = [&](unsigned (&vd)[SUB][2][C]) {
 #pragma unroll
@@ -365,19 +411,23 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                 }
         };
         unsigned vd[SUB][2][C];                       // those scales times v_mul
-        __half2 v_top = __float2half2_rn(0.f);
         v_scales(vd);
+        if (v_scaled) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) vd[u][i][c] = as_u32(__hmul2(as_half2(vd[u][i][c]), v_mul[c]));
+        }
+        unsigned v_bits = 0u;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const __half2 d = __hmul2(as_half2(vd[u][i][c]), v_mul[c]);
-                    vd[u][i][c] = as_u32(d);
-                    v_top = __hmax2(v_top, __habs2(d));
-                }
-        const bool v_grew = !__hbleu2(v_top, __float2half2_rn(1.f));
+                for (int c = 0; c < C; ++c) v_bits |= vd[u][i][c];
+        const bool v_grew = v_bits & 0x40004000u;     // an exponent of 2 and more
         if (__any_sync(0xffffffffu, grew || v_grew)) {
             float up[C];                              // change of O's factors
 #pragma unroll
@@ -393,10 +443,11 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                         for (int i = 0; i < 2; ++i) m = __hmax2(m, __habs2(as_half2(vd[u][i][c])));
                     const unsigned w = as_u32(m);
                     const unsigned big = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
-                    // scales are below 2^(field - 14) by their exponent field; one
-                    // step more, so that few tiles raise it again
-                    const int e = max(-15, min(15, 13 - static_cast<int>(big >> 10)));
-                    const __half2 mul = __hmin2(v_mul[c], __float2half2_rn(exp2f(static_cast<float>(e))));
+                    // below 2^(field - 14) by the exponent's field: from 2^-8 up to 2 they stay,
+                    // larger ones go below 1, smaller ones to 1/4 .. 1/2
+                    const int field = static_cast<int>(big >> 10);
+                    const int e = field >= 16 ? 14 - field : field >= 7 ? 0 : 13 - field;
+                    const __half2 mul = __hmin2(v_mul[c], __float2half2_rn(exp2f(static_cast<float>(max(-15, min(15, e))))));
                     up[c] = __low2float(mul) / __low2float(v_mul[c]);
                     v_mul[c] = mul;
 #pragma unroll
@@ -404,6 +455,9 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
                         for (int i = 0; i < 2; ++i) vd[u][i][c] = as_u32(__hmul2(as_half2(vd[u][i][c]), mul));
                 }
+                v_scaled = false;
+#pragma unroll
+                for (int c = 0; c < C; ++c) v_scaled |= __low2float(v_mul[c]) != 1.f;
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -502,45 +556,55 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                     ldsm4_trans(w[u], stage + Lay::V0 + u * 16 * RS + (c2 + 1 < C ? m_lane : m_row) + 16 * c2);
 #pragma unroll
                 for (int c = c2; c < c2 + 2 && c < C; ++c) {
-                    float acc[NT][2][4];              // the tile's part of dims 32 c + ...
+                    unsigned pd[SUB][NT][2][2];       // p times the block's scale, in two terms
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[n][i / 4][i % 4] = 0.f;
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const __half2 d = as_half2(vd[u][i][c]);
+                                const __half2 hi = as_half2(pf[u][n][0][i]), t1 = __hmul2_rn(hi, d);
+                                pd[u][n][0][i] = as_u32(t1);
+                                pd[u][n][1][i] = as_u32(__hfma2(as_half2(pf[u][n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
+                            }
+                    // the MMA's sum cuts off what does not fit in 24 bits: with HI the tile's
+                    // products are summed apart and added to O with rounding
+                    float apart[HI ? NT : 1][2][4];
+                    if constexpr (HI) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) apart[n][i / 4][i % 4] = 0.f;
+                    }
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
                         unsigned f0[4], f1[4];        // keys 0 .. 7, 8 .. 15 of the half
                         codes4_f16(w[u][2 * (c - c2)], f0);
                         codes4_f16(w[u][2 * (c - c2) + 1], f1);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            unsigned pd[2][2];        // p times the block's scale, in two terms
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const __half2 d = as_half2(vd[u][i][c]);
-                                const __half2 hi = as_half2(pf[u][n][0][i]), t1 = __hmul2_rn(hi, d);
-                                pd[0][i] = as_u32(t1);
-                                pd[1][i] = as_u32(__hfma2(as_half2(pf[u][n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
-                            }
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j)
-                                    mma<false>(acc[n][j], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pd[q][0], pd[q][1]);
-                        }
+                                    mma<false>(HI ? apart[n][j] : o[n][2 * c + j], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1],
+                                               pd[u][n][q][0], pd[u][n][q][1]);
                     }
+                    if constexpr (HI) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
+                            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                float* to = &o[n][2 * c + j][i];
-                                const float2 x = fma2(make_float2(acc[n][j][i], acc[n][j][i + 1]), make_float2(down, down),
-                                                      make_float2(to[0], to[1]));
-                                to[0] = x.x;
-                                to[1] = x.y;
-                            }
+                                for (int i = 0; i < 4; i += 2) {
+                                    float* to = &o[n][2 * c + j][i];
+                                    const float2 x = fma2(make_float2(apart[n][j][i], apart[n][j][i + 1]), make_float2(down, down),
+                                                          make_float2(to[0], to[1]));
+                                    to[0] = x.x;
+                                    to[1] = x.y;
+                                }
+                    }
                 }
             }
             if constexpr (!HI) break;

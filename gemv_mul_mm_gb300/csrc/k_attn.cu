@@ -90,8 +90,9 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     const cudaError_t e = attn::launch_one(l, fmt, D);
     if (e != cudaSuccess) return e;
     const int64_t items = B * Hkv * p->head_chunks;
-    const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + 15) : max_len;
-    const int64_t step = attn::kWarps * (fmt == QMM_KV_Q4_0 ? 32 : 16);   // keys that a block's warps take at once
+    const int tile = fmt == QMM_KV_Q4_0 ? 32 : 16;               // a window begins inside one
+    const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + tile - 1) : max_len;
+    const int64_t step = attn::kWarps * tile;                    // keys that a block's warps take at once
     const int64_t steps = (keys + step - 1) / step;
     // The split count n with the least expected time, in steps of 64 keys (an SM
     // takes 0.5 to 0.7 us for one, and q8_0 a quarter more for each block
@@ -116,8 +117,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     // Without HI the MMAs sum a block's keys, cutting off bits (see the kernel):
     // 16384 keys are 1.2e-5 of the result, little against a 16-bit output's own
     // rounding, and more are not taken.
-    // Over q4_0 they are summed with rounding.
-    const int64_t least = p->hi || fmt == QMM_KV_Q4_0 ? 1 : (steps + 255) / 256;
+    const int64_t least = p->hi ? 1 : (steps * step + 16383) / 16384;
     // More than 64 blocks per SM are not made (only sequences of a million
     // keys and batches that nearly fill the memory would take them): the workspace
     // has a bound that grows with the sizes, though the count itself does not.

@@ -60,6 +60,21 @@ __device__ __forceinline__ void pair_of(int e, int rot, bool half, int& pair, in
     }
 }
 
+// An element's rotation. q4_0 keys are rotated operation by operation as a plain
+// fp32 computation does it (rope_cs_plain, products rounded before their sum): their
+// codes are an eighth of a block's largest value apart, and a difference in the
+// last bit turns a few of ten million over, which are then the ones that such a
+// computation stores.
+template <int FMT> __device__ __forceinline__ void angle_of(int32_t pos, uint64_t turns, float mscale, float& c, float& s) {
+    if constexpr (FMT == QMM_KV_Q4_0) rope_cs_plain(pos, turns, mscale, c, s);
+    else rope_cs(pos, turns, mscale, c, s);
+}
+// x c + y s
+template <int FMT> __device__ __forceinline__ float turned(float x, float c, float y, float s) {
+    if constexpr (FMT == QMM_KV_Q4_0) return __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    else return x * c + y * s;
+}
+
 // Where a token's rows go.
 struct Place {
     uint8_t* base;               // its page
@@ -114,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, i
         if (!is_v && i == 0) {           // behind the first loads
             const int32_t pos = a.pos[t];
 #pragma unroll
-            for (int j = 0; j < N; ++j) rope_cs(pos, a.turns[e + j], a.mscale, c[j], s[j]);
+            for (int j = 0; j < N; ++j) angle_of<FMT>(pos, a.turns[e + j], a.mscale, c[j], s[j]);
         }
 #pragma unroll
         for (int k = 0; k < kB; ++k) {
@@ -125,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, i
             if (!is_v) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float y = f0[j] * c[j] - f1[j] * s[j];
-                    f1[j] = f1[j] * c[j] + f0[j] * s[j];
+                    const float y = FMT == QMM_KV_Q4_0 ? turned<FMT>(f0[j], c[j], f1[j], -s[j]) : f0[j] * c[j] - f1[j] * s[j];
+                    f1[j] = turned<FMT>(f1[j], c[j], f0[j], s[j]);
                     f0[j] = y;
                 }
             }
@@ -192,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 3 : 5) k_kv_store(KvStoreArgs
                         c[j] = c[j - 1];
                         s[j] = -s[j - 1];
                     } else {
-                        rope_cs(pos, a.turns[pair], a.mscale, c[j], s[j]);
+                        angle_of<FMT>(pos, a.turns[pair], a.mscale, c[j], s[j]);
                         s[j] *= sign;
                     }
                 }
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 3 : 5) k_kv_store(KvStoreArgs
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < N; ++j) f[j] = e + j < a.rot ? f[j] * c[j] + g[j] * s[j] : f[j];
+                for (int j = 0; j < N; ++j) f[j] = e + j < a.rot ? turned<FMT>(f[j], c[j], g[j], s[j]) : f[j];
             }
             put8<FMT>(a.c, at.base + head(k) * unit, at.row, e, f, at.writes);
         }

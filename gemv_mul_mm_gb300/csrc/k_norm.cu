@@ -140,7 +140,7 @@ __device__ __forceinline__ Row row_of(const NormArgs& a, int64_t row) {
     return {t * a.x_ts + h * a.x_hs, t * a.r_ts + h * a.r_hs, t * a.ro_ts + h * a.ro_hs, t * a.y_ts + h * a.y_hs};
 }
 
-// y = (h * inv) * (w + o)
+// weight + offset
 template <int N, bool ALIGNED> __device__ __forceinline__ void weights(const NormArgs& a, int64_t e, float (&w)[N]) {
     if (!a.W) {
 #pragma unroll
@@ -155,8 +155,46 @@ template <int N, bool ALIGNED> __device__ __forceinline__ void weights(const Nor
 #pragma unroll
         for (int j = 0; j < N; ++j) w[j] = a.W[e + j];
     }
+    if (a.w_off != 0.f) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) w[j] += a.w_off;
+        for (int j = 0; j < N; ++j) w[j] += a.w_off;
+    }
+}
+
+// Two elements in one instruction where there are two.
+template <int N> __device__ __forceinline__ void add_to(float (&h)[N], const float (&f)[N]) {
+    if constexpr (N == 1) {
+        h[0] += f[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = add2(make_float2(h[j], h[j + 1]), make_float2(f[j], f[j + 1]));
+            h[j] = v.x;
+            h[j + 1] = v.y;
+        }
+    }
+}
+template <int N> __device__ __forceinline__ float2 squares(const float (&h)[N], float2 s) {
+    if constexpr (N == 1) {
+        s.x = fmaf(h[0], h[0], s.x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) s = fma2(make_float2(h[j], h[j + 1]), make_float2(h[j], h[j + 1]), s);
+    }
+    return s;
+}
+// y = (h * inv) * w
+template <int N> __device__ __forceinline__ void scale(float (&h)[N], float inv, const float (&w)[N]) {
+    if constexpr (N == 1) {
+        h[0] = h[0] * inv * w[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = mul2(mul2(make_float2(h[j], h[j + 1]), make_float2(inv, inv)), make_float2(w[j], w[j + 1]));
+            h[j] = v.x;
+            h[j + 1] = v.y;
+        }
+    }
 }
 
 // A row in `group` threads of a warp (a power of two), ITEMS vectors a thread.
@@ -181,7 +219,8 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
             if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
         }
     }
-    float h[ITEMS][N], ss = 0.f;
+    float h[ITEMS][N];
+    float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int e = (k * group + in) * N;
@@ -190,15 +229,13 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
             if (res) {
                 float f[N];
                 r[k].get(f, a.r_dt);
-#pragma unroll
-                for (int j = 0; j < N; ++j) h[k][j] += f[j];
+                add_to(h[k], f);
                 if (a.RO && live) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+            sq = squares(h[k], sq);
         }
     }
-    const float inv = rsqrtf(warp_sum(ss, group) / static_cast<float>(a.D) + a.eps);
+    const float inv = rsqrtf(warp_sum(sq.x + sq.y, group) / static_cast<float>(a.D) + a.eps);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int e = (k * group + in) * N;
@@ -206,8 +243,7 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
         float w[N];
         if (mine) {
             weights<N, ALIGNED>(a, e, w);
-#pragma unroll
-            for (int j = 0; j < N; ++j) h[k][j] = h[k][j] * inv * w[j];
+            scale(h[k], inv, w);
         }
         if constexpr (N == 8) {
             if (a.y_fmt == QMM_NORM_Q8_0) {          // one row a warp
@@ -225,8 +261,8 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
 }
 
 // A row a block.
-template <int N, bool ALIGNED, int ITEMS>
-__global__ void __launch_bounds__(1024) k_norm_block(const __grid_constant__ NormArgs a) {
+template <int N, bool ALIGNED, int ITEMS, int MOST>
+__global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ NormArgs a) {
     grid_dep_launch();
     grid_dep_wait();
     __shared__ __align__(16) uint8_t stage[N == 8 ? 32 : 1][272];
@@ -243,7 +279,8 @@ __global__ void __launch_bounds__(1024) k_norm_block(const __grid_constant__ Nor
             if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
         }
     }
-    float h[ITEMS][N], ss = 0.f;
+    float h[ITEMS][N];
+    float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
@@ -252,15 +289,13 @@ __global__ void __launch_bounds__(1024) k_norm_block(const __grid_constant__ Nor
             if (res) {
                 float f[N];
                 r[k].get(f, a.r_dt);
-#pragma unroll
-                for (int j = 0; j < N; ++j) h[k][j] += f[j];
+                add_to(h[k], f);
                 if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+            sq = squares(h[k], sq);
         }
     }
-    ss = warp_sum(ss, 32);
+    float ss = warp_sum(sq.x + sq.y, 32);
     if (lane == 0) part[wid] = ss;
     __syncthreads();
     ss = warp_sum(lane < threads / 32 ? part[lane] : 0.f, 32);
@@ -272,8 +307,7 @@ __global__ void __launch_bounds__(1024) k_norm_block(const __grid_constant__ Nor
         if (mine) {
             float w[N];
             weights<N, ALIGNED>(a, e, w);
-#pragma unroll
-            for (int j = 0; j < N; ++j) h[k][j] = h[k][j] * inv * w[j];
+            scale(h[k], inv, w);
         }
         if constexpr (N == 8) {
             if (a.y_fmt == QMM_NORM_Q8_0) {
@@ -309,18 +343,16 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
         if (res) {
             float f[N];
             r.get(f, a.r_dt);
-#pragma unroll
-            for (int j = 0; j < N; ++j) h[j] += f[j];
+            add_to(h, f);
         }
     };
-    float ss = 0.f;
+    float2 sq = make_float2(0.f, 0.f);
     for (int64_t e = threadIdx.x * N; e < a.D; e += threads * N) {
         float h[N];
         sum_of(e, h);
-#pragma unroll
-        for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
+        sq = squares(h, sq);
     }
-    ss = warp_sum(ss, 32);
+    float ss = warp_sum(sq.x + sq.y, 32);
     if (lane == 0) part[wid] = ss;
     __syncthreads();
     ss = warp_sum(lane < threads / 32 ? part[lane] : 0.f, 32);
@@ -337,8 +369,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
             if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h);
             float w[N];
             weights<N, ALIGNED>(a, e, w);
-#pragma unroll
-            for (int j = 0; j < N; ++j) h[j] = h[j] * inv * w[j];
+            scale(h, inv, w);
         }
         if constexpr (N == 8) {
             if (a.y_fmt == QMM_NORM_Q8_0) {
@@ -351,23 +382,34 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
     }
 }
 
+// Threads and vectors a thread. Few rows are spread over as many threads as they have
+// vectors (latency); from four rows per SM on a thread takes four, whose loads
+// are in flight together, and rows of up to four vectors a lane a warp alone.
 template <int N, bool ALIGNED> cudaError_t run(const NormArgs& a, cudaStream_t s) {
     const int64_t rows = a.T * a.H, vecs = (a.D + N - 1) / N;
     if (rows > 0x7fffffff) return cudaErrorInvalidValue;
-    if (vecs <= 64) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool many = rows >= 4 * static_cast<int64_t>(sm_count(dev));
+    if (vecs <= (many ? 128 : 64)) {
         const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
         int group = q8 ? 32 : 1;
         while (group < 32 && group < vecs) group *= 2;
         const int64_t per_block = kWide / group, blocks = (rows + per_block - 1) / per_block;
         auto go = [&](auto k) { return launch_chained(k, dim3(static_cast<unsigned>(blocks)), kWide, 0, s, a, group, rows); };
-        return vecs <= 32 ? go(k_norm_warp<N, ALIGNED, 1>) : go(k_norm_warp<N, ALIGNED, 2>);
+        return vecs <= 32 ? go(k_norm_warp<N, ALIGNED, 1>) : vecs <= 64 ? go(k_norm_warp<N, ALIGNED, 2>) : go(k_norm_warp<N, ALIGNED, 4>);
     }
     const dim3 grid(static_cast<unsigned>(rows));
-    auto threads = [&](int items) { return static_cast<int>((vecs + items * 32 - 1) / (items * 32)) * 32; };
-    auto go = [&](auto k, int items) { return launch_chained(k, grid, threads(items), 0, s, a); };
-    if (vecs <= 512) return go(k_norm_block<N, ALIGNED, 1>, 1);
-    if (vecs <= 1024) return go(k_norm_block<N, ALIGNED, 2>, 2);
-    if (vecs <= 4096) return go(k_norm_block<N, ALIGNED, 4>, 4);
+    auto go = [&](auto k, int items) {
+        return launch_chained(k, grid, static_cast<int>((vecs + items * 32 - 1) / (items * 32)) * 32, 0, s, a);
+    };
+    if (!many && vecs <= 512) return go(k_norm_block<N, ALIGNED, 1, 512>, 1);
+    if (!many && vecs <= 1024) return go(k_norm_block<N, ALIGNED, 2, 512>, 2);
+    if (vecs <= 1024) return go(k_norm_block<N, ALIGNED, 4, 256>, 4);
+    if (vecs <= 4096) return go(k_norm_block<N, ALIGNED, 4, 1024>, 4);
+    if constexpr (N == 1) {
+        if (vecs <= 16384) return go(k_norm_block<N, ALIGNED, 16, 1024>, 16);
+    }
     return launch_chained(k_norm_long<N, ALIGNED>, grid, 1024, 0, s, a);
 }
 

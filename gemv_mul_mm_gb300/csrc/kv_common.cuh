@@ -114,6 +114,27 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // cos and sin of 2 pi frac(pos * turns / 2^64). The product wraps modulo 2^64,
 // which drops whole turns exactly, so the angle is as good at position 10^6 as
 // at 1 (an fp32 product pos * frequency is off by up to 4e-3 rad at 10^5). The
@@ -125,6 +146,17 @@ __device__ __forceinline__ void rope_cs(int32_t pos, uint64_t turns, float mscal
     sincospif(half_turns, &s, &c);
     c *= mscale;
     s *= mscale;
+}
+
+// The same operation by operation as a plain fp32 computation has it: the phase
+// rounded to fp32 and multiplied by 2 pi / 2^32, cosf, sinf. (A little further from
+// the angle, off by up to 3e-7 instead of 1e-7.) For codes of so few bits that a
+// last bit's difference now and then turns one over to its neighbour.
+__device__ __forceinline__ void rope_cs_plain(int32_t pos, uint64_t turns, float mscale, float& c, float& s) {
+    const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+    const float angle = __fmul_rn(static_cast<float>(static_cast<int32_t>(ph >> 32)), 1.4629180792671596e-09f);
+    c = __fmul_rn(cosf(angle), mscale);
+    s = __fmul_rn(sinf(angle), mscale);
 }
 
 // Programmatic dependent launch: the operators here are launched so that the
