@@ -87,12 +87,26 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     // the query rows, read before anything waits for the lengths
     constexpr int QN = 8 * NT * D / kThreads;
     float qv[QN];
+    auto load_q = [&](auto type) {
+        using T = decltype(type);
+        const T* q = static_cast<const T*>(a.q) + b * a.q_bs + h0 * a.q_hs;
 #pragma unroll
-    for (int i = 0; i < QN; ++i) {
-        const int j = i * kThreads + threadIdx.x, h = j / D, d = j % D;
-        qv[i] = h < nh ? load_act(a.q, a.dtype, b * a.q_bs + (h0 + h) * a.q_hs + d) : 0.f;
-    }
+        for (int i = 0; i < QN; ++i) {
+            const int j = i * kThreads + threadIdx.x, h = j / D;
+            qv[i] = h < nh ? to_f32<T>(q[h * a.q_hs + j % D]) : 0.f;
+        }
+    };
+    if constexpr (HI) load_q(0.f);
+    else if (a.dtype == QMM_F16) load_q(__half());
+    else load_q(__nv_bfloat16());
     const int32_t* table = a.table + b * a.table_stride;
+    // and the pages of this warp's first tiles, as they are without a window
+    int first_page[STAGES];
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+        const int64_t key = static_cast<int64_t>(split) * chunk + (warp + i * kWarps) * KT;
+        first_page[i] = table[imin64(key >> a.c.page_shift, a.table_width - 1)];
+    }
     const Range rg = range_of(a, b, chunk);
     if (rg.splits == 0) {                             // nothing to attend to (or a bad length)
         if (split == 0) {
@@ -197,13 +211,16 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     int base = begin + warp * KT;
     int id[SUB][2];                                   // pages of the next tile to load
     int ahead = base;                                 // its first key
-    page_ids(ahead, id);
+    const bool known = rg.lo16 == 0 && one_page;
+    if (known) id[0][0] = first_page[0];
+    else page_ids(ahead, id);
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
         if (ahead < end) {
             load_tile(ahead, id, ring + i * Lay::STAGE);
             ahead += stride;
-            page_ids(ahead, id);
+            if (known) id[0][0] = first_page[i + 1];
+            else page_ids(ahead, id);
         }
         copies_commit();
     }
@@ -215,7 +232,8 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
         sm_q[j / D][j % D] = qv[i];
     }
     __syncthreads();
-    {                                                 // rows scaled into the middle of f16's range
+    const bool norm = HI || a.dtype != QMM_F16;       // rows scaled into the middle of f16's range
+    if (norm) {
         for (int h = warp; h < 8 * NT; h += kWarps) {
             float m = 0.f;
             for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(sm_q[h][d]));
@@ -231,7 +249,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     float sc[NT][2];                                  // score scale of heads 2t, 2t + 1, to log2 units unless capped
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float f = sm_scale[8 * n + g];
+        const float f = norm ? sm_scale[8 * n + g] : 1.f;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             if (j % kWarps != warp) continue;
@@ -250,7 +268,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             sc[n][k] = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-            sc[n][k] /= sm_scale[8 * n + 2 * t + k];
+            if (norm) sc[n][k] /= sm_scale[8 * n + 2 * t + k];
         }
     }
     __syncthreads();
@@ -635,6 +653,9 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     if (bad && lane == 0) atomicOr(a.err, DEV_ERR_BAD_SLOT);
     __syncthreads();                                  // every warp's ring is consumed
     float* sm_o = reinterpret_cast<float*>(smem);     // [warp][head][OD]
+    float v_div[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) v_div[c] = 1.f / __low2float(v_mul[c]);
     constexpr int OD = Lay::OD;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -655,7 +676,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
             for (int i = 0; i < 4; ++i) {
                 // rows g and g + 8 of a tile: codes 2 (j % 2) and the next of four
                 const int d = j / 2 * 32 + 4 * g + 2 * (j % 2) + (i >> 1);
-                p[(i & 1) * OD + d] = o[n][j][i] / __low2float(v_mul[j / 2]);
+                p[(i & 1) * OD + d] = o[n][j][i] * v_div[j / 2];
             }
     }
     __syncthreads();

@@ -22,13 +22,28 @@ __device__ __forceinline__ float warp_sum(float v, int width) {
     return v;
 }
 
+// How a row's N elements are reached. kVec: 16-byte accesses. kShift: rows of any
+// size that begin anywhere, alike in all arrays (an odd D, contiguous): a thread's vectors
+// lie on the arrays' 16-byte grid, `shift` elements before where they would, so that only
+// the first and the last of a row are partial. kOne: one by one.
+enum Mode { kOne, kVec, kShift };
+
 // N elements as they lie in memory, of a type known at run time (a branch that
-// a whole grid takes alike).
+// a whole grid takes alike). Of elements e .. e + N - 1 of a row those outside it are zeros.
 template <int N> struct Raw;
 template <> struct Raw<8> {
     uint4 a, b;
-    template <bool ALIGNED> __device__ __forceinline__ void load(const void* p, int64_t i, int dt) {
-        if constexpr (ALIGNED) {
+    template <int MODE> __device__ __forceinline__ void load(const void* p, int64_t i, int dt, int64_t e, int64_t D) {
+        if (MODE == kShift && (e < 0 || e + 8 > D)) {
+            unsigned* u = &a.x;
+            a = b = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (e + j < 0 || e + j >= D) continue;
+                if (dt == QMM_F32) (j < 4 ? u[j] : (&b.x)[j - 4]) = static_cast<const unsigned*>(p)[i + j];
+                else u[j / 2] |= static_cast<unsigned>(static_cast<const unsigned short*>(p)[i + j]) << (j % 2 * 16);
+            }
+        } else if constexpr (MODE != kOne) {
             if (dt == QMM_F32) {
                 const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
                 a = q[0];
@@ -71,7 +86,7 @@ template <> struct Raw<8> {
 };
 template <> struct Raw<1> {
     float v;
-    template <bool ALIGNED> __device__ __forceinline__ void load(const void* p, int64_t i, int dt) {
+    template <int MODE> __device__ __forceinline__ void load(const void* p, int64_t i, int dt, int64_t, int64_t) {
         v = dt == QMM_F32   ? static_cast<const float*>(p)[i]
             : dt == QMM_F16 ? __half2float(static_cast<const __half*>(p)[i])
                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -79,9 +94,9 @@ template <> struct Raw<1> {
     __device__ __forceinline__ void get(float (&x)[1], int) const { x[0] = v; }
 };
 
-template <int N, bool ALIGNED>
-__device__ __forceinline__ void put(void* p, int64_t i, int dt, const float (&x)[N]) {
-    if constexpr (ALIGNED && N > 1) {
+template <int N, int MODE>
+__device__ __forceinline__ void put(void* p, int64_t i, int dt, const float (&x)[N], int64_t e, int64_t D) {
+    if (MODE != kOne && (MODE == kVec || (e >= 0 && e + N <= D))) {
         if (dt == QMM_F32) {
             Vec<float, N> v;
             v.set(x);
@@ -98,6 +113,7 @@ __device__ __forceinline__ void put(void* p, int64_t i, int dt, const float (&x)
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
+            if (MODE == kShift && (e + j < 0 || e + j >= D)) continue;
             if (dt == QMM_F32) static_cast<float*>(p)[i + j] = x[j];
             else if (dt == QMM_F16) static_cast<__half*>(p)[i + j] = __float2half_rn(x[j]);
             else static_cast<__nv_bfloat16*>(p)[i + j] = __float2bfloat16_rn(x[j]);
@@ -132,28 +148,42 @@ __device__ __forceinline__ void put_q8(uint8_t* to, uint8_t* stage, int lane, in
 
 struct Row {
     int64_t x, r, ro, y;
+    int shift;                       // kShift: of the row's vectors
 };
+// (rows are below 2^31; row / H by a multiplication, see launch_norm)
 __device__ __forceinline__ Row row_of(const NormArgs& a, int64_t row) {
-    int64_t t = row;
-    int h = 0;
-    if (a.H > 1) div_mod(row, static_cast<int>(a.H), t, h);
-    return {t * a.x_ts + h * a.x_hs, t * a.r_ts + h * a.r_hs, t * a.ro_ts + h * a.ro_hs, t * a.y_ts + h * a.y_hs};
+    unsigned t = static_cast<unsigned>(row), h = 0;
+    if (a.H > 1) {
+        t = __umulhi(static_cast<unsigned>(row), a.h_mul) >> a.h_shift;
+        h = static_cast<unsigned>(row) - t * static_cast<unsigned>(a.H);
+    }
+    auto at = [&](int64_t ts, int64_t hs) { return static_cast<int64_t>(t) * ts + static_cast<int64_t>(h) * hs; };
+    Row r;
+    r.x = at(a.x_ts, a.x_hs);
+    r.y = at(a.y_ts, a.y_hs);
+    r.r = r.ro = 0;
+    if (a.R) {
+        r.r = at(a.r_ts, a.r_hs);
+        r.ro = at(a.ro_ts, a.ro_hs);
+    }
+    r.shift = static_cast<int>((r.x + a.x_shift) & 7);
+    return r;
 }
 
 // weight + offset
-template <int N, bool ALIGNED> __device__ __forceinline__ void weights(const NormArgs& a, int64_t e, float (&w)[N]) {
+template <int N, int MODE> __device__ __forceinline__ void weights(const NormArgs& a, int64_t e, float (&w)[N]) {
     if (!a.W) {
 #pragma unroll
         for (int j = 0; j < N; ++j) w[j] = 1.f;
         return;
     }
-    if constexpr (ALIGNED && N > 1) {
+    if constexpr (MODE == kVec) {
         Vec<float, N> v;
         v.load(a.W + e);
         v.get(w);
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = a.W[e + j];
+        for (int j = 0; j < N; ++j) w[j] = MODE == kOne || (e + j >= 0 && e + j < a.D) ? a.W[e + j] : 0.f;
     }
     if (a.w_off != 0.f) {
 #pragma unroll
@@ -198,7 +228,7 @@ template <int N> __device__ __forceinline__ void scale(float (&h)[N], float inv,
 }
 
 // A row in `group` threads of a warp (a power of two), ITEMS vectors a thread.
-template <int N, bool ALIGNED, int ITEMS>
+template <int N, int MODE, int ITEMS>
 __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ NormArgs a, int group, int64_t rows) {
     grid_dep_launch();
     grid_dep_wait();
@@ -213,24 +243,24 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
     const bool res = a.R != nullptr;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * group + in) * N;
+        const int e = (k * group + in) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
-            x[k].template load<ALIGNED>(a.X, at.x + e, a.x_dt);
-            if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+            x[k].template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
+            if (res) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         }
     }
     float h[ITEMS][N];
     float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * group + in) * N;
+        const int e = (k * group + in) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].get(h[k], a.x_dt);
             if (res) {
                 float f[N];
                 r[k].get(f, a.r_dt);
                 add_to(h[k], f);
-                if (a.RO && live) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
+                if (a.RO && live) put<N, MODE>(a.RO, at.ro + e, a.r_dt, h[k], e, a.D);
             }
             sq = squares(h[k], sq);
         }
@@ -238,14 +268,14 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
     const float inv = rsqrtf(warp_sum(sq.x + sq.y, group) / static_cast<float>(a.D) + a.eps);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * group + in) * N;
+        const int e = (k * group + in) * N - (MODE == kShift ? at.shift : 0);
         const bool mine = e < a.D;
         float w[N];
         if (mine) {
-            weights<N, ALIGNED>(a, e, w);
+            weights<N, MODE>(a, e, w);
             scale(h[k], inv, w);
         }
-        if constexpr (N == 8) {
+        if constexpr (N == 8 && MODE != kShift) {
             if (a.y_fmt == QMM_NORM_Q8_0) {          // one row a warp
                 const int left = (static_cast<int>(a.D) - k * 256) / 8;
                 if (left <= 0) continue;
@@ -256,12 +286,12 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
                 continue;
             }
         }
-        if (mine && live) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h[k]);
+        if (mine && live) put<N, MODE>(a.Y, at.y + e, a.y_fmt, h[k], e, a.D);
     }
 }
 
 // A row a block.
-template <int N, bool ALIGNED, int ITEMS, int MOST>
+template <int N, int MODE, int ITEMS, int MOST>
 __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ NormArgs a) {
     grid_dep_launch();
     grid_dep_wait();
@@ -273,24 +303,24 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
     const bool res = a.R != nullptr;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
-            x[k].template load<ALIGNED>(a.X, at.x + e, a.x_dt);
-            if (res) r[k].template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+            x[k].template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
+            if (res) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         }
     }
     float h[ITEMS][N];
     float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].get(h[k], a.x_dt);
             if (res) {
                 float f[N];
                 r[k].get(f, a.r_dt);
                 add_to(h[k], f);
-                if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h[k]);
+                if (a.RO) put<N, MODE>(a.RO, at.ro + e, a.r_dt, h[k], e, a.D);
             }
             sq = squares(h[k], sq);
         }
@@ -302,14 +332,14 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
     const float inv = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N;
+        const int e = (k * threads + static_cast<int>(threadIdx.x)) * N - (MODE == kShift ? at.shift : 0);
         const bool mine = e < a.D;
         if (mine) {
             float w[N];
-            weights<N, ALIGNED>(a, e, w);
+            weights<N, MODE>(a, e, w);
             scale(h[k], inv, w);
         }
-        if constexpr (N == 8) {
+        if constexpr (N == 8 && MODE != kShift) {
             if (a.y_fmt == QMM_NORM_Q8_0) {
                 const int first = (k * threads + wid * 32) * 8, left = (static_cast<int>(a.D) - first) / 8;
                 if (left <= 0) continue;
@@ -320,13 +350,13 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
                 continue;
             }
         }
-        if (mine) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h[k]);
+        if (mine) put<N, MODE>(a.Y, at.y + e, a.y_fmt, h[k], e, a.D);
     }
 }
 
 // Rows too long for a block's registers: x and r are read again for the product
 // (r' may be r or x, so that it is written with y).
-template <int N, bool ALIGNED>
+template <int N, int MODE>
 __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ NormArgs a) {
     grid_dep_launch();
     grid_dep_wait();
@@ -337,8 +367,8 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
     const bool res = a.R != nullptr;
     auto sum_of = [&](int64_t e, float (&h)[N]) {
         Raw<N> x, r;
-        x.template load<ALIGNED>(a.X, at.x + e, a.x_dt);
-        if (res) r.template load<ALIGNED>(a.R, at.r + e, a.r_dt);
+        x.template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
+        if (res) r.template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         x.get(h, a.x_dt);
         if (res) {
             float f[N];
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
         }
     };
     float2 sq = make_float2(0.f, 0.f);
-    for (int64_t e = threadIdx.x * N; e < a.D; e += threads * N) {
+    for (int64_t e = static_cast<int64_t>(threadIdx.x) * N - (MODE == kShift ? at.shift : 0); e < a.D; e += threads * N) {
         float h[N];
         sum_of(e, h);
         sq = squares(h, sq);
@@ -358,64 +388,74 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
     ss = warp_sum(lane < threads / 32 ? part[lane] : 0.f, 32);
     const float inv = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
     // a warp's lanes stay together: they share blocks of the 8-bit output
-    for (int64_t first = wid * 32 * N; first < a.D; first += threads * N) {
-        const int64_t e = first + lane * N;
+    for (int64_t first = wid * 32 * N; first < a.D + (MODE == kShift ? 7 : 0); first += threads * N) {
+        const int64_t e = first + lane * N - (MODE == kShift ? at.shift : 0);
         const bool mine = e < a.D;
         float h[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) h[j] = 0.f;
         if (mine) {
             sum_of(e, h);
-            if (a.RO) put<N, ALIGNED>(a.RO, at.ro + e, a.r_dt, h);
+            if (a.RO) put<N, MODE>(a.RO, at.ro + e, a.r_dt, h, e, a.D);
             float w[N];
-            weights<N, ALIGNED>(a, e, w);
+            weights<N, MODE>(a, e, w);
             scale(h, inv, w);
         }
-        if constexpr (N == 8) {
+        if constexpr (N == 8 && MODE != kShift) {
             if (a.y_fmt == QMM_NORM_Q8_0) {
                 put_q8(static_cast<uint8_t*>(a.Y) + at.y + first / 32 * 34, stage[wid], lane,
                        static_cast<int>(imin64(32, (a.D - first) / 8)), h);
                 continue;
             }
         }
-        if (mine) put<N, ALIGNED>(a.Y, at.y + e, a.y_fmt, h);
+        if (mine) put<N, MODE>(a.Y, at.y + e, a.y_fmt, h, e, a.D);
     }
 }
 
 // Threads and vectors a thread. Few rows are spread over as many threads as they have
 // vectors (latency); from four rows per SM on a thread takes four, whose loads
-// are in flight together, and rows of up to four vectors a lane a warp alone.
-template <int N, bool ALIGNED> cudaError_t run(const NormArgs& a, cudaStream_t s) {
-    const int64_t rows = a.T * a.H, vecs = (a.D + N - 1) / N;
+// are in flight together, and rows of up to four vectors a lane a warp alone. (Rows of a
+// vector a lane are bound by instructions: two or four at a time were slower.)
+template <int N, int MODE> cudaError_t run(const NormArgs& a, cudaStream_t s) {
+    const int64_t rows = a.T * a.H, vecs = (a.D + (MODE == kShift ? 7 : 0) + N - 1) / N;
     if (rows > 0x7fffffff) return cudaErrorInvalidValue;
     int dev = 0;
     cudaGetDevice(&dev);
-    const bool many = rows >= 4 * static_cast<int64_t>(sm_count(dev));
+    const int64_t sms = sm_count(dev);
+    const bool many = rows >= 4 * sms;
     if (vecs <= (many ? 128 : 64)) {
         const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
         int group = q8 ? 32 : 1;
         while (group < 32 && group < vecs) group *= 2;
         const int64_t per_block = kWide / group, blocks = (rows + per_block - 1) / per_block;
-        auto go = [&](auto k) { return launch_chained(k, dim3(static_cast<unsigned>(blocks)), kWide, 0, s, a, group, rows); };
-        return vecs <= 32 ? go(k_norm_warp<N, ALIGNED, 1>) : vecs <= 64 ? go(k_norm_warp<N, ALIGNED, 2>) : go(k_norm_warp<N, ALIGNED, 4>);
+        auto go = [&](auto k, int64_t n) { return launch_chained(k, dim3(static_cast<unsigned>(n)), kWide, 0, s, a, group, rows); };
+        return vecs <= 32   ? go(k_norm_warp<N, MODE, 1>, blocks)
+               : vecs <= 64 ? go(k_norm_warp<N, MODE, 2>, blocks)
+                            : go(k_norm_warp<N, MODE, 4>, blocks);
     }
     const dim3 grid(static_cast<unsigned>(rows));
     auto go = [&](auto k, int items) {
         return launch_chained(k, grid, static_cast<int>((vecs + items * 32 - 1) / (items * 32)) * 32, 0, s, a);
     };
-    if (!many && vecs <= 512) return go(k_norm_block<N, ALIGNED, 1, 512>, 1);
-    if (!many && vecs <= 1024) return go(k_norm_block<N, ALIGNED, 2, 512>, 2);
-    if (vecs <= 1024) return go(k_norm_block<N, ALIGNED, 4, 256>, 4);
-    if (vecs <= 4096) return go(k_norm_block<N, ALIGNED, 4, 1024>, 4);
+    if (!many && vecs <= 512) return go(k_norm_block<N, MODE, 1, 512>, 1);
+    if (!many && vecs <= 1024) return go(k_norm_block<N, MODE, 2, 512>, 2);
+    if (vecs <= 1024) return go(k_norm_block<N, MODE, 4, 256>, 4);
+    if (vecs <= 4096) return go(k_norm_block<N, MODE, 4, 1024>, 4);
     if constexpr (N == 1) {
-        if (vecs <= 16384) return go(k_norm_block<N, ALIGNED, 16, 1024>, 16);
+        if (vecs <= 16384) return go(k_norm_block<N, MODE, 16, 1024>, 16);
     }
-    return launch_chained(k_norm_long<N, ALIGNED>, grid, 1024, 0, s, a);
+    return launch_chained(k_norm_long<N, MODE>, grid, 1024, 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs& args, cudaStream_t s) {
+    NormArgs a = args;
+    // n / H for n < 2^31 as (n * mul) >> (32 + shift): with mul = ceil(2^(32 + shift) / H), 2^shift < H
+    // <= 2^(shift + 1), the product is off by less than n / 2^32 of a quotient's step, below 1 / H
+    a.h_shift = 0;
+    while ((int64_t(2) << a.h_shift) < a.H) ++a.h_shift;
+    a.h_mul = static_cast<unsigned>(((uint64_t(1) << (32 + a.h_shift)) + static_cast<uint64_t>(a.H) - 1) / static_cast<uint64_t>(a.H));
     auto size = [](int dt) { return static_cast<int64_t>(dt == QMM_F32 ? 4 : 2); };
     const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
     auto ok = [&](const void* p, int64_t ts, int64_t hs, int64_t sz) {
@@ -424,8 +464,18 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     const bool vec = a.D % 8 == 0 && ok(a.X, a.x_ts, a.x_hs, size(a.x_dt)) && (!a.R || ok(a.R, a.r_ts, a.r_hs, size(a.r_dt))) &&
                      (!a.RO || ok(a.RO, a.ro_ts, a.ro_hs, size(a.r_dt))) && ok(a.W, 0, 0, 4) &&
                      (q8 || ok(a.Y, a.y_ts, a.y_hs, size(a.y_fmt)));
-    if (vec) return run<8, true>(a, s);
-    return q8 ? run<8, false>(a, s) : run<1, false>(a, s);
+    if (vec) return run<8, kVec>(a, s);
+    if (q8) return run<8, kOne>(a, s);
+    // vectors of eight elements on a grid of 8 * size bytes: every array's rows begin alike
+    a.x_shift = static_cast<int>(reinterpret_cast<uintptr_t>(a.X) / size(a.x_dt) % 8);
+    auto alike = [&](const void* p, int64_t ts, int64_t hs, int64_t sz) {
+        return static_cast<int>(reinterpret_cast<uintptr_t>(p) / sz % 8) == a.x_shift && (a.T == 1 || (ts - a.x_ts) % 8 == 0) &&
+               (a.H == 1 || (hs - a.x_hs) % 8 == 0);
+    };
+    if (a.D >= 32 && (!a.R || alike(a.R, a.r_ts, a.r_hs, size(a.r_dt))) && (!a.RO || alike(a.RO, a.ro_ts, a.ro_hs, size(a.r_dt))) &&
+        alike(a.Y, a.y_ts, a.y_hs, size(a.y_fmt)))
+        return run<8, kShift>(a, s);
+    return run<1, kOne>(a, s);
 }
 
 }  // namespace qmm

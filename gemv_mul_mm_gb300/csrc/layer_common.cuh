@@ -16,6 +16,9 @@ struct NormArgs {
     int y_fmt;                     // one of them, or QMM_NORM_Q8_0 (y strides in bytes)
     int64_t x_ts, x_hs, r_ts, r_hs, ro_ts, ro_hs, y_ts, y_hs;
     float w_off, eps;
+    unsigned h_mul = 0;            // row / H (set by the launcher, as is x_shift)
+    int h_shift = 0;
+    int x_shift = 0;               // elements by which X begins past an 8-element grid
     int64_t T, H, D;
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);

@@ -73,58 +73,79 @@ __device__ __forceinline__ void quant8(const float (&x)[kQuantN], uint2& codes, 
     codes = make_uint2(w[0], w[1]);
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Q4_0: d = f16(m / -8) for the value m of largest magnitude (the first of them),
 // code = rint(x / d) in [-8, 7], each division rounded once; d = 0 gives codes 0,
 // bad blocks d = NaN as above. Bits 4 j .. 4 j + 3 of `codes` are element j's
-// code plus 8. Magnitudes are compared as integers, in which NaN is the largest.
-// Quotients go the same way as above: |x / d| <= 12 is off by less than 2^-18.
+// code plus 8.
+//
+// m is the largest or the smallest value; which comes first matters only where they
+// are opposite, and is looked up only then. Quotients go the same way as above:
+// |x / d| <= 12 is off by less than 2^-18. Away from subnormal d they do not
+// pass -8 by more than 2^-8, so that the upper end alone is clamped. Codes are put
+// together in fp32, four in a sum below 2^16.
 __device__ __forceinline__ void quant4(const float (&x)[kQuantN], unsigned& codes, __half& d) {
-    unsigned most = __float_as_uint(x[0]) & 0x7fffffffu;
-    float m = x[0];
+    constexpr unsigned kAll = 0xffffffffu;
+    float hi = x[0], lo = x[0];
 #pragma unroll
     for (int j = 1; j < kQuantN; ++j) {
-        const unsigned b = __float_as_uint(x[j]) & 0x7fffffffu;
-        m = b > most ? x[j] : m;
-        most = max(most, b);
+        hi = max_nan(hi, x[j]);
+        lo = min_nan(lo, x[j]);
     }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {                    // of equal ones the lower lane's
-        const float other = __shfl_xor_sync(0xffffffffu, m, o);
-        const unsigned b = __float_as_uint(other) & 0x7fffffffu;
-        const bool take = b > most || (b == most && (threadIdx.x & o));
-        m = take ? other : m;
-        most = max(most, b);
+    for (int o = 1; o < 4; o <<= 1) {
+        hi = max_nan(hi, __shfl_xor_sync(kAll, hi, o));
+        lo = min_nan(lo, __shfl_xor_sync(kAll, lo, o));
+    }
+    float m = hi > -lo ? hi : lo;                        // (NaN: lo is)
+    if (__any_sync(kAll, hi == -lo && hi > 0.f)) {
+        float first = 0.f;                               // of this lane's that have the magnitude
+#pragma unroll
+        for (int j = kQuantN - 1; j >= 0; --j) first = fabsf(x[j]) == hi ? x[j] : first;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {                // the lower lane's before the upper one's
+            const float other = __shfl_xor_sync(kAll, first, o);
+            const bool upper = threadIdx.x & o;
+            const float a = upper ? other : first, b = upper ? first : other;
+            first = a != 0.f ? a : b;
+        }
+        if (hi == -lo && hi > 0.f) m = first;
     }
     d = __float2half_rn(m * -0.125f);
     const float df = __half2float(d);
     if (!(fabsf(df) < INFINITY)) d = __ushort_as_half(0x7fff);
     codes = 0x88888888u;
     if (!(fabsf(df) > 0.f && fabsf(df) < INFINITY)) return;
-    constexpr float kRound = 12582912.f;
+    constexpr float kInt = 12582912.f;                   // 1.5 2^23: sums with it are integers
+    constexpr float kRound = kInt + 8.f;                 // the sum less kInt is the code plus 8
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df));
-    float q[kQuantN];
+    float2 u[4];                                         // codes plus 8 of elements j and j + 4
     float off = 0.f;
 #pragma unroll
-    for (int j = 0; j < kQuantN; j += 2) {
-        const float2 v = make_float2(x[j], x[j + 1]), rr = make_float2(r, r);
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = make_float2(x[j], x[j + 4]), rr = make_float2(r, r);
         const float2 n = fma2(v, rr, make_float2(kRound, kRound));
         const float2 k = fma2(n, make_float2(-1.f, -1.f), make_float2(kRound, kRound));   // minus the integer
         const float2 e = fma2(v, rr, k);
         off = fmaxf(fmaxf(off, fabsf(e.x)), fabsf(e.y));
-        q[j] = n.x;
-        q[j + 1] = n.y;
+        u[j] = add2(make_float2(fminf(n.x, kRound + 7.f), fminf(n.y, kRound + 7.f)), make_float2(-kInt, -kInt));
     }
-    if (off > 0.49999f) {
+    if (off > 0.49999f || fabsf(df) < 6.103515625e-05f) {
 #pragma unroll
-        for (int j = 0; j < kQuantN; ++j) q[j] = rintf(__fdiv_rn(x[j], df)) + kRound;
+        for (int j = 0; j < 4; ++j) {
+            u[j].x = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[j], df))));
+            u[j].y = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[j + 4], df))));
+        }
     }
-    codes = 0u;
-#pragma unroll
-    for (int j = 0; j < kQuantN; ++j) {
-        const float c = fminf(fmaxf(q[j], kRound - 8.f), kRound + 7.f);
-        codes |= ((__float_as_uint(c) + 8u) & 15u) << (4 * j);
-    }
+    const float2 by16 = make_float2(16.f, 16.f);
+    const float2 w = add2(fma2(fma2(fma2(u[3], by16, u[2]), by16, u[1]), by16, u[0]), make_float2(8388608.f, 8388608.f));
+    codes = __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
 }
 
 }  // namespace qmm

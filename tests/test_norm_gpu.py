@@ -72,14 +72,38 @@ def test_heads_of_a_projection(Q, dt, T, H, D, pad):
     res = randn((T, H, D + pad), "f32", 4)[..., :D]
     check(Q, x, w, res, dt)
     before = buf.clone()
+    # sums go in another order where the arrays' rows begin unalike: both are within the tolerance
+    want, _ = L.norm(f64(x), None, f64(w), 0.0, 1e-6)
     assert Q.qrmsnorm(x, w, out=x) is x
-    assert torch.equal(x, y)
+    assert np.all(np.abs(f64(x) - want) <= L.norm_tol(want, dt))
     x.copy_(before[:, 1:1 + H, pad // 2: pad // 2 + D])
     assert torch.equal(buf, before)
     # an output that is a view
     to = torch.full((T, H, 2 * D), 7.0, dtype=U.dtype(dt), device="cuda")
     Q.qrmsnorm(x, w, out=to[..., D:])
-    assert torch.equal(to[..., D:], y) and bool((to[..., :D] == 7).all())
+    assert np.all(np.abs(f64(to[..., D:]) - want) <= L.norm_tol(want, dt)) and bool((to[..., :D] == 7).all())
+    assert torch.equal(y, Q.qrmsnorm(x, w))
+
+
+@pytest.mark.parametrize("x,r,out", [("f32", None, "f16"), ("bf16", "f32", "bf16"), ("f16", "bf16", "f32"), ("bf16", "bf16", "bf16")])
+@pytest.mark.parametrize("T,D,off", [(5, 33, 0), (700, 35, 1), (9, 63, 5), (4000, 129, 0), (3, 257, 7), (800, 511, 2), (6, 1001, 3),
+                                     (700, 1001, 0), (5, 4639, 6), (700, 4639, 1), (3, 8191, 4), (2, 32763, 1), (1, 40001, 3)])
+def test_rows_of_odd_sizes(Q, x, r, out, T, D, off):
+    """Rows that begin anywhere on the 16-byte grid, alike in all arrays: contiguous
+    ones of odd sizes, from an offset on; nothing beside them changes."""
+    import torch
+    n = T * D
+    X, w = randn((n + 16,), x, D)[off:off + n].view(T, D), randn((D,), "f32", 1)
+    R = None if r is None else randn((n + 16,), r, 2, 3.0)
+    r0 = None if r is None else R.clone()
+    Y = torch.full((n + 16,), 7.0, dtype=U.dtype(out), device="cuda")
+    Q.qrmsnorm(X, w, residual=None if r is None else R[off:off + n].view(T, D), out=Y[off:off + n].view(T, D))
+    want, _ = L.norm(f64(X), None if r is None else f64(r0[off:off + n].view(T, D)), f64(w), 0.0, 1e-6)
+    assert np.all(np.abs(f64(Y[off:off + n].view(T, D)) - want) <= L.norm_tol(want, out))
+    assert bool((Y[:off] == 7).all() and (Y[off + n:] == 7).all())
+    if r is not None:
+        r0[off:off + n] = (X.float() + r0[off:off + n].view(T, D).float()).to(U.dtype(r)).view(-1)
+        assert torch.equal(R, r0)
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
