@@ -5,7 +5,8 @@
 //   ids: the top_k largest c of those, ties to the lower index
 //   w = s (/ their sum) * scale
 //
-// A warp takes a token, a lane V consecutive experts of it. The instructions that a
+// A warp takes a token, a lane V consecutive experts of it (or, of many tokens with few
+// experts to choose, eight lanes take one: k_route_four). The instructions that a
 // token takes bound the operator, not the reading of its logits, so that the
 // selection does not search the whole warp again for each of the top_k:
 //   1. a lower bound of the top_k-th value: the top_k-th largest of the lanes'
@@ -20,7 +21,12 @@
 // the order that matter lie closer than that and do not come from equal inputs,
 // the warp computes the candidates (for groups: all c) in 64 bits and
 // counts again. With the scores of 256 experts that is one token in some hundred.
+//
+// Measured: 65536 tokens x 128 experts, bf16, top 8: 13.6 us (1.5 TB/s; 25.6 with a warp a
+// token, 183 instructions a token against 496); 8192 x 256 in 8 groups, sigmoid with a
+// bias: 12 us, of which 2 are the few tokens in 64 bits; one token 2 to 4 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_common.cuh"
 
@@ -59,19 +65,54 @@ __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[i]);
 }
 
-// ---- in 64 bits, for the few tokens that need it; a row's softmax has its largest
-// logit `top` and the sum of exponentials relative to it
+// ---- in 64 bits, for the few tokens that need it. What they take is felt at the end of
+// every call of some thousand tokens, all of which run at once, and is mostly the
+// fetching of code that ran nowhere before: hence a short exponential and quotient.
+
+// e^x to 2 ulp for |x| <= 700: x = k ln 2 + r with ln 2 in two parts (Cody and Waite),
+// e^r by its Taylor sum to r^13 / 13! (|r| <= 0.35: the next term is 5e-18).
+__device__ __forceinline__ double exp_mid(double x) {
+    const double k = rint(x * 1.4426950408889634);
+    double r = fma(k, -0.6931471805592082, x);                 // ln 2 cut off to 40 bits: k times it is exact
+    r = fma(k, -7.371002565167799e-13, r);                     // the rest of it
+    const double r2 = r * r, r4 = r2 * r2;
+    const double p0 = fma(r, 1.0, 1.0), p1 = fma(r, 1.0 / 6, 0.5), p2 = fma(r, 1.0 / 120, 1.0 / 24), p3 = fma(r, 1.0 / 5040, 1.0 / 720);
+    const double p4 = fma(r, 1.0 / 362880, 1.0 / 40320), p5 = fma(r, 1.0 / 39916800, 1.0 / 3628800);
+    const double p6 = fma(r, 1.0 / 6227020800.0, 1.0 / 479001600);
+    const double q0 = fma(p1, r2, p0), q1 = fma(p3, r2, p2), q2 = fma(p5, r2, p4);
+    const double e = fma(fma(fma(p6, r4, q2), r4, q1), r4, q0);
+    return __hiloint2double(__double2hiint(e) + (static_cast<int>(k) << 20), __double2loint(e));
+}
+// 1 / d to 1 ulp for d in fp32's range: Newton's steps from an fp32 quotient.
+__device__ __forceinline__ double inverse(double d) {
+    double y = static_cast<double>(__fdividef(1.f, static_cast<float>(d)));
+    y = fma(y, fma(-d, y, 1.0), y);
+    return fma(y, fma(-d, y, 1.0), y);
+}
+// The sum of a row's exponentials relative to its largest logit `top`, inverted.
 __device__ __noinline__ double sum64(const RouteArgs& a, int64_t t, float top) {
     if (a.score == QMM_SCORE_SIGMOID || top == -INFINITY) return 1.0;
     double s = 0.0;
-    for (int e = threadIdx.x % 32; e < a.E; e += 32) s += exp(static_cast<double>(logit(a, t, e)) - top);
+    for (int e = threadIdx.x % 32; e < a.E; e += 32) {
+        const double x = static_cast<double>(logit(a, t, e)) - top;
+        s += x >= -700.0 ? exp_mid(x) : isnan(x) ? x : 0.0;
+    }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    return s;
+    return inverse(s);
 }
-__device__ __noinline__ double value64(const RouteArgs& a, int64_t t, int e, float top, double sum) {
+__device__ __noinline__ double value64(const RouteArgs& a, int64_t t, int e, float top, double by_sum) {
     const double x = logit(a, t, e), b = a.bias ? a.bias[e] : 0.0;
-    if (a.score == QMM_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-x)) + b;
-    return (top == -INFINITY ? 0.0 : exp(x - top) / sum) + b;
+    if (a.score == QMM_SCORE_SIGMOID) {
+        if (fabs(x) <= 80.0) return inverse(1.0 + exp_mid(-x)) + b;
+        return 1.0 / (1.0 + exp(-x)) + b;
+    }
+    const double y = x - top;
+    return (top == -INFINITY ? 0.0 : y >= -700.0 ? exp_mid(y) * by_sum : isnan(y) ? y : 0.0) + b;
+}
+// Keys of doubles as key_of's of floats.
+__device__ __forceinline__ unsigned long long key64(double v) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));
+    return isnan(v) ? ~0ull : u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
 // The groups that stay, as bits. `keys`: all c in fp32; `least`: for each group, what
 // one of its group_top largest has at least in fp32. Only the few that reach it
@@ -112,20 +153,17 @@ __device__ __noinline__ unsigned groups64(const RouteArgs& a, int64_t t, float t
     return __ballot_sync(kAll, lane < a.groups && place < a.top_groups);
 }
 // The top_k of n candidates, into `sorted`.
-__device__ __noinline__ void places64(const RouteArgs& a, int64_t t, float top, const Cand* cand, double* value, int n, Cand* sorted) {
+__device__ __noinline__ void places64(const RouteArgs& a, int64_t t, float top, const Cand* cand, unsigned long long* value, int n, Cand* sorted) {
     const int lane = threadIdx.x % 32;
-    const double sum = sum64(a, t, top);
-    for (int i = lane; i < n; i += 32) value[i] = value64(a, t, expert_in(cand[i]), top, sum);
+    const double by_sum = sum64(a, t, top);
+    for (int i = lane; i < n; i += 32) value[i] = key64(value64(a, t, expert_in(cand[i]), top, by_sum));
     __syncwarp();
     for (int i = lane; i < n; i += 32) {
         const Cand me = cand[i];
-        const double w = value[i];
+        const unsigned long long w = value[i];
         int place = 0;
-        for (int j = 0; j < n; ++j) {
-            const double o = value[j];
-            const bool first = static_cast<unsigned>(cand[j]) > static_cast<unsigned>(me);   // the lower index
-            place += o > w || (o == w && first) || (isnan(o) && (!isnan(w) || first));
-        }
+        for (int j = 0; j < n; ++j)                       // of equal ones the lower index
+            place += value[j] > w || (value[j] == w && static_cast<unsigned>(cand[j]) > static_cast<unsigned>(me));
         if (place < a.top_k) sorted[place] = me;
     }
     __syncwarp();
@@ -162,15 +200,11 @@ __host__ __device__ constexpr size_t warp_bytes(int E, bool by_score) {
     return static_cast<size_t>(cands_of(E)) * (by_score ? 16 : 8) + (kMaxTopK + 2) * 8;
 }
 
+// One token by a whole warp.
 template <int V, typename T, bool BY_SCORE>
-__global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs a, bool wide) {
-    grid_dep_launch();
-    grid_dep_wait();
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t t = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + warp;
-    if (t >= a.T) return;
-    Cand* cand = reinterpret_cast<Cand*>(smem + warp * warp_bytes(a.E, BY_SCORE));
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool wide, uint8_t* smem) {
+    const int lane = threadIdx.x % 32;
+    Cand* cand = reinterpret_cast<Cand*>(smem);
     double* value = reinterpret_cast<double*>(cand + cands_of(a.E));
     Cand* sorted = cand + cands_of(a.E) * (BY_SCORE ? 2 : 1);
     const int e0 = lane * V;
@@ -215,8 +249,8 @@ __global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs
 
     // ---- groups
     unsigned kept = kAll;
-    const int gs = a.E / a.groups;
     if (a.groups > 1) {
+        const int gs = a.E / a.groups;
         // a lane for each group: its one or two largest c, summed
         unsigned m1, m2 = 0u;
         auto take = [&](unsigned b) {
@@ -303,33 +337,47 @@ __global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs
         const float v = value_of(bound);
         if (bound != 1u && !isnan(v)) bound = min(bound, max(1u, key_of(v - tau(v))));
     }
-    // ---- 2. the candidates; equal keys at the bound: the first top_k of them, where keys are exact
-    unsigned count = 0u;                                  // above the bound; equal to it in the upper half
+    // ---- 2. the candidates
+    int count = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        count += key[i] > bound ? 1u : 0u;
-        count += key[i] == bound ? 0x10000u : 0u;
-    }
-    unsigned scan = count;
+    for (int i = 0; i < V; ++i) count += key[i] >= bound;
+    int scan = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned up = __shfl_up_sync(kAll, scan, o);
+        const int up = __shfl_up_sync(kAll, scan, o);
         if (lane >= o) scan += up;
     }
-    const unsigned total = __shfl_sync(kAll, scan, 31);
-    const int above = static_cast<int>(total & 0xffffu), equal = static_cast<int>(total >> 16);
-    const int take_equal = biased ? equal : min(equal, a.top_k), n = above + take_equal;
-    if (count) {
-        unsigned at = scan - count;
+    int n = __shfl_sync(kAll, scan, 31);
+    if (n <= 64 || biased) {
+        int at = scan - count;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (key[i] >= bound) {
-                const bool over = key[i] > bound;
-                const int nth = static_cast<int>(at >> 16);
-                if (over || nth < take_equal) cand[over ? static_cast<int>(at & 0xffffu) : above + nth] = cand_of(key[i], e0 + i);
-                at += over ? 1u : 0x10000u;
-            }
+        for (int i = 0; i < V; ++i)
+            if (key[i] >= bound) cand[at++] = cand_of(key[i], e0 + i);
+    } else {
+        // many equal keys at the bound (a row of padding), and keys are exact: the first top_k of those
+        unsigned both = 0u;                               // above the bound; equal to it in the upper half
+#pragma unroll
+        for (int i = 0; i < V; ++i) both += key[i] > bound ? 1u : key[i] == bound ? 0x10000u : 0u;
+        unsigned sum2 = both;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned up = __shfl_up_sync(kAll, sum2, o);
+            if (lane >= o) sum2 += up;
         }
+        const unsigned total = __shfl_sync(kAll, sum2, 31);
+        const int above = static_cast<int>(total & 0xffffu), equal = min(static_cast<int>(total >> 16), a.top_k);
+        unsigned at = sum2 - both;
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+            unsigned k = key[0];
+#pragma unroll
+            for (int j = 1; j < V; ++j) k = i == j ? key[j] : k;
+            const int nth = static_cast<int>(at >> 16);
+            if (k > bound) cand[at & 0xffffu] = cand_of(k, e0 + i);
+            else if (k == bound && nth < equal) cand[above + nth] = cand_of(k, e0 + i);
+            at += k > bound ? 1u : k == bound ? 0x10000u : 0u;
+        }
+        n = above + equal;
     }
     if (lane < 3 && n + lane < cands_of(a.E)) cand[n + lane] = 0u;
     __syncwarp();
@@ -355,7 +403,7 @@ __global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs
                 close = logit(a, t, e) != logit(a, t, f) || a.bias[e] != a.bias[f];
             }
         }
-        if (__any_sync(kAll, close)) places64(a, t, top, cand, value, n, sorted);
+        if (__any_sync(kAll, close)) places64(a, t, top, cand, reinterpret_cast<unsigned long long*>(value), n, sorted);
     }
 
     // ---- weights
@@ -382,19 +430,288 @@ __global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs
     }
 }
 
+template <int V, typename T, bool BY_SCORE>
+__global__ void __launch_bounds__(256) k_route(const __grid_constant__ RouteArgs a, bool wide) {
+    grid_dep_launch();
+    grid_dep_wait();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x / 32;
+    const int64_t t = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + warp;
+    if (t < a.T) route_token<V, T, BY_SCORE>(a, t, wide, smem + warp * warp_bytes(a.E, BY_SCORE));
+}
+
+// For the tokens that k_route_four leaves.
+template <int V, typename T, bool BY_SCORE>
+__device__ __noinline__ void route_again(const RouteArgs& a, int64_t t, uint8_t* smem) {
+    route_token<V, T, BY_SCORE>(a, t, true, smem);
+    __syncwarp();
+}
+
+// Four tokens a warp, eight lanes each, for top_k up to 8 and experts in 8 V that
+// V divides: what a warp does together (the bound, the scan, the few lanes that count
+// places and weigh) serves four tokens. Tokens whose candidates are many (equal
+// keys), or need 64 bits, are left to the whole warp at the end.
+constexpr int kFew = 32;                                  // candidates of a token
+constexpr int kFourBytes = (4 * (kFew + 10) + kFew) * 8;  // of a warp: candidates, the chosen and the next, values in 64 bits
+constexpr int kFourTopK = 8;
+
+__device__ __forceinline__ unsigned max8(unsigned v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+template <int V, typename T, bool BY_SCORE>
+__global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid_constant__ RouteArgs a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, seg = lane / 8, sl = lane % 8;
+    const size_t bytes = max(warp_bytes(a.E, BY_SCORE), static_cast<size_t>(kFourBytes));
+    uint8_t* mem = smem + warp * bytes;
+    Cand* cand = reinterpret_cast<Cand*>(mem) + seg * kFew;
+    Cand* sorted = reinterpret_cast<Cand*>(mem) + 4 * kFew + seg * 10;
+    const int64_t t0 = (blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + warp) * 4;
+    if (t0 >= a.T) return;
+    const int64_t t = imin64(t0 + seg, a.T - 1);
+    const int e0 = sl * V;
+    float x[V];
+    load_row<V, T>(static_cast<const T*>(a.logits) + t * a.stride, e0, a.E, true, x);
+    const bool softmax = a.score == QMM_SCORE_SOFTMAX, biased = BY_SCORE && a.bias != nullptr;
+    bool leave = false;
+
+    float top = 0.f, sum = 1.f;
+    if (softmax && (BY_SCORE || !a.renorm)) {
+        unsigned m = key_of(x[0]);
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = max(m, key_of(x[i]));
+        top = value_of(max8(m));
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += top == -INFINITY ? 0.f : __expf(x[i] - top);
+        sum = sum8(s);
+    }
+    unsigned key[V];
+    [[maybe_unused]] float base = 0.f;
+    auto tau = [&](float v) { return base + 2.384185791015625e-07f * fabsf(v); };        // as above
+    if constexpr (BY_SCORE) {
+        base = softmax ? static_cast<float>(V + 12) * 1.1920928955078125e-07f / sum : 4.76837158203125e-07f;
+        float bias[V];
+        if (biased) load_row<V, float>(a.bias, e0, a.E, true, bias);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float s = softmax ? (top == -INFINITY ? 0.f : __fdividef(__expf(x[i] - top), sum)) : __fdividef(1.f, 1.f + __expf(-x[i]));
+            key[i] = key_of(biased ? s + bias[i] : s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = key_of(x[i]);
+    }
+    bool mine = e0 < a.E;
+    if (a.groups > 1) {
+        // groups of whole lanes, a power of two of them
+        const int lanes = a.E / a.groups / V;
+        unsigned m1 = key[0], m2 = 0u;
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
+            m2 = max(m2, min(m1, key[i]));
+            m1 = max(m1, key[i]);
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            const unsigned b1 = __shfl_xor_sync(kAll, m1, o), b2 = __shfl_xor_sync(kAll, m2, o);
+            m2 = max(max(m2, b2), min(m1, b1));
+            m1 = max(m1, b1);
+        }
+        const unsigned k = !mine ? 0u : a.group_top == 2 ? key_of(value_of(m1) + value_of(m2)) : m1;
+        int place = 0;
+        for (int from = 0; from < 8; from += lanes) {     // (lanes past the experts have 0)
+            const unsigned other = __shfl_sync(kAll, k, from, 8);
+            place += other > k || (other == k && from + lanes <= sl);
+        }
+        const bool stays = mine && place < a.top_groups;
+        if (BY_SCORE && a.top_groups < a.groups) {
+            const unsigned last = ~max8(stays ? ~k : 0u), next = max8(stays ? 0u : k);
+            const float lo = value_of(last), hi = value_of(next);
+            leave = last != kAll && lo - hi <= tau(lo) + tau(hi);
+        }
+        mine = stays;
+        if (BY_SCORE && !biased) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = key_of(x[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = mine ? key[i] : 0u;
+
+    // ---- 1. the bound: of the largest values of the lanes' quarters, in order in each lane
+    unsigned m[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        m[q] = key[q * (V / 4)];
+#pragma unroll
+        for (int i = 1; i < V / 4; ++i) m[q] = max(m[q], key[q * (V / 4) + i]);
+    }
+    auto order = [&](int i, int j) {
+        const unsigned hi = max(m[i], m[j]);
+        m[j] = min(m[i], m[j]);
+        m[i] = hi;
+    };
+    order(0, 1);
+    order(2, 3);
+    order(0, 2);
+    order(1, 3);
+    order(1, 2);
+    unsigned bound = 0u;
+    for (int r = 0; r < a.top_k; ++r) {
+        bound = max8(m[0]);
+        if (m[0] == bound) {
+            m[0] = m[1];
+            m[1] = m[2];
+            m[2] = m[3];
+            m[3] = 0u;
+        }
+    }
+    bound = max(bound, 1u);
+    if (biased) {
+        const float v = value_of(bound);
+        if (bound != 1u && !isnan(v)) bound = min(bound, max(1u, key_of(v - tau(v))));
+    }
+    // ---- 2. the candidates
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) count += key[i] >= bound;
+    int scan = count;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        const int up = __shfl_up_sync(kAll, scan, o, 8);
+        if (sl >= o) scan += up;
+    }
+    int n = __shfl_sync(kAll, scan, 7, 8);
+    leave |= n > kFew;
+    if (!leave) {
+        int at = scan - count;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] >= bound) cand[at++] = cand_of(key[i], e0 + i);
+        if (sl == 0 && (n & 1)) cand[n] = 0u;
+    } else {
+        n = 0;
+    }
+    __syncwarp();
+    // ---- 3. their places
+    auto places = [&](auto rounds) {
+        constexpr int R = decltype(rounds)::value;
+        Cand me[R];
+        int place[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            me[r] = cand[min(sl + 8 * r, kFew - 1)];
+            place[r] = 0;
+        }
+        for (int j = 0; j < n; j += 2) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cand + j);
+#pragma unroll
+            for (int r = 0; r < R; ++r) place[r] += (q.x > me[r]) + (q.y > me[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (sl + 8 * r < n && place[r] <= a.top_k) sorted[place[r]] = me[r];
+    };
+    if (__any_sync(kAll, n > 16)) places(std::integral_constant<int, 4>{});
+    else places(std::integral_constant<int, 2>{});
+    __syncwarp();
+    const bool chosen = sl < a.top_k;
+    if (biased) {
+        bool close = false;
+        if (chosen && sl + 1 < n) {
+            const Cand p = sorted[sl], q = sorted[sl + 1];
+            const float v = value_of(key_in(p));
+            if (v - value_of(key_in(q)) <= tau(v)) {
+                const int e = expert_in(p), f = expert_in(q);
+                close = logit(a, t, e) != logit(a, t, f) || a.bias[e] != a.bias[f];
+            }
+        }
+        unsigned redo = __ballot_sync(kAll, close && !leave);
+        redo = (redo | redo >> 4) & 0x0f0f0f0fu;
+        redo = (redo | redo >> 2) & 0x03030303u;
+        redo = (redo | redo >> 1) & 0x01010101u;          // a bit for each token
+        for (; redo; redo &= redo - 1u) {
+            const int from = __ffs(static_cast<int>(redo)) - 1;
+            const int64_t tq = imin64(t0 + from / 8, a.T - 1);
+            places64(a, tq, __shfl_sync(kAll, top, from), reinterpret_cast<Cand*>(mem) + from / 8 * kFew,
+                     reinterpret_cast<unsigned long long*>(mem) + 4 * (kFew + 10), __shfl_sync(kAll, n, from),
+                     reinterpret_cast<Cand*>(mem) + 4 * kFew + from / 8 * 10);
+        }
+    }
+
+    // ---- weights
+    const Cand own = sorted[chosen && !leave ? sl : 0];
+    const int e = leave ? 0 : expert_in(own);
+    const float lx = leave ? 0.f : biased ? logit(a, t, e) : value_of(key_in(own));
+    float w;
+    if (softmax) {
+        if (a.renorm) top = biased ? value_of(max8(chosen ? key_of(lx) : 0u)) : value_of(key_in(sorted[0]));
+        w = top == -INFINITY ? 0.f : expf(lx - top);
+        if (!a.renorm) w /= sum;
+    } else {
+        w = 1.f / (1.f + expf(-lx));
+    }
+    if (a.renorm) {
+        const float s = sum8(chosen ? w : 0.f);
+        w = s == 0.f ? 0.f : __fdividef(w, s);
+    }
+    if (chosen && !leave && t0 + seg < a.T) {
+        a.ids[t * a.top_k + sl] = e;
+        a.weights[t * a.top_k + sl] = w * a.scale;
+    }
+    unsigned again = __ballot_sync(kAll, leave && sl == 0 && t0 + seg < a.T);
+    for (; again; again &= again - 1u) {
+        __syncwarp();
+        route_again<V / 4, T, BY_SCORE>(a, t0 + (__ffs(static_cast<int>(again)) - 1) / 8, mem);
+    }
+}
+
+// Warps of a block: what fits 48 KB, at most eight, fewer where that fills more SMs.
+int block_warps(int64_t warps, size_t bytes, int sms) {
+    const int64_t per_sm = (warps + sms - 1) / sms;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, static_cast<int64_t>(49152 / bytes), per_sm})));
+}
+
+// V: experts a lane where a warp takes a token.
 template <int V, typename T, bool BY_SCORE> cudaError_t go(const RouteArgs& a, cudaStream_t s) {
-    // warps of a block: what fits 48 KB, at most eight, fewer where that fills more SMs
     int dev = 0;
     cudaGetDevice(&dev);
-    const int64_t per_sm = (a.T + sm_count(dev) - 1) / sm_count(dev);
+    const int sms = sm_count(dev);
+    const bool at16 = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 &&
+                      (a.T == 1 || a.stride * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+    if constexpr (V == 2 || V == 4 || V == 8) {
+        // Four tokens a warp from 24 tokens an SM on (128 experts: 4800 tokens 3.1 us, a warp each 3.8;
+        // 2400 2.7 and 2.8), by score from 40 on (256 experts in groups: 8192 tokens 11.9 and
+        // 14.4 us, 4800 10.0 and 8.3); but not by score with 32 experts a lane and no groups,
+        // where registers decide (8192 tokens 11.8 and 9.9 us).
+        const int gs = a.E / a.groups, lanes = gs / (4 * V);
+        const bool whole = a.groups == 1 || (gs == lanes * 4 * V && (lanes & (lanes - 1)) == 0);
+        if (a.top_k <= kFourTopK && a.E % (4 * V) == 0 && at16 && whole && !(BY_SCORE && V == 8 && a.groups == 1) &&
+            a.T >= (BY_SCORE ? 40 : 24) * static_cast<int64_t>(sms)) {
+            const size_t bytes = std::max(warp_bytes(a.E, BY_SCORE), static_cast<size_t>(kFourBytes));
+            const int warps = block_warps((a.T + 3) / 4, bytes, sms);
+            const int64_t blocks = (a.T + 4 * warps - 1) / (4 * warps);
+            if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+            return launch_chained(k_route_four<4 * V, T, BY_SCORE>, dim3(static_cast<unsigned>(blocks)), warps * 32,
+                                  static_cast<int>(warps * bytes), s, a);
+        }
+    }
     const size_t bytes = warp_bytes(a.E, BY_SCORE);
-    const int warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, static_cast<int64_t>(49152 / bytes), per_sm})));
+    const int warps = block_warps(a.T, bytes, sms);
     const int64_t blocks = (a.T + warps - 1) / warps;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const bool wide = a.E % V == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 &&
-                      (a.T == 1 || a.stride * static_cast<int64_t>(sizeof(T)) % 16 == 0);
     return launch_chained(k_route<V, T, BY_SCORE>, dim3(static_cast<unsigned>(blocks)), warps * 32, static_cast<int>(warps * bytes), s, a,
-                          wide);
+                          at16 && a.E % V == 0);
 }
 
 template <int V, typename T> cudaError_t by(const RouteArgs& a, cudaStream_t s) {
