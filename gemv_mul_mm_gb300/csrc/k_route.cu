@@ -114,40 +114,82 @@ __device__ __forceinline__ unsigned long long key64(double v) {
     const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));
     return isnan(v) ? ~0ull : u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
-// The groups that stay, as bits. `keys`: all c in fp32; `least`: for each group, what
-// one of its group_top largest has at least in fp32. Only the few that reach it
-// are computed, a lane for each (a double exponential and quotient are about a
-// microsecond of dependent instructions); `value` gets them, `list` their experts.
-__device__ __noinline__ unsigned groups64(const RouteArgs& a, int64_t t, float top, const unsigned* keys, const float* least,
-                                          double* value, int* list) {
+// c in fp32.
+__device__ __forceinline__ float score32(bool softmax, float x, float top, float sum) {
+    if (!softmax) return __fdividef(1.f, 1.f + __expf(-x));
+    return top == -INFINITY ? 0.f : __fdividef(__expf(x - top), sum);
+}
+// Twice its error at magnitude |c| (k_route's comment), from its part at c = 0.
+__device__ __forceinline__ float tau_of(float base, float v) { return base + 2.384185791015625e-07f * fabsf(v); }   // 2^-22
+
+// The groups that stay, as bits; 16 bytes of `mem` an expert. Of all c in fp32 only the
+// few that may be among a group's group_top largest are computed, a lane for each.
+__device__ __noinline__ unsigned groups64(const RouteArgs& a, int64_t t, float top, float sum, float base, uint8_t* mem) {
     const int lane = threadIdx.x % 32, gs = a.E / a.groups;
-    const double sum = sum64(a, t, top);
+    float* c = reinterpret_cast<float*>(mem);
+    int* list = reinterpret_cast<int*>(c + a.E);
+    double* value = reinterpret_cast<double*>(mem) + a.E;
+    const double by_sum = sum64(a, t, top);
+    for (int first = 0; first < a.E; first += 256) {      // eight loads in flight
+        float x[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = min(first + 32 * i + lane, a.E - 1);
+            x[i] = logit(a, t, e);
+            b[i] = a.bias ? a.bias[e] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = first + 32 * i + lane;
+            const float s = score32(a.score == QMM_SCORE_SOFTMAX, x[i], top, sum);
+            if (e < a.E) c[e] = a.bias ? s + b[i] : s;
+            if (e < a.E) value[e] = -INFINITY;
+        }
+    }
+    __syncwarp();
+    float least = INFINITY;                               // what one of the group's largest has at least in fp32
+    if (lane < a.groups) {
+        float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 8
+        for (int i = 0; i < gs; ++i) {
+            const float b = c[lane * gs + i];
+            m2 = fmaxf(m2, fminf(m1, b));
+            m1 = fmaxf(m1, b);
+        }
+        least = a.group_top == 2 ? m2 : m1;
+        least -= tau_of(base, least);
+    }
     int n = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
-        const bool in = e < a.E && !(value_of(keys[min(e, a.E - 1)]) < least[min(e, a.E - 1) / gs]);
+        const float from = __shfl_sync(kAll, least, min(e, a.E - 1) / gs);
+        const bool in = e < a.E && !(c[min(e, a.E - 1)] < from);
         const unsigned b = __ballot_sync(kAll, in);
         if (in) list[n + __popc(b & ((1u << lane) - 1u))] = e;
         n += __popc(b);
-        if (e < a.E) value[e] = -INFINITY;
     }
     __syncwarp();
-    for (int i = lane; i < n; i += 32) value[list[i]] = value64(a, t, list[i], top, sum);
+    for (int i = lane; i < n; i += 32) value[list[i]] = value64(a, t, list[i], top, by_sum);
     __syncwarp();
     double w = -INFINITY;
     if (lane < a.groups) {
-        double m1 = value[lane * gs], m2 = -INFINITY;
-        for (int i = 1; i < gs; ++i) {
-            const double b = value[lane * gs + i];
-            m2 = fmax(m2, b > m1 ? m1 : b);
-            m1 = fmax(m1, b);
+        double m1 = -INFINITY, m2 = -INFINITY;
+        bool bad = false;                                 // a NaN: the largest
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const int e = list[i];
+            const double b = e / gs == lane ? value[e] : -INFINITY;
+            bad |= isnan(b);
+            m2 = b > m1 ? m1 : b > m2 ? b : m2;
+            m1 = b > m1 ? b : m1;
         }
-        w = a.group_top == 2 ? m1 + m2 : m1;
+        w = bad ? NAN : a.group_top == 2 ? m1 + m2 : m1;
     }
+    const unsigned long long k = lane < a.groups ? key64(w) : 0ull;
     int place = 0;
     for (int g = 0; g < a.groups; ++g) {
-        const double other = __shfl_sync(kAll, w, g);
-        place += other > w || (other == w && g < lane);
+        const unsigned long long other = __shfl_sync(kAll, k, g);
+        place += other > k || (other == k && g < lane);
     }
     __syncwarp();
     return __ballot_sync(kAll, lane < a.groups && place < a.top_groups);
@@ -232,14 +274,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
     // more: below 2^-21.9. Softmax scores are off, relative to the largest, 1 / sum, by
     // 2^-22 from the exponential, as much from the quotient, and by a common factor of the
     // sum's V + 5 roundings. The sum with the bias: 2^-24 |c|.
-    auto tau = [&](float v) { return base + 2.384185791015625e-07f * fabsf(v); };        // 2^-22
+    auto tau = [&](float v) { return tau_of(base, v); };
     if constexpr (BY_SCORE) {
         base = softmax ? static_cast<float>(V + 12) * 1.1920928955078125e-07f / sum : 4.76837158203125e-07f;   // 2^-23, 2^-21
         float bias[V];
         if (biased) load_row<V, float>(a.bias, e0, a.E, wide, bias);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float s = softmax ? (top == -INFINITY ? 0.f : __fdividef(__expf(x[i] - top), sum)) : __fdividef(1.f, 1.f + __expf(-x[i]));
+            const float s = score32(softmax, x[i], top, sum);
             key[i] = key_of(biased ? s + bias[i] : s);
         }
     } else {
@@ -293,17 +335,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
             const unsigned next = __reduce_max_sync(kAll, kept >> lane & 1 ? 0u : k);
             const float lo = value_of(last), hi = value_of(next);
             // (a sum of two is off by as much as both, and twice that again for the difference)
-            if (last != kAll && lo - hi <= tau(lo) + tau(hi)) {
-                unsigned* all = reinterpret_cast<unsigned*>(cand);
-                float* least = reinterpret_cast<float*>(sorted);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e0 + i < a.E) all[e0 + i] = key[i];
-                const float v = value_of(a.group_top == 2 ? m2 : m1);
-                if (mine) least[lane] = v - tau(v);
-                __syncwarp();
-                kept = groups64(a, t, top, all, least, value, reinterpret_cast<int*>(all + a.E));
-            }
+            if (last != kAll && lo - hi <= tau(lo) + tau(hi)) kept = groups64(a, t, top, sum, base, smem);
         }
         // those that do not stay: key 0
         int g = e0 / gs, left = gs - (e0 - g * gs);
@@ -450,7 +482,7 @@ __device__ __noinline__ void route_again(const RouteArgs& a, int64_t t, uint8_t*
 // Four tokens a warp, eight lanes each, for top_k up to 8 and experts in 8 V that
 // V divides: what a warp does together (the bound, the scan, the few lanes that count
 // places and weigh) serves four tokens. Tokens whose candidates are many (equal
-// keys), or need 64 bits, are left to the whole warp at the end.
+// keys) are left to the whole warp at the end.
 constexpr int kFew = 32;                                  // candidates of a token
 constexpr int kFourBytes = (4 * (kFew + 10) + kFew) * 8;  // of a warp: candidates, the chosen and the next, values in 64 bits
 constexpr int kFourTopK = 8;
@@ -498,14 +530,14 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
     }
     unsigned key[V];
     [[maybe_unused]] float base = 0.f;
-    auto tau = [&](float v) { return base + 2.384185791015625e-07f * fabsf(v); };        // as above
+    auto tau = [&](float v) { return tau_of(base, v); };
     if constexpr (BY_SCORE) {
         base = softmax ? static_cast<float>(V + 12) * 1.1920928955078125e-07f / sum : 4.76837158203125e-07f;
         float bias[V];
         if (biased) load_row<V, float>(a.bias, e0, a.E, true, bias);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float s = softmax ? (top == -INFINITY ? 0.f : __fdividef(__expf(x[i] - top), sum)) : __fdividef(1.f, 1.f + __expf(-x[i]));
+            const float s = score32(softmax, x[i], top, sum);
             key[i] = key_of(biased ? s + bias[i] : s);
         }
     } else {
@@ -533,11 +565,18 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
             const unsigned other = __shfl_sync(kAll, k, from, 8);
             place += other > k || (other == k && from + lanes <= sl);
         }
-        const bool stays = mine && place < a.top_groups;
+        bool stays = mine && place < a.top_groups;
         if (BY_SCORE && a.top_groups < a.groups) {
             const unsigned last = ~max8(stays ? ~k : 0u), next = max8(stays ? 0u : k);
             const float lo = value_of(last), hi = value_of(next);
-            leave = last != kAll && lo - hi <= tau(lo) + tau(hi);
+            const bool near = last != kAll && lo - hi <= tau(lo) + tau(hi);
+            for (unsigned redo = __ballot_sync(kAll, near && sl == 0); redo; redo &= redo - 1u) {
+                // by the whole warp, whose shared memory holds nothing yet
+                const int from = __ffs(static_cast<int>(redo)) - 1;
+                const unsigned kept = groups64(a, imin64(t0 + from / 8, a.T - 1), __shfl_sync(kAll, top, from), __shfl_sync(kAll, sum, from),
+                                               __shfl_sync(kAll, base, from), mem);
+                if (lane / 8 == from / 8) stays = mine && (kept >> (sl / lanes) & 1);
+            }
         }
         mine = stays;
         if (BY_SCORE && !biased) {
