@@ -37,8 +37,12 @@ template <typename K> cudaError_t launch_kernel(const Launch& l, K kernel, int b
 
 #ifdef QMM_ATTN_Q4
 template <int D, bool HI, int NT, int SUB, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
-    static std::atomic<int> fits[kDevices];
-    return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB>, Layout4<D, NT, SUB, STAGES>::BYTES, fits);
+    static std::atomic<int> fits[kDevices], fits_small[kDevices];
+    constexpr int bytes = Layout4<D, NT, SUB, STAGES>::BYTES;
+    // (a plan, without blocks, has no page size)
+    if (l.blocks && (1 << l.a.c.page_shift) < 16 * SUB)
+        return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB, false>, bytes, fits_small);
+    return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB, true>, bytes, fits);
 }
 
 // Keys per tile, depth of the ring and blocks per SM, measured on 64 sequences of 8192

@@ -59,7 +59,8 @@ __device__ __forceinline__ void codes4_f16(unsigned w, unsigned (&p)[4]) {
     p[3] = as_u32(__hfma2(as_half2(and_or(v, 0x00f000f0u, 0x64006400u)), r16, m72));
 }
 
-template <int D, bool HI, int NT, int SUB, int STAGES>
+// ONE: pages of 32 keys and more, so that a tile lies in one page.
+template <int D, bool HI, int NT, int SUB, int STAGES, bool ONE>
 __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int chunk, int head_chunks) {
     using Lay = Layout4<D, NT, SUB, STAGES>;
     constexpr int NQ = HI ? 2 : 1, NP = 2;            // f16 terms of q and of the weights
@@ -129,14 +130,17 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     // Pages of a 16-key half: one, or with pages of 8 one for each eight keys.
     // Keys outside the range name a page inside it, so that every address is that of
     // a page the sequence owns.
-    const bool small_pages = shift < 4, one_page = (1 << shift) >= KT;
+    const bool small_pages = shift < 4;
     auto page_id = [&](int key) { return table[max(page_lo, min(key >> shift, page_hi))]; };
     auto page_ids = [&](int base, int (&id)[SUB][2]) {
+        if constexpr (ONE) {                          // (a tile begins in the page of its first key in range)
+            if (base < end) id[0][0] = table[base >> shift];
+        } else {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-            if (u && one_page) id[u][0] = id[0][0];
-            else id[u][0] = page_id(base + 16 * u);
-            if (small_pages) id[u][1] = page_id(base + 16 * u + 8);
+            for (int u = 0; u < SUB; ++u) {
+                id[u][0] = page_id(base + 16 * u);
+                if (small_pages) id[u][1] = page_id(base + 16 * u + 8);
+            }
         }
     };
     auto page_at = [&](int id) {                      // this head's K rows in a page
@@ -181,29 +185,29 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     // Rows outside the range are copied like the others: they are masked by their
     // key (K) and have weights and scales of zero (V), and codes are never NaN.
     auto load_tile = [&](int base, const int (&id)[SUB][2], uint32_t stage) {
-        if (one_page) {
+        if constexpr (ONE) {
             load_whole(base, id[0][0], stage);
-            return;
-        }
+        } else {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {               // pages of 16 or 8 keys
-            const int first = base + 16 * u, row0 = first & page_mask, row1 = (first + 8) & page_mask;
-            const uint8_t* page0 = page_at(id[u][0]);
-            const uint8_t* page1 = small_pages ? page_at(id[u][1]) : page0;
-            if (lane < 4 * C) {                       // scales: C pieces per eight keys, of K then of V
-                const uint8_t* p = (lane / C & 1 ? page1 + row1 * (2 * C) : page0 + row0 * (2 * C)) + (ROW << shift) + lane % C * 16;
-                copy16(stage + Lay::S0 + u * 32 * C + lane % (2 * C) * 16 + (lane < 2 * C ? 0 : Lay::SV), lane < 2 * C ? p : p + v_minus_k);
-            }
-            const uint8_t* k0 = page0 + row0 * ROW + lane * 16;
-            const uint8_t* k1 = page1 + (row1 - 8) * ROW + lane * 16;
+            for (int u = 0; u < SUB; ++u) {               // pages of 16 or 8 keys
+                const int first = base + 16 * u, row0 = first & page_mask, row1 = (first + 8) & page_mask;
+                const uint8_t* page0 = page_at(id[u][0]);
+                const uint8_t* page1 = small_pages ? page_at(id[u][1]) : page0;
+                if (lane < 4 * C) {                       // scales: C pieces per eight keys, of K then of V
+                    const uint8_t* p = (lane / C & 1 ? page1 + row1 * (2 * C) : page0 + row0 * (2 * C)) + (ROW << shift) + lane % C * 16;
+                    copy16(stage + Lay::S0 + u * 32 * C + lane % (2 * C) * 16 + (lane < 2 * C ? 0 : Lay::SV), lane < 2 * C ? p : p + v_minus_k);
+                }
+                const uint8_t* k0 = page0 + row0 * ROW + lane * 16;
+                const uint8_t* k1 = page1 + (row1 - 8) * ROW + lane * 16;
 #pragma unroll
-            for (int i = 0; i < (ROW + 31) / 32; ++i) {
-                const int q = 32 * i + lane, row = q / CPR;
-                if (ROW % 32 && q >= ROW) break;
-                const uint32_t dst = stage + 16 * u * RS + (32 % CPR == 0 ? dst_lane + i * (32 / CPR) * RS : row * RS + q % CPR * 16);
-                const uint8_t* src = ((ROW / 2) % 32 == 0 ? 32 * i >= ROW / 2 : row >= 8) ? k1 : k0;
-                copy16(dst, src + i * 512);
-                copy16(dst + Lay::V0, src + v_minus_k + i * 512);
+                for (int i = 0; i < (ROW + 31) / 32; ++i) {
+                    const int q = 32 * i + lane, row = q / CPR;
+                    if (ROW % 32 && q >= ROW) break;
+                    const uint32_t dst = stage + 16 * u * RS + (32 % CPR == 0 ? dst_lane + i * (32 / CPR) * RS : row * RS + q % CPR * 16);
+                    const uint8_t* src = ((ROW / 2) % 32 == 0 ? 32 * i >= ROW / 2 : row >= 8) ? k1 : k0;
+                    copy16(dst, src + i * 512);
+                    copy16(dst + Lay::V0, src + v_minus_k + i * 512);
+                }
             }
         }
     };
@@ -211,7 +215,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     int base = begin + warp * KT;
     int id[SUB][2];                                   // pages of the next tile to load
     int ahead = base;                                 // its first key
-    const bool known = rg.lo16 == 0 && one_page;
+    const bool known = ONE && rg.lo16 == 0;
     if (known) id[0][0] = first_page[0];
     else page_ids(ahead, id);
 #pragma unroll
@@ -725,12 +729,12 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     }
 }
 
-template <int D, bool HI, int NT, int SUB, int STAGES, int MINB>
+template <int D, bool HI, int NT, int SUB, int STAGES, int MINB, bool ONE>
 __global__ void __launch_bounds__(kThreads, MINB)
     k_attn_q4(const __grid_constant__ AttnArgs a, int splits, int chunk, int head_chunks) {
     grid_dep_launch();
     grid_dep_wait();
-    attn_block_q4<D, HI, NT, SUB, STAGES>(a, splits, chunk, head_chunks);
+    attn_block_q4<D, HI, NT, SUB, STAGES, ONE>(a, splits, chunk, head_chunks);
 }
 
 }  // namespace attn
