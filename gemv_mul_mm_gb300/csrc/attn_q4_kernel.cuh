@@ -521,17 +521,14 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
         };
         unsigned bands = 1;                           // those that have a weight in this tile
         if constexpr (HI) {
-            bool low = false;
+            float least = INFINITY;
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        low |= y[u][n][i] < kLow && y[u][n][i] >= kLow - 3 * kBand;
-                        l[n][i & 1] += ex2(y[u][n][i]);
-                    }
-            if (__any_sync(0xffffffffu, low)) {
+                    for (int i = 0; i < 4; ++i) least = fminf(least, y[u][n][i]);
+            if (__any_sync(0xffffffffu, least < kLow)) {
 #pragma unroll 1
                 for (int k = 1; k < 4; ++k) {
                     bool in = false;
@@ -561,8 +558,9 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         x[i] = ex2(HI ? y[u][n][i] + kBand * static_cast<float>(k) : y[u][n][i]);
-                        if (!HI) l[n][i & 1] += x[i];
                         if (HI && bands > 1 && !in_band(y[u][n][i], k)) x[i] = isnan(x[i]) ? x[i] : 0.f;
+                        if (HI) l[n][i & 1] = fmaf(x[i], down, l[n][i & 1]);
+                        else l[n][i & 1] += x[i];
                     }
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
