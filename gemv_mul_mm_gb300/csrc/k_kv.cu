@@ -92,13 +92,17 @@ __device__ __forceinline__ Place place_of(const KvStoreArgs& a, int64_t t, bool 
     return p;
 }
 
+// Whether a thread issues the next heads' loads before it quantises and writes these.
+// (q4_0: 16384 x 8 x 128 fp32 36 us at two blocks per SM, 38 without at three.)
+template <int FMT> constexpr bool kPrefetch = FMT == QMM_KV_Q4_0;
+
 // The usual rotation: half layout, whole heads, dims a multiple of 64, aligned.
 // One thread owns eight elements of a head's first half and their partners, of
 // `heads_per` heads of one token of K (blockIdx.y 0) or of V: every element
 // is read once and a cos and sin serve two of them in every head. 16384 x 8 x
 // 128 fp32 to q8_0: 38 us, against 45 with the partner reads of k_kv_store.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
+__global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_pairs(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
     grid_dep_launch();
     grid_dep_wait();
     const int64_t id0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
@@ -116,15 +120,30 @@ __global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, i
     const T* x = static_cast<const T*>(is_v ? a.V : a.K) + t * (is_v ? a.v_ts : a.k_ts);
     const int64_t hs = is_v ? a.v_hs : a.k_hs;
     float c[N], s[N];
+    // the last group repeats its last head: lanes stay together
+    auto head = [&](int k) { return min(h0 + k, h1 - 1); };
+    auto load = [&](int i, Vec<T, N> (&v0)[kB], Vec<T, N> (&v1)[kB]) {
+#pragma unroll
+        for (int k = 0; k < kB; ++k) {
+            v0[k].load(x + head(i + k) * hs + e);
+            v1[k].load(x + head(i + k) * hs + e + half);
+        }
+    };
+    constexpr bool AHEAD = kPrefetch<FMT>;
+    Vec<T, N> n0[kB], n1[kB];
+    if constexpr (AHEAD) load(0, n0, n1);
 #pragma unroll 1
     for (int i = 0; i < heads_per; i += kB) {
         Vec<T, N> v0[kB], v1[kB];
-        // the last group repeats its last head: lanes stay together
-        auto head = [&](int k) { return min(h0 + i + k, h1 - 1); };
+        if constexpr (AHEAD) {
 #pragma unroll
-        for (int k = 0; k < kB; ++k) {
-            v0[k].load(x + head(k) * hs + e);
-            v1[k].load(x + head(k) * hs + e + half);
+            for (int k = 0; k < kB; ++k) {
+                v0[k] = n0[k];
+                v1[k] = n1[k];
+            }
+            if (i + kB < heads_per) load(i + kB, n0, n1);
+        } else {
+            load(i, v0, v1);
         }
         if (!is_v && i == 0) {           // behind the first loads
             const int32_t pos = a.pos[t];
@@ -145,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, i
                     f0[j] = y;
                 }
             }
-            put8<FMT>(a.c, at.base + head(k) * unit, at.row, e, f0, at.writes);
-            put8<FMT>(a.c, at.base + head(k) * unit, at.row, e + half, f1, at.writes);
+            put8<FMT>(a.c, at.base + head(i + k) * unit, at.row, e, f0, at.writes);
+            put8<FMT>(a.c, at.base + head(i + k) * unit, at.row, e + half, f1, at.writes);
         }
     }
 }
