@@ -139,23 +139,24 @@ def test_bad_slots(Q):
     assert torch.isnan(K[1:3]).all() and torch.isnan(V[1:3]).all() and torch.isfinite(K[0]).all() and torch.equal(K[3], V[3])
 
 
-def test_offsets_past_32_bits(Q):
+@pytest.mark.parametrize("page", [16, 32])
+def test_offsets_past_32_bits(Q, page):
     import torch
-    page, H, D, fmt = 16, 2, 64, "q4_0"
+    H, D, fmt = 2, 64, "q4_0"
     nbytes = Q.qkv_page_bytes(fmt, page, H, D)
     stride = (1 << 31) + 4096
     big = torch.empty(2 * stride + 2 * nbytes, dtype=torch.uint8, device="cuda")
     kc = big.as_strided((3, nbytes), (stride, 1), 0)
     vc = big.as_strided((3, nbytes), (stride, 1), nbytes)
-    x, y = randn((48, H, D), "f32", 1), randn((48, H, D), "f32", 2)
-    slots = torch.randperm(48, generator=torch.Generator().manual_seed(1)).cuda()
+    x, y = randn((3 * page, H, D), "f32", 1), randn((3 * page, H, D), "f32", 2)
+    slots = torch.randperm(3 * page, generator=torch.Generator().manual_seed(1)).cuda()
     Q.qkv_store(fmt, x, y, slots, kc, vc, page)
     small = Q.qkv_cache(fmt, 3, page, H, D)
     Q.qkv_store(fmt, x, y, slots, small[0], small[1], page)
     for a, b in zip(Q.qkv_load(fmt, slots, kc, vc, page, H, D), Q.qkv_load(fmt, slots, small[0], small[1], page, H, D)):
         assert torch.equal(a, b) and float(a.abs().max()) > 0
     q = randn((1, 4, D), "f16", 3)
-    table, lens = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"), torch.tensor([47], dtype=torch.int32, device="cuda")
+    table, lens = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"), torch.tensor([3 * page - 1], dtype=torch.int32, device="cuda")
     assert torch.equal(Q.qattn_decode(fmt, q, kc, vc, table, lens, page, H),
                        Q.qattn_decode(fmt, q, small[0], small[1], table, lens, page, H))
     assert Q.check_device_error() == 0

@@ -67,16 +67,34 @@ def test_many_tokens(Q):
     check(Q, randn((20000, 128), "bf16", 3), 8)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top,score,biased", [
+    (128, 8, 1, 1, 1, "softmax", False), (64, 6, 1, 1, 1, "sigmoid", True), (128, 8, 4, 2, 2, "softmax", True),
+    (256, 8, 8, 4, 2, "sigmoid", True), (256, 1, 8, 1, 1, "softmax", False), (192, 7, 2, 1, 2, "sigmoid", False),
+    (160, 5, 5, 3, 2, "softmax", True), (48, 8, 3, 2, 1, "sigmoid", False), (40, 3, 1, 1, 1, "softmax", True)])
+def test_batches_of_four_tokens_a_warp(Q, dt, E, k, groups, top_groups, group_top, score, biased):
+    """Large calls, not a multiple of four tokens, with rows of equal values among them."""
+    import torch
+    x = randn((9731, E), dt, E)
+    x[17::501] = 0
+    x[40::333, ::3] = x[40::333, :1]
+    check(Q, x, k, score, 0.2 * randn((E,), "f32", 2) if biased else None, groups, top_groups, group_top)
+
+
+@pytest.mark.parametrize("times", [1, 300])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups,top_groups,group_top,k", [(64, 1, 1, 1, 8), (64, 8, 4, 2, 8), (96, 4, 2, 1, 5), (1024, 1, 1, 1, 32),
-                                                             (256, 8, 3, 2, 32)])
-def test_equal_values_go_to_the_lower_index(Q, score, E, groups, top_groups, group_top, k):
+                                                             (256, 8, 3, 2, 32), (256, 8, 3, 2, 8)])
+def test_equal_values_go_to_the_lower_index(Q, score, E, groups, top_groups, group_top, k, times):
     import torch
+    if times > 1 and E == 1024:
+        times = 3
     x = torch.zeros((40, E), device="cuda")                         # padded rows: all equal
     g = torch.Generator(device="cuda").manual_seed(E)
     x[10:20] = torch.randint(0, 2, (10, E), generator=g, device="cuda").float()
     x[20:30] = torch.randint(-3, 3, (10, E), generator=g, device="cuda").float()
     x[30:, : E // 2], x[30:35, E // 2:] = -0.0, 0.0
+    x = x.repeat(times, 1)
     for bias in (None, torch.zeros(E, device="cuda"), torch.full((E,), 0.25, device="cuda"),
                  torch.randint(0, 2, (E,), generator=g, device="cuda").float()):
         check(Q, x, k, score, bias, groups, top_groups, group_top)
@@ -97,9 +115,14 @@ def test_values_that_fp32_cannot_tell_apart(Q, score, group_top):
         check(Q, x[t:t + 1], 8, score, bias)
         check(Q, x[t:t + 1], 8, score, bias, 8, 4, group_top)
         check(Q, x[t:t + 10], 8, score, bias, 4, 2, group_top)
+        if t % 50 == 0:                                             # four tokens a warp
+            many = x[t:t + 1].expand(8000, -1) + 0.0
+            check(Q, many, 8, score, bias)
+            check(Q, many, 8, score, bias, 4, 2, group_top)
 
 
-def test_infinite_and_nan_logits(Q):
+@pytest.mark.parametrize("times", [1, 1000])
+def test_infinite_and_nan_logits(Q, times):
     import torch
     inf, nan = math.inf, math.nan
     x = randn((8, 40), "f32", 1)
@@ -110,6 +133,7 @@ def test_infinite_and_nan_logits(Q):
     x[4] = nan
     x[5, ::2] = -inf
     x[6] = -200.0                                                   # sigmoids of all zero in fp32
+    x = x.repeat(times, 1)
     for score in ("softmax", "sigmoid"):
         for bias in (None, 0.1 * randn((40,), "f32", 2)):
             for groups in (1, 4):
