@@ -36,22 +36,22 @@ template <typename K> cudaError_t launch_kernel(const Launch& l, K kernel, int b
 }
 
 #ifdef QMM_ATTN_Q4
-template <int D, bool HI, int NT, int SUB, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
+template <int D, bool HI, int NT, int MINB> cudaError_t go_with(const Launch& l) {
     static std::atomic<int> fits[kDevices], fits_small[kDevices];
-    constexpr int bytes = Layout4<D, NT, SUB, STAGES>::BYTES;
+    constexpr int bytes = Layout4<D, NT>::BYTES;
     // (a plan, without blocks, has no page size)
-    if (l.blocks && (1 << l.a.c.page_shift) < 16 * SUB)
-        return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB, false>, bytes, fits_small);
-    return launch_kernel(l, k_attn_q4<D, HI, NT, SUB, STAGES, MINB, true>, bytes, fits);
+    if (l.blocks && (1 << l.a.c.page_shift) < Layout4<D, NT>::KT)
+        return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, false>, bytes, fits_small);
+    return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, true>, bytes, fits);
 }
 
-// Keys per tile, depth of the ring and blocks per SM, measured on 64 sequences of 8192
-// tokens and on one of 131072 (f16 activations, 8 heads of 128). Instructions bound the
-// kernel (62 % of the issue slots, 0.57 of the copy bandwidth): tiles of 32 keys take
-// 156 and 45 us, of 16 keys 184, of 64 206 us; four blocks, for which registers
-// spill, 154 and 51; three stages 157 and 57 us. Dim 64 fits four blocks (97 us, 109 with three).
+// Blocks per SM, keys per tile and depth of the ring, measured on 64 sequences of 8192
+// tokens and on one of 131072 (f16 activations, 8 key-value heads of 128). Instructions bound
+// the kernel: tiles of 32 keys, two stages and three blocks take 140 and 40 us; four blocks, for
+// which registers spill, 145 and 45; tiles of 16 keys 154 and 47, of 64 155 and 43;
+// three stages 142 and 42. Dim 64 fits four blocks (64 x 8192: 90 us).
 template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
-    return go_with<D, HI, NT, 2, 2, (D > 128 || NT == 2 ? 2 : D == 64 ? 4 : 3)>(l);
+    return go_with<D, HI, NT, (D > 128 || NT == 2 ? 2 : D == 64 ? 4 : 3)>(l);
 }
 #else
 template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {
