@@ -15,8 +15,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int N = kQuantN;
 
+// Eight q4_0 codes, and their block's scale from the lane that has its first.
+__device__ __forceinline__ void put4(const KvCache& c, uint8_t* unit, int64_t row, int e, unsigned codes, __half d) {
+    *reinterpret_cast<unsigned*>(unit + row * (c.D / 2) + e / 2) = codes;
+    if (e % 32 == 0)
+        reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D / 2) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
+}
+
 // Where a thread's eight elements of a row go: the same place in every head's
-// unit. All 32 lanes of a warp call put8 together (quant8 and quant4 shuffle); lanes with
+// unit (q4_0: put4). All 32 lanes of a warp call put8 together (quant8 shuffles); lanes with
 // `writes` false write nothing.
 template <int FMT>
 __device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t row, int e, const float (&x)[N], bool writes) {
@@ -28,14 +35,6 @@ __device__ __forceinline__ void put8(const KvCache& c, uint8_t* unit, int64_t ro
         *reinterpret_cast<uint2*>(unit + row * c.D + e) = codes;
         if (e % 32 == 0)
             reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
-    } else if constexpr (FMT == QMM_KV_Q4_0) {
-        unsigned codes;
-        __half d;
-        quant4(x, codes, d);
-        if (!writes) return;
-        *reinterpret_cast<unsigned*>(unit + row * (c.D / 2) + e / 2) = codes;
-        if (e % 32 == 0)
-            reinterpret_cast<__half*>(unit + (static_cast<int64_t>(c.D / 2) << c.page_shift))[row * (c.D / 32) + e / 32] = d;
     } else {
         if (!writes) return;
         using T = typename std::conditional<FMT == QMM_KV_F16, __half, __nv_bfloat16>::type;
@@ -102,7 +101,7 @@ template <int FMT> constexpr bool kPrefetch = FMT == QMM_KV_Q4_0;
 // is read once and a cos and sin serve two of them in every head. 16384 x 8 x
 // 128 fp32 to q8_0: 38 us, against 45 with the partner reads of k_kv_store.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_pairs(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
+__global__ void __launch_bounds__(kThreads, 3) k_kv_store_pairs(KvStoreArgs a, int64_t threads, int head_groups, int heads_per) {
     grid_dep_launch();
     grid_dep_wait();
     const int64_t id0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
@@ -115,7 +114,8 @@ __global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_p
     div_mod(r, head_groups, t, hg);
     const int h0 = hg * heads_per, h1 = min(h0 + heads_per, a.c.heads);
     const Place at = place_of(a, t, is_v, active, e == 0);
-    constexpr int kB = 2;                // heads whose loads are in flight together
+    constexpr bool AHEAD = kPrefetch<FMT>;
+    constexpr int kB = AHEAD ? 1 : 2;    // heads whose loads are in flight together
     const int64_t unit = a.c.unit();
     const T* x = static_cast<const T*>(is_v ? a.V : a.K) + t * (is_v ? a.v_ts : a.k_ts);
     const int64_t hs = is_v ? a.v_hs : a.k_hs;
@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_p
             v1[k].load(x + head(i + k) * hs + e + half);
         }
     };
-    constexpr bool AHEAD = kPrefetch<FMT>;
     Vec<T, N> n0[kB], n1[kB];
     if constexpr (AHEAD) load(0, n0, n1);
 #pragma unroll 1
@@ -153,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_p
 #pragma unroll
         for (int k = 0; k < kB; ++k) {
             if (i + k >= heads_per) break;
-            float f0[N], f1[N];
+            float f[2][N];
+            float (&f0)[N] = f[0], (&f1)[N] = f[1];
             v0[k].get(f0);
             v1[k].get(f1);
             if (!is_v) {
@@ -164,8 +164,19 @@ __global__ void __launch_bounds__(kThreads, kPrefetch<FMT> ? 2 : 3) k_kv_store_p
                     f0[j] = y;
                 }
             }
-            put8<FMT>(a.c, at.base + head(i + k) * unit, at.row, e, f0, at.writes);
-            put8<FMT>(a.c, at.base + head(i + k) * unit, at.row, e + half, f1, at.writes);
+            uint8_t* to = at.base + head(i + k) * unit;
+            if constexpr (FMT == QMM_KV_Q4_0) {
+                unsigned codes[2];
+                __half d[2];
+                quant4<2>(f, codes, d);
+                if (at.writes) {
+                    put4(a.c, to, at.row, e, codes[0], d[0]);
+                    put4(a.c, to, at.row, e + half, codes[1], d[1]);
+                }
+            } else {
+                put8<FMT>(a.c, to, at.row, e, f0, at.writes);
+                put8<FMT>(a.c, to, at.row, e + half, f1, at.writes);
+            }
         }
     }
 }
@@ -232,10 +243,7 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 3 : 5) k_kv_store(KvStoreArgs
                 }
             }
         }
-#pragma unroll
-        for (int k = 0; k < kB; ++k) {
-            if (i + k >= heads_per) break;
-            float f[N];
+        auto rotated = [&](int k, float (&f)[N]) {
             v[k].get(f);
             if (turn) {
                 float g[N];
@@ -257,7 +265,29 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 3 : 5) k_kv_store(KvStoreArgs
 #pragma unroll
                 for (int j = 0; j < N; ++j) f[j] = e + j < a.rot ? turned<FMT>(f[j], c[j], g[j], s[j]) : f[j];
             }
-            put8<FMT>(a.c, at.base + head(k) * unit, at.row, e, f, at.writes);
+        };
+        if constexpr (FMT == QMM_KV_Q4_0) {
+#pragma unroll
+            for (int k = 0; k < kB; k += 2) {            // two heads' blocks at once; the second may be a repetition
+                if (i + k >= heads_per) break;
+                float f[2][N];
+                unsigned codes[2];
+                __half d[2];
+                rotated(k, f[0]);
+                rotated(k + 1, f[1]);
+                quant4<2>(f, codes, d);
+                if (!at.writes) continue;
+                put4(a.c, at.base + head(k) * unit, at.row, e, codes[0], d[0]);
+                if (i + k + 1 < heads_per) put4(a.c, at.base + head(k + 1) * unit, at.row, e, codes[1], d[1]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+                if (i + k >= heads_per) break;
+                float f[N];
+                rotated(k, f);
+                put8<FMT>(a.c, at.base + head(k) * unit, at.row, e, f, at.writes);
+            }
         }
     }
 }

@@ -89,63 +89,80 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either 
 // |x / d| <= 12 is off by less than 2^-18. Away from subnormal d they do not
 // pass -8 by more than 2^-8, so that the upper end alone is clamped. Codes are put
 // together in fp32, four in a sum below 2^16.
-__device__ __forceinline__ void quant4(const float (&x)[kQuantN], unsigned& codes, __half& d) {
+// K vectors at once, whose shuffles overlap. All 32 lanes call it.
+template <int K> __device__ __forceinline__ void quant4(const float (&x)[K][kQuantN], unsigned (&codes)[K], __half (&d)[K]) {
     constexpr unsigned kAll = 0xffffffffu;
-    float hi = x[0], lo = x[0];
+    float hi[K], lo[K], m[K];
 #pragma unroll
-    for (int j = 1; j < kQuantN; ++j) {
-        hi = max_nan(hi, x[j]);
-        lo = min_nan(lo, x[j]);
-    }
+    for (int k = 0; k < K; ++k) {
+        hi[k] = lo[k] = x[k][0];
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        hi = max_nan(hi, __shfl_xor_sync(kAll, hi, o));
-        lo = min_nan(lo, __shfl_xor_sync(kAll, lo, o));
-    }
-    float m = hi > -lo ? hi : lo;                        // (NaN: lo is)
-    if (__any_sync(kAll, hi == -lo && hi > 0.f)) {
-        float first = 0.f;                               // of this lane's that have the magnitude
-#pragma unroll
-        for (int j = kQuantN - 1; j >= 0; --j) first = fabsf(x[j]) == hi ? x[j] : first;
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {                // the lower lane's before the upper one's
-            const float other = __shfl_xor_sync(kAll, first, o);
-            const bool upper = threadIdx.x & o;
-            const float a = upper ? other : first, b = upper ? first : other;
-            first = a != 0.f ? a : b;
+        for (int j = 1; j < kQuantN; ++j) {
+            hi[k] = max_nan(hi[k], x[k][j]);
+            lo[k] = min_nan(lo[k], x[k][j]);
         }
-        if (hi == -lo && hi > 0.f) m = first;
     }
-    d = __float2half_rn(m * -0.125f);
-    const float df = __half2float(d);
-    if (!(fabsf(df) < INFINITY)) d = __ushort_as_half(0x7fff);
-    codes = 0x88888888u;
-    if (!(fabsf(df) > 0.f && fabsf(df) < INFINITY)) return;
-    constexpr float kInt = 12582912.f;                   // 1.5 2^23: sums with it are integers
-    constexpr float kRound = kInt + 8.f;                 // the sum less kInt is the code plus 8
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df));
-    float2 u[4];                                         // codes plus 8 of elements j and j + 4
-    float off = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 v = make_float2(x[j], x[j + 4]), rr = make_float2(r, r);
-        const float2 n = fma2(v, rr, make_float2(kRound, kRound));
-        const float2 k = fma2(n, make_float2(-1.f, -1.f), make_float2(kRound, kRound));   // minus the integer
-        const float2 e = fma2(v, rr, k);
-        off = fmaxf(fmaxf(off, fabsf(e.x)), fabsf(e.y));
-        u[j] = add2(make_float2(fminf(n.x, kRound + 7.f), fminf(n.y, kRound + 7.f)), make_float2(-kInt, -kInt));
+    for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            hi[k] = max_nan(hi[k], __shfl_xor_sync(kAll, hi[k], o));
+            lo[k] = min_nan(lo[k], __shfl_xor_sync(kAll, lo[k], o));
+        }
+    bool tie = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        m[k] = hi[k] > -lo[k] ? hi[k] : lo[k];               // (NaN: lo is)
+        tie |= hi[k] == -lo[k] && hi[k] > 0.f;
     }
-    if (off > 0.49999f || fabsf(df) < 6.103515625e-05f) {
+    if (__any_sync(kAll, tie)) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float first = 0.f;                               // of this lane's that have the magnitude
+#pragma unroll
+            for (int j = kQuantN - 1; j >= 0; --j) first = fabsf(x[k][j]) == hi[k] ? x[k][j] : first;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {                // the lower lane's before the upper one's
+                const float other = __shfl_xor_sync(kAll, first, o);
+                const bool upper = threadIdx.x & o;
+                const float p = upper ? other : first, q = upper ? first : other;
+                first = p != 0.f ? p : q;
+            }
+            if (hi[k] == -lo[k] && hi[k] > 0.f) m[k] = first;
+        }
+    }
+    constexpr float kInt = 12582912.f;                       // 1.5 2^23: sums with it are integers
+    constexpr float kRound = kInt + 8.f;                     // the sum less kInt is the code plus 8
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        d[k] = __float2half_rn(m[k] * -0.125f);
+        const float df = __half2float(d[k]);
+        const bool bad = !(fabsf(df) < INFINITY), zero = df == 0.f;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df));
+        float2 u[4];                                         // codes plus 8 of elements j and j + 4
+        float off = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            u[j].x = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[j], df))));
-            u[j].y = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[j + 4], df))));
+            const float2 v = make_float2(x[k][j], x[k][j + 4]), rr = make_float2(r, r);
+            const float2 n = fma2(v, rr, make_float2(kRound, kRound));
+            const float2 i = fma2(n, make_float2(-1.f, -1.f), make_float2(kRound, kRound));   // minus the integer
+            const float2 e = fma2(v, rr, i);
+            off = fmaxf(fmaxf(off, fabsf(e.x)), fabsf(e.y));
+            u[j] = add2(make_float2(fminf(n.x, kRound + 7.f), fminf(n.y, kRound + 7.f)), make_float2(-kInt, -kInt));
         }
+        if (off > 0.49999f || fabsf(df) < 6.103515625e-05f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[j].x = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[k][j], df))));
+                u[j].y = 8.f + fmaxf(-8.f, fminf(7.f, rintf(__fdiv_rn(x[k][j + 4], df))));
+            }
+        }
+        const float2 by16 = make_float2(16.f, 16.f);
+        const float2 w = add2(fma2(fma2(fma2(u[3], by16, u[2]), by16, u[1]), by16, u[0]), make_float2(8388608.f, 8388608.f));
+        codes[k] = bad || zero ? 0x88888888u : __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
+        if (bad) d[k] = __ushort_as_half(0x7fff);
     }
-    const float2 by16 = make_float2(16.f, 16.f);
-    const float2 w = add2(fma2(fma2(fma2(u[3], by16, u[2]), by16, u[1]), by16, u[0]), make_float2(8388608.f, 8388608.f));
-    codes = __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
 }
 
 }  // namespace qmm
