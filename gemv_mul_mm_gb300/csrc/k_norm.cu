@@ -8,6 +8,7 @@
 // do not allow 16-byte accesses); short rows take part of a warp each, long ones
 // a block each, and rows that no block can hold are read twice.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_common.cuh"
 #include "quant.cuh"
@@ -181,6 +182,22 @@ template <int N, int MODE> __device__ __forceinline__ void weights(const NormArg
         Vec<float, N> v;
         v.load(a.W + e);
         v.get(w);
+    } else if (MODE == kShift && a.w_at16 && e >= 0 && e - (e & 3) + 12 <= a.D) {
+        // three aligned vectors around them; where they lie in those is alike for a whole row
+        float f[12];
+        Vec<float, 12> v;
+        v.load(a.W + (e - (e & 3)));
+        v.get(f);
+        auto from = [&](auto first) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = f[(j + decltype(first)::value) % 12];
+        };
+        switch (e & 3) {
+        case 0: from(std::integral_constant<int, 0>{}); break;
+        case 1: from(std::integral_constant<int, 1>{}); break;
+        case 2: from(std::integral_constant<int, 2>{}); break;
+        default: from(std::integral_constant<int, 3>{});
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) w[j] = MODE == kOne || (e + j >= 0 && e + j < a.D) ? a.W[e + j] : 0.f;
@@ -228,7 +245,7 @@ template <int N> __device__ __forceinline__ void scale(float (&h)[N], float inv,
 }
 
 // A row in `group` threads of a warp (a power of two), ITEMS vectors a thread.
-template <int N, int MODE, int ITEMS>
+template <int N, int MODE, bool RES, int ITEMS>
 __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ NormArgs a, int group, int64_t rows) {
     grid_dep_launch();
     grid_dep_wait();
@@ -239,14 +256,13 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
     const int64_t row = warp * per + lane / group;
     const bool live = row < rows;
     const Row at = row_of(a, live ? row : rows - 1);
-    Raw<N> x[ITEMS], r[ITEMS];
-    const bool res = a.R != nullptr;
+    Raw<N> x[ITEMS], r[RES ? ITEMS : 1];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int e = (k * group + in) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
-            if (res) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
+            if constexpr (RES) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         }
     }
     float h[ITEMS][N];
@@ -256,7 +272,7 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
         const int e = (k * group + in) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].get(h[k], a.x_dt);
-            if (res) {
+            if constexpr (RES) {
                 float f[N];
                 r[k].get(f, a.r_dt);
                 add_to(h[k], f);
@@ -291,7 +307,7 @@ __global__ void __launch_bounds__(kWide) k_norm_warp(const __grid_constant__ Nor
 }
 
 // A row a block.
-template <int N, int MODE, int ITEMS, int MOST>
+template <int N, int MODE, bool RES, int ITEMS, int MOST>
 __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ NormArgs a) {
     grid_dep_launch();
     grid_dep_wait();
@@ -299,14 +315,13 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
     __shared__ float part[32];
     const int lane = threadIdx.x % 32, wid = threadIdx.x / 32, threads = static_cast<int>(blockDim.x);
     const Row at = row_of(a, blockIdx.x);
-    Raw<N> x[ITEMS], r[ITEMS];
-    const bool res = a.R != nullptr;
+    Raw<N> x[ITEMS], r[RES ? ITEMS : 1];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int e = (k * threads + static_cast<int>(threadIdx.x)) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
-            if (res) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
+            if constexpr (RES) r[k].template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         }
     }
     float h[ITEMS][N];
@@ -316,7 +331,7 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
         const int e = (k * threads + static_cast<int>(threadIdx.x)) * N - (MODE == kShift ? at.shift : 0);
         if (e < a.D) {
             x[k].get(h[k], a.x_dt);
-            if (res) {
+            if constexpr (RES) {
                 float f[N];
                 r[k].get(f, a.r_dt);
                 add_to(h[k], f);
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(MOST) k_norm_block(const __grid_constant__ Nor
 
 // Rows too long for a block's registers: x and r are read again for the product
 // (r' may be r or x, so that it is written with y).
-template <int N, int MODE>
+template <int N, int MODE, bool RES>
 __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ NormArgs a) {
     grid_dep_launch();
     grid_dep_wait();
@@ -364,13 +379,12 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
     __shared__ float part[32];
     const int lane = threadIdx.x % 32, wid = threadIdx.x / 32, threads = static_cast<int>(blockDim.x);
     const Row at = row_of(a, blockIdx.x);
-    const bool res = a.R != nullptr;
     auto sum_of = [&](int64_t e, float (&h)[N]) {
         Raw<N> x, r;
         x.template load<MODE>(a.X, at.x + e, a.x_dt, e, a.D);
-        if (res) r.template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
+        if constexpr (RES) r.template load<MODE>(a.R, at.r + e, a.r_dt, e, a.D);
         x.get(h, a.x_dt);
-        if (res) {
+        if constexpr (RES) {
             float f[N];
             r.get(f, a.r_dt);
             add_to(h, f);
@@ -396,7 +410,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
         for (int j = 0; j < N; ++j) h[j] = 0.f;
         if (mine) {
             sum_of(e, h);
-            if (a.RO) put<N, MODE>(a.RO, at.ro + e, a.r_dt, h, e, a.D);
+            if (RES && a.RO) put<N, MODE>(a.RO, at.ro + e, a.r_dt, h, e, a.D);
             float w[N];
             weights<N, MODE>(a, e, w);
             scale(h, inv, w);
@@ -416,7 +430,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const __grid_constant__ Norm
 // vectors (latency); from four rows per SM on a thread takes four, whose loads
 // are in flight together, and rows of up to four vectors a lane a warp alone. (Rows of a
 // vector a lane are bound by instructions: two or four at a time were slower.)
-template <int N, int MODE> cudaError_t run(const NormArgs& a, cudaStream_t s) {
+template <int N, int MODE, bool RES> cudaError_t run(const NormArgs& a, cudaStream_t s) {
     const int64_t rows = a.T * a.H, vecs = (a.D + (MODE == kShift ? 7 : 0) + N - 1) / N;
     if (rows > 0x7fffffff) return cudaErrorInvalidValue;
     int dev = 0;
@@ -429,22 +443,22 @@ template <int N, int MODE> cudaError_t run(const NormArgs& a, cudaStream_t s) {
         while (group < 32 && group < vecs) group *= 2;
         const int64_t per_block = kWide / group, blocks = (rows + per_block - 1) / per_block;
         auto go = [&](auto k, int64_t n) { return launch_chained(k, dim3(static_cast<unsigned>(n)), kWide, 0, s, a, group, rows); };
-        return vecs <= 32   ? go(k_norm_warp<N, MODE, 1>, blocks)
-               : vecs <= 64 ? go(k_norm_warp<N, MODE, 2>, blocks)
-                            : go(k_norm_warp<N, MODE, 4>, blocks);
+        return vecs <= 32   ? go(k_norm_warp<N, MODE, RES, 1>, blocks)
+               : vecs <= 64 ? go(k_norm_warp<N, MODE, RES, 2>, blocks)
+                            : go(k_norm_warp<N, MODE, RES, 4>, blocks);
     }
     const dim3 grid(static_cast<unsigned>(rows));
     auto go = [&](auto k, int items) {
         return launch_chained(k, grid, static_cast<int>((vecs + items * 32 - 1) / (items * 32)) * 32, 0, s, a);
     };
-    if (!many && vecs <= 512) return go(k_norm_block<N, MODE, 1, 512>, 1);
-    if (!many && vecs <= 1024) return go(k_norm_block<N, MODE, 2, 512>, 2);
-    if (vecs <= 1024) return go(k_norm_block<N, MODE, 4, 256>, 4);
-    if (vecs <= 4096) return go(k_norm_block<N, MODE, 4, 1024>, 4);
+    if (!many && vecs <= 512) return go(k_norm_block<N, MODE, RES, 1, 512>, 1);
+    if (!many && vecs <= 1024) return go(k_norm_block<N, MODE, RES, 2, 512>, 2);
+    if (vecs <= 1024) return go(k_norm_block<N, MODE, RES, 4, 256>, 4);
+    if (vecs <= 4096) return go(k_norm_block<N, MODE, RES, 4, 1024>, 4);
     if constexpr (N == 1) {
-        if (vecs <= 16384) return go(k_norm_block<N, MODE, 16, 1024>, 16);
+        if (vecs <= 16384) return go(k_norm_block<N, MODE, RES, 16, 1024>, 16);
     }
-    return launch_chained(k_norm_long<N, MODE>, grid, 1024, 0, s, a);
+    return launch_chained(k_norm_long<N, MODE, RES>, grid, 1024, 0, s, a);
 }
 
 }  // namespace
@@ -458,15 +472,20 @@ cudaError_t launch_norm(const NormArgs& args, cudaStream_t s) {
     a.h_mul = static_cast<unsigned>(((uint64_t(1) << (32 + a.h_shift)) + static_cast<uint64_t>(a.H) - 1) / static_cast<uint64_t>(a.H));
     auto size = [](int dt) { return static_cast<int64_t>(dt == QMM_F32 ? 4 : 2); };
     const bool q8 = a.y_fmt == QMM_NORM_Q8_0;
+    auto go = [&](auto n, auto mode) {
+        constexpr int N = decltype(n)::value, MODE = decltype(mode)::value;
+        return a.R ? run<N, MODE, true>(a, s) : run<N, MODE, false>(a, s);
+    };
     auto ok = [&](const void* p, int64_t ts, int64_t hs, int64_t sz) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.T == 1 || ts * sz % 16 == 0) && (a.H == 1 || hs * sz % 16 == 0);
     };
     const bool vec = a.D % 8 == 0 && ok(a.X, a.x_ts, a.x_hs, size(a.x_dt)) && (!a.R || ok(a.R, a.r_ts, a.r_hs, size(a.r_dt))) &&
                      (!a.RO || ok(a.RO, a.ro_ts, a.ro_hs, size(a.r_dt))) && ok(a.W, 0, 0, 4) &&
                      (q8 || ok(a.Y, a.y_ts, a.y_hs, size(a.y_fmt)));
-    if (vec) return run<8, kVec>(a, s);
-    if (q8) return run<8, kOne>(a, s);
+    if (vec) return go(std::integral_constant<int, 8>{}, std::integral_constant<int, kVec>{});
+    if (q8) return go(std::integral_constant<int, 8>{}, std::integral_constant<int, kOne>{});
     // vectors of eight elements on a grid of 8 * size bytes: every array's rows begin alike
+    a.w_at16 = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
     a.x_shift = static_cast<int>(reinterpret_cast<uintptr_t>(a.X) / size(a.x_dt) % 8);
     auto alike = [&](const void* p, int64_t ts, int64_t hs, int64_t sz) {
         return static_cast<int>(reinterpret_cast<uintptr_t>(p) / sz % 8) == a.x_shift && (a.T == 1 || (ts - a.x_ts) % 8 == 0) &&
@@ -474,8 +493,8 @@ cudaError_t launch_norm(const NormArgs& args, cudaStream_t s) {
     };
     if (a.D >= 32 && (!a.R || alike(a.R, a.r_ts, a.r_hs, size(a.r_dt))) && (!a.RO || alike(a.RO, a.ro_ts, a.ro_hs, size(a.r_dt))) &&
         alike(a.Y, a.y_ts, a.y_hs, size(a.y_fmt)))
-        return run<8, kShift>(a, s);
-    return run<1, kOne>(a, s);
+        return go(std::integral_constant<int, 8>{}, std::integral_constant<int, kShift>{});
+    return go(std::integral_constant<int, 1>{}, std::integral_constant<int, kOne>{});
 }
 
 }  // namespace qmm

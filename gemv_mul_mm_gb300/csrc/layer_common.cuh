@@ -18,6 +18,7 @@ struct NormArgs {
     float w_off, eps;
     unsigned h_mul = 0;            // row / H (set by the launcher, as is x_shift)
     int h_shift = 0;
+    bool w_at16 = false;           // W on a 16-byte boundary
     int x_shift = 0;               // elements by which X begins past an 8-element grid
     int64_t T, H, D;
 };
