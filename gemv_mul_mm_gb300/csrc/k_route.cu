@@ -122,6 +122,14 @@ __device__ __forceinline__ float score32(bool softmax, float x, float top, float
 // Twice its error at magnitude |c| (k_route's comment), from its part at c = 0.
 __device__ __forceinline__ float tau_of(float base, float v) { return base + 2.384185791015625e-07f * fabsf(v); }   // 2^-22
 
+// What a group's value is off by at most, with some room: a sum of two by as much as
+// both, whatever is left of them, and by its rounding. Infinite values are not off, and those of
+// equal ones (and NaN) that stay are the first, as in 64 bits.
+__device__ __forceinline__ float group_off(float base, int group_top, unsigned m1, unsigned m2) {
+    const float v1 = value_of(m1), v2 = group_top == 2 ? value_of(m2) : 0.f;
+    return isinf(v1) || isinf(v2) ? 0.f : tau_of(base, fabsf(v1) + fabsf(v2));
+}
+
 // The groups that stay, as bits; 16 bytes of `mem` an expert. Of all c in fp32 only the
 // few that may be among a group's group_top largest are computed, a lane for each.
 __device__ __noinline__ unsigned groups64(const RouteArgs& a, int64_t t, float top, float sum, float base, uint8_t* mem) {
@@ -264,7 +272,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s += top == -INFINITY ? 0.f : __expf(x[i] - top);
-        sum = warp_sum(s);
+        s = warp_sum(s);
+        sum = top == -INFINITY ? 1.f : s;
     }
     // ---- c in fp32, as keys (the logits themselves where their order is the scores')
     unsigned key[V];
@@ -331,11 +340,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
         }
         kept = __ballot_sync(kAll, mine && place < a.top_groups);
         if (BY_SCORE && a.top_groups < a.groups) {
-            const unsigned last = __reduce_min_sync(kAll, kept >> lane & 1 ? k : kAll);
-            const unsigned next = __reduce_max_sync(kAll, kept >> lane & 1 ? 0u : k);
-            const float lo = value_of(last), hi = value_of(next);
-            // (a sum of two is off by as much as both, and twice that again for the difference)
-            if (last != kAll && lo - hi <= tau(lo) + tau(hi)) kept = groups64(a, t, top, sum, base, smem);
+            const float v = value_of(k), off = group_off(base, a.group_top, m1, m2);
+            const float lo = value_of(__reduce_min_sync(kAll, kept >> lane & 1 ? key_of(v - off) : kAll));
+            const float hi = value_of(__reduce_max_sync(kAll, mine && !(kept >> lane & 1) ? key_of(v + off) : 0u));
+            if (lo <= hi && fabsf(hi) < INFINITY) kept = groups64(a, t, top, sum, base, smem);
         }
         // those that do not stay: key 0
         int g = e0 / gs, left = gs - (e0 - g * gs);
@@ -448,13 +456,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
         if (a.renorm) top = biased ? value_of(__reduce_max_sync(kAll, key_of(lx))) : value_of(key_in(sorted[0]));
         w = top == -INFINITY ? 0.f : expf(lx - top);
         if (!a.renorm) w /= sum;
+        if (BY_SCORE && isnan(sum)) w = sum;              // by a logit that need not be among the chosen
     } else {
         w = 1.f / (1.f + expf(-lx));
     }
     if (a.renorm) {
         float s = chosen ? w : 0.f;
         for (int o = 1; o < a.top_k; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
-        w = s == 0.f ? 0.f : __fdividef(w, s);
+        w = s == 0.f ? 0.f : softmax ? __fdividef(w, s) : w / s;   // (a softmax's s is 1 .. top_k)
     }
     if (chosen) {
         a.ids[t * a.top_k + lane] = e;
@@ -526,7 +535,8 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s += top == -INFINITY ? 0.f : __expf(x[i] - top);
-        sum = sum8(s);
+        s = sum8(s);
+        sum = top == -INFINITY ? 1.f : s;
     }
     unsigned key[V];
     [[maybe_unused]] float base = 0.f;
@@ -567,9 +577,10 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
         }
         bool stays = mine && place < a.top_groups;
         if (BY_SCORE && a.top_groups < a.groups) {
-            const unsigned last = ~max8(stays ? ~k : 0u), next = max8(stays ? 0u : k);
-            const float lo = value_of(last), hi = value_of(next);
-            const bool near = last != kAll && lo - hi <= tau(lo) + tau(hi);
+            const float v = value_of(k), off = group_off(base, a.group_top, m1, m2);
+            const float lo = value_of(~max8(stays ? ~key_of(v - off) : 0u));
+            const float hi = value_of(max8(mine && !stays ? key_of(v + off) : 0u));
+            const bool near = lo <= hi && fabsf(hi) < INFINITY;
             for (unsigned redo = __ballot_sync(kAll, near && sl == 0); redo; redo &= redo - 1u) {
                 // by the whole warp, whose shared memory holds nothing yet
                 const int from = __ffs(static_cast<int>(redo)) - 1;
@@ -697,12 +708,13 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
         if (a.renorm) top = biased ? value_of(max8(chosen ? key_of(lx) : 0u)) : value_of(key_in(sorted[0]));
         w = top == -INFINITY ? 0.f : expf(lx - top);
         if (!a.renorm) w /= sum;
+        if (BY_SCORE && isnan(sum)) w = sum;              // by a logit that need not be among the chosen
     } else {
         w = 1.f / (1.f + expf(-lx));
     }
     if (a.renorm) {
         const float s = sum8(chosen ? w : 0.f);
-        w = s == 0.f ? 0.f : __fdividef(w, s);
+        w = s == 0.f ? 0.f : softmax ? __fdividef(w, s) : w / s;   // (a softmax's s is 1 .. top_k)
     }
     if (chosen && !leave && t0 + seg < a.T) {
         a.ids[t * a.top_k + sl] = e;

@@ -459,7 +459,8 @@ QMM_API int qrope(const void* X, int dtype, size_t x_elems, int64_t x_ts, int64_
  * in [-127, 127]; d = 0 gives codes 0; a block holding an Inf or NaN, or whose
  * d overflows f16, gets d = NaN, so that it reads back as NaN. QMM_KV_Q4_0 the
  * same with d = f16(m / -8) for the value m of largest magnitude (the first of
- * them) and codes in [-8, 7].
+ * them) and codes in [-8, 7]. Its keys are rotated as a plain fp32 computation
+ * rotates them (the angle rounded to fp32, cos and sin within 3e-7).
  *
  *   K, V     device, dtype, element (t, h, d) at t * ts + h * hs + d; sizes in
  *            elements
@@ -505,7 +506,7 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * more and the result is as near as a plain fp32 computation's. With q of the
  * cache's type the weights carry 22 bits (16 over bf16), and sums over up to 16384
  * keys are cut off, not rounded, to 24: 2^-16 and less of the result, before the
- * output's one rounding to 16 bits (over Q4_0 f16 q counts as the cache's type).
+ * output's one rounding to 16 bits (over Q4_0 f16 and bf16 q count as the cache's type).
  * Scores in log2 units (times 1.4427) have to
  * be finite floats, and |scale| times the largest |q| of a row below 2^136.
  *
@@ -559,7 +560,8 @@ QMM_API int qattn_decode_splits(int fmt, int dtype, int64_t B, int n_q_heads, in
  * The norm takes h before it is rounded for residual_out. H = 1 norms tokens; more
  * norm each head of a projection's rows. A row whose sum of squares passes
  * the fp32 range (values of about 2^60 and more) gives zeros, one that holds an
- * Inf or NaN gives NaN.
+ * Inf or NaN gives NaN; with eps = 0 one of zeros, or of values so small that
+ * all squares vanish in fp32 (below 2^-75), is divided by zero.
  *
  *   X             device, x_dtype, element (t, h, d) at t * x_ts + h * x_hs + d
  *   residual      device, r_dtype, the same at r_ts, r_hs, or NULL

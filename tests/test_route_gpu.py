@@ -158,6 +158,56 @@ def test_infinite_and_nan_logits(Q, times):
     check(Q, x[[0, 5, 7]], 10, "softmax", bias)
 
 
+@pytest.mark.parametrize("T", [5, 8002])
+@pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_rows_without_a_finite_logit(Q, T, groups, top_groups, group_top, renorm):
+    """A row of only -Inf has scores of zero, also where they are not renormalised."""
+    x = randn((T, 64), "f32", 1)
+    x[::3] = -math.inf
+    for bias in (None, 0.1 * randn((64,), "f32", 2)):
+        check(Q, x, 6, "softmax", bias, groups, top_groups, group_top, renorm)
+
+
+@pytest.mark.parametrize("T", [5, 8002])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_a_softmax_without_a_value_gives_nan_weights(Q, T, bad, groups, group_top, renorm):
+    """The infinite or NaN logit makes all of the token's scores NaN, chosen or not."""
+    import torch
+    x = randn((T, 64), "f32", 1)
+    x[1::3, 61] = bad
+    for bias in (None, 0.1 * randn((64,), "f32", 2)):
+        ids, w = Q.qmoe_route(x, 6, bias=bias, groups=groups, top_groups=min(2, groups), group_top=group_top, renorm=renorm)
+        nan = torch.isnan(w)
+        assert bool(nan[1::3].all()) and not bool(nan[::3].any()) and not bool(nan[2::3].any())
+        i = ids.cpu().numpy()
+        assert i.min() >= 0 and i.max() < 64 and all(len(set(r)) == 6 for r in i)
+
+
+@pytest.mark.parametrize("T", [150, 8002])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("by", [50.0, 3e5])
+def test_biases_of_either_sign_that_cancel_in_a_group(Q, T, score, by):
+    """The two largest of each group are near by and -by: fp32 has rounded the scores
+    in both, the sums of the real numbers are theirs."""
+    import torch
+    bias = torch.full((64,), -by, device="cuda")
+    bias[::8] = by
+    check(Q, randn((T, 64), "f32", 3), 4, score, bias, 8, 4, 2)
+
+
+def test_sigmoids_below_the_normal_range(Q):
+    """Scores of 2^-126 and less, whose sum has no fp32 inverse."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for T in (7, 8002):
+        x = -88.5 + torch.rand((T, 64), generator=g, device="cuda")
+        check(Q, x, 2, "sigmoid")
+        check(Q, x, 2, "sigmoid", 0.1 * randn((64,), "f32", 2))
+
+
 def test_refusals(Q):
     import torch
     x = randn((4, 64), "f32", 1)
