@@ -36,22 +36,26 @@ template <typename K> cudaError_t launch_kernel(const Launch& l, K kernel, int b
 }
 
 #ifdef QMM_ATTN_Q4
-template <int D, bool HI, int NT, int MINB> cudaError_t go_with(const Launch& l) {
+template <int D, bool HI, int NT, int MINB, bool PACK> cudaError_t go_with(const Launch& l) {
     static std::atomic<int> fits[kDevices], fits_small[kDevices];
     constexpr int bytes = Layout4<D, NT>::BYTES;
     // (a plan, without blocks, has no page size)
     if (l.blocks && (1 << l.a.c.page_shift) < Layout4<D, NT>::KT)
-        return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, false>, bytes, fits_small);
-    return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, true>, bytes, fits);
+        return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, false, PACK>, bytes, fits_small);
+    return launch_kernel(l, k_attn_q4<D, HI, NT, MINB, true, PACK>, bytes, fits);
 }
 
 // Blocks per SM, keys per tile and depth of the ring, measured on 64 sequences of 8192
 // tokens and on one of 131072 (f16 activations, 8 key-value heads of 128). Instructions bound
-// the kernel: tiles of 32 keys, two stages and three blocks take 140 and 40 us; four blocks, for
-// which registers spill, 145 and 45; tiles of 16 keys 154 and 47, of 64 155 and 43;
-// three stages 142 and 42. Dim 64 fits four blocks (64 x 8192: 90 us).
+// the kernel: tiles of 32 keys, two stages and three blocks take 134 and 39 us, four blocks
+// 135 and 43. (With an MMA for each term, 140 and 40 us, tiles of 16 keys took 154 and 47, of
+// 64 155 and 43, three stages 142 and 42.) Dim 64 fits four blocks (64 x 8192: 88 us; three 89).
 template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {
-    return go_with<D, HI, NT, (D > 128 || NT == 2 ? 2 : D == 64 ? 4 : 3)>(l);
+    constexpr int minb = D > 128 || NT == 2 ? 2 : D == 64 ? 4 : 3;
+    if constexpr (NT == 1) {
+        if (l.p.pack) return go_with<D, HI, 1, minb, true>(l);
+    }
+    return go_with<D, HI, NT, minb, false>(l);
 }
 #else
 template <int FMT, int D, bool HI, int NT, int STAGES, int MINB> cudaError_t go_with(const Launch& l) {

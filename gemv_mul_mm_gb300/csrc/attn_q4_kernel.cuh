@@ -8,9 +8,9 @@
 // dependent instructions to interleave. Pages of 32 keys and more hold whole tiles, which
 // are copied without a look at pages inside; smaller ones take a kernel of their own.
 //
-// Measured, 64 sequences of 8192 tokens, 8 key-value heads of 128, 4 query heads each: 140 us
-// with f16 activations (0.63 of the copy bandwidth, 4.3 TB/s; 700 instructions a tile
-// of 32 keys, 60 % of the issue slots), 176 us with fp32; one sequence of 131072: 40 and 48 us.
+// Measured, 64 sequences of 8192 tokens, 8 key-value heads of 128, 4 query heads each: 134 us
+// with f16 activations (0.66 of the copy bandwidth, 4.5 TB/s; some 680 instructions a tile
+// of 32 keys, 60 % of the issue slots), 156 us with fp32; one sequence of 131072: 39 and 44 us.
 //
 // Codes. ldmatrix reads a row's 32-dim block as eight 16-bit elements, four codes
 // each: lane (g, t) gets codes 8t .. 8t + 7 of key g (K), or dims 4g .. 4g + 3 of
@@ -26,7 +26,9 @@
 //
 // Scales as over q8_0: K's multiplies the fp32 sum of a 32-dim block, V's the two
 // f16 terms of the weights, after a power of two for each block of dims where its scales
-// pass 2 or stay below 2^-8. With 16-bit activations (bf16 rows are f16 values once scaled by
+// pass 2 or stay below 2^-8. The MMAs have eight columns, and up to four query heads fill half
+// of them: the other four then take the second terms, of the weights and of fp32 queries, of the
+// same heads (PACK: half the MMAs; 140 -> 134 and 176 -> 156 us). With 16-bit activations (bf16 rows are f16 values once scaled by
 // a power of two) the MMAs sum O, with fp32 ones each tile's part is added with rounding.
 #pragma once
 
@@ -74,11 +76,14 @@ __device__ __forceinline__ void codes4_f16(unsigned w, unsigned (&p)[4]) {
 }
 
 // ONE: pages of 32 keys and more, so that a tile lies in one page.
-template <int D, bool HI, int NT, bool ONE>
+// PACK: at most four query heads, as columns 0 .. 3 and, their second terms, 4 .. 7.
+template <int D, bool HI, int NT, bool ONE, bool PACK>
 __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int chunk, int head_chunks) {
     using Lay = Layout4<D, NT>;
     constexpr int STAGES = Lay::STAGES;
-    constexpr int NQ = HI ? 2 : 1, NP = 2;            // f16 terms of q and of the weights
+    static_assert(!PACK || NT == 1);
+    // f16 terms of q and of the weights that take an MMA each
+    constexpr int NQ = HI && !PACK ? 2 : 1, NP = PACK ? 1 : 2;
     constexpr int C = Lay::C, KT = Lay::KT, ROW = Lay::ROW, RS = Lay::RS;
     constexpr int MT = D / 16;                        // 16-dim tiles of the output
 
@@ -108,7 +113,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
         const T* q = static_cast<const T*>(a.q) + b * a.q_bs + h0 * a.q_hs;
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int j = i * kThreads + threadIdx.x, h = j / D;
+            const int j = i * kThreads + threadIdx.x, h = PACK ? j / D % 4 : j / D;
             qv[i] = h < nh ? to_f32<T>(q[h * a.q_hs + j % D]) : 0.f;
         }
     };
@@ -280,6 +285,10 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                 float x0 = sm_q[8 * n + g][d] * f, x1 = sm_q[8 * n + g][d + 4] * f;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) w[q][k] = take16<false>(x0, x1);
+                if constexpr (PACK && HI) {
+                    const unsigned second = take16<false>(x0, x1);
+                    w[0][k] = g < 4 ? w[0][k] : second;
+                }
             }
 #pragma unroll
             for (int q = 0; q < NQ; ++q) sm_qf[(n * NQ + q) * MT + j][lane] = make_uint2(w[q][0], w[q][1]);
@@ -379,6 +388,13 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                     }
                 }
             }
+        }
+
+        if constexpr (PACK && HI) {                   // both terms' scores
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sx[u][0][i] += __shfl_xor_sync(0xffffffffu, sx[u][0][i], 2);
         }
 
         // ---- scores, less ref, in log2 units
@@ -564,7 +580,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                 continue;
             }
             [[maybe_unused]] const float down = HI ? ex2(-kBand * static_cast<float>(k)) : 1.f;
-            unsigned pf[SUB][NT][NP][2];
+            unsigned pf[SUB][NT][2][2];
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -578,11 +594,18 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                         else l[n][i & 1] += x[i];
                     }
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        pf[u][n][q][0] = transpose8x8(take16<false>(x[0], x[1]));
-                        pf[u][n][q][1] = transpose8x8(take16<false>(x[2], x[3]));
+                    for (int q = 0; q < 2; ++q) {
+                        unsigned lo = take16<false>(x[0], x[1]), hi = take16<false>(x[2], x[3]);
+                        if (PACK && q == 1 && t < 2) lo = hi = 0u;
+                        pf[u][n][q][0] = transpose8x8(lo);
+                        pf[u][n][q][1] = transpose8x8(hi);
                     }
                 }
+            [[maybe_unused]] unsigned minus[SUB][2];  // -hi, or 0 where hi d is wanted itself
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) minus[u][i] = g < 4 ? 0u : pf[u][0][0][i] ^ 0x80008000u;
 #pragma unroll
             for (int c2 = 0; c2 < C; c2 += 2) {
                 unsigned w[SUB][4];
@@ -591,7 +614,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                     ldsm4_trans(w[u], stage + Lay::V0 + u * 16 * RS + (c2 + 1 < C ? m_lane : m_row) + 16 * c2);
 #pragma unroll
                 for (int c = c2; c < c2 + 2 && c < C; ++c) {
-                    unsigned pd[SUB][NT][2][2];       // p times the block's scale, in two terms
+                    unsigned pd[SUB][NT][NP][2];      // p times the block's scale, in two terms
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -599,9 +622,15 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const __half2 d = as_half2(vd[u][i][c]);
-                                const __half2 hi = as_half2(pf[u][n][0][i]), t1 = __hmul2_rn(hi, d);
-                                pd[u][n][0][i] = as_u32(t1);
-                                pd[u][n][1][i] = as_u32(__hfma2(as_half2(pf[u][n][1][i]), d, __hfma2(hi, d, __hneg2(t1))));
+                                const __half2 hi = as_half2(pf[u][n][0][i]), lo = as_half2(pf[u][n][1][i]);
+                                if constexpr (PACK) {     // columns 0 .. 3: hi d + 0; the others what that has left
+                                    const __half2 t1 = __hmul2_rn(as_half2(minus[u][i]), d);
+                                    pd[u][n][0][i] = as_u32(__hfma2(lo, d, __hfma2(hi, d, t1)));
+                                } else {
+                                    const __half2 t1 = __hmul2_rn(hi, d);
+                                    pd[u][n][0][i] = as_u32(t1);
+                                    pd[u][n][1][i] = as_u32(__hfma2(lo, d, __hfma2(hi, d, __hneg2(t1))));
+                                }
                             }
                     // the MMA's sum cuts off what does not fit in 24 bits: with HI the tile's
                     // products are summed apart and added to O with rounding
@@ -723,7 +752,11 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = sm_m[w][h];
-            const float4 v = *reinterpret_cast<const float4*>(&sm_o[(w * 8 * NT + h) * OD + d]);
+            float4 v = *reinterpret_cast<const float4*>(&sm_o[(w * 8 * NT + h) * OD + d]);
+            if constexpr (PACK) {
+                const float4 low = *reinterpret_cast<const float4*>(&sm_o[(w * 8 * NT + h + 4) * OD + d]);
+                v = make_float4(v.x + low.x, v.y + low.y, v.z + low.z, v.w + low.w);
+            }
             x.x = fmaf(f, v.x, x.x);
             x.y = fmaf(f, v.y, x.y);
             x.z = fmaf(f, v.z, x.z);
@@ -742,12 +775,12 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
     }
 }
 
-template <int D, bool HI, int NT, int MINB, bool ONE>
+template <int D, bool HI, int NT, int MINB, bool ONE, bool PACK>
 __global__ void __launch_bounds__(kThreads, MINB)
     k_attn_q4(const __grid_constant__ AttnArgs a, int splits, int chunk, int head_chunks) {
     grid_dep_launch();
     grid_dep_wait();
-    attn_block_q4<D, HI, NT, ONE>(a, splits, chunk, head_chunks);
+    attn_block_q4<D, HI, NT, ONE, PACK>(a, splits, chunk, head_chunks);
 }
 
 }  // namespace attn

@@ -83,6 +83,7 @@ cudaError_t attn_plan(int fmt, int dtype, int64_t B, int Hq, int Hkv, int D, int
     p->tiles = group > 8 && D <= 128 ? 2 : 1;
     p->head_chunks = (group + 8 * p->tiles - 1) / (8 * p->tiles);
     p->hi = attn::needs_hi(fmt, dtype);
+    p->pack = fmt == QMM_KV_Q4_0 && group <= 4;
     int resident = 0;
     attn::Launch l{};
     l.p = *p;

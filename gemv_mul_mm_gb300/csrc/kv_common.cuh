@@ -257,6 +257,7 @@ struct AttnPlan {
     int tiles;                     // 8-head tiles of a head group
     int head_chunks;               // head groups per key-value head
     bool hi;                       // the kernel with more terms
+    bool pack;                     // q4_0: two terms of up to four heads in one MMA
     size_t ws_bytes;               // what a split call asks for: no less than smaller sizes need
 };
 bool attn_dim_ok(int D);

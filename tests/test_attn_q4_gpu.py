@@ -142,6 +142,30 @@ def test_small_and_large_scores(Q, dt, qscale):
     check(Q, problem(Q, dt, 128, 1, 4, 32, [400, 90], 6, qscale))
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5])
+def test_few_query_heads_over_small_and_large_pages(Q, dt, D, group):
+    for page in (8, 32):
+        check(Q, problem(Q, dt, D, 2, group, page, [1, 31, 33, 200, 0, 411], D + group + page))
+    check(Q, problem(Q, dt, D, 2, group, 32, [90, 411], D + group), 40, 5.0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [4, 8, 16])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_without_a_value_stays_in_its_head(Q, dt, group, bad):
+    import torch
+    p = problem(Q, dt, 128, 2, group, 32, [300, 2, 5000], 3)
+    want = call(Q, p)
+    p["q"][:, 1, 7] = bad
+    p["q"][:, group + group - 1, 100] = bad
+    got = call(Q, p)
+    hit = torch.zeros(2 * group, dtype=torch.bool, device="cuda")
+    hit[[1, 2 * group - 1]] = True
+    assert bool(torch.isnan(got[:, hit]).all()) and torch.equal(got[:, ~hit], want[:, ~hit])
+
+
 def test_infinities_and_nan_in_range_show(Q):
     import torch
     p = problem(Q, "f16", 64, 1, 2, 16, [50, 50, 50], 8)
