@@ -122,6 +122,23 @@ __device__ __forceinline__ float score32(bool softmax, float x, float top, float
 // Twice its error at magnitude |c| (k_route's comment), from its part at c = 0.
 __device__ __forceinline__ float tau_of(float base, float v) { return base + 2.384185791015625e-07f * fabsf(v); }   // 2^-22
 
+// Whether q may come before p, which has the larger or an equal fp32 value: where that is near,
+// unless the inputs are the same.
+enum Near { kFar, kNear, kSame };
+__device__ __forceinline__ Near near_of(const RouteArgs& a, int64_t t, float base, Cand p, Cand q) {
+    const float v = value_of(key_in(p));
+    if (!(v - value_of(key_in(q)) <= tau_of(base, v))) return kFar;
+    const int e = expert_in(p), f = expert_in(q);
+    return logit(a, t, e) != logit(a, t, f) || a.bias[e] != a.bias[f] ? kNear : kSame;
+}
+
+// Whether any of this lane's candidates may.
+__device__ __noinline__ bool near_behind(const RouteArgs& a, int64_t t, float base, Cand p, const Cand* cand, int i, int step, int n) {
+    bool any = false;
+    for (; i < n; i += step) any |= cand[i] < p && near_of(a, t, base, p, cand[i]) == kNear;
+    return any;
+}
+
 // What a group's value is off by at most, with some room: a sum of two by as much as
 // both, whatever is left of them, and by its rounding. Infinite values are not off, and those of
 // equal ones (and NaN) that stay are the first, as in 64 bits.
@@ -434,16 +451,15 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
     __syncwarp();
     const bool chosen = lane < a.top_k;
     if (biased) {
-        bool close = false;
-        if (chosen && lane + 1 < n) {
-            const Cand p = sorted[lane], q = sorted[lane + 1];
-            const float v = value_of(key_in(p));
-            if (v - value_of(key_in(q)) <= tau(v)) {
-                const int e = expert_in(p), f = expert_in(q);
-                close = logit(a, t, e) != logit(a, t, f) || a.bias[e] != a.bias[f];
-            }
+        Near near = kFar;
+        if (chosen && lane + 1 < n) near = near_of(a, t, base, sorted[lane], sorted[lane + 1]);
+        const bool run = near == kSame && lane + 1 == a.top_k;
+        if (__any_sync(kAll, run || near == kNear)) {
+            // behind a run of equal inputs at the end others may come
+            bool close = near == kNear;
+            if (__any_sync(kAll, run)) close |= near_behind(a, t, base, sorted[a.top_k - 1], cand, lane, 32, n);
+            if (__any_sync(kAll, close)) places64(a, t, top, cand, reinterpret_cast<unsigned long long*>(value), n, sorted);
         }
-        if (__any_sync(kAll, close)) places64(a, t, top, cand, reinterpret_cast<unsigned long long*>(value), n, sorted);
     }
 
     // ---- weights
@@ -677,14 +693,14 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
     __syncwarp();
     const bool chosen = sl < a.top_k;
     if (biased) {
-        bool close = false;
+        bool close = false, run = false;
         if (chosen && sl + 1 < n) {
-            const Cand p = sorted[sl], q = sorted[sl + 1];
-            const float v = value_of(key_in(p));
-            if (v - value_of(key_in(q)) <= tau(v)) {
-                const int e = expert_in(p), f = expert_in(q);
-                close = logit(a, t, e) != logit(a, t, f) || a.bias[e] != a.bias[f];
-            }
+            const Near near = near_of(a, t, base, sorted[sl], sorted[sl + 1]);
+            close = near == kNear;
+            run = near == kSame && sl + 1 == a.top_k;
+        }
+        if (__ballot_sync(kAll, run) >> (seg * 8) & 0xffu) {   // what is behind a run of equal inputs at the end
+            close |= near_behind(a, t, base, sorted[a.top_k - 1], cand, sl, 8, n);
         }
         unsigned redo = __ballot_sync(kAll, close && !leave);
         redo = (redo | redo >> 4) & 0x0f0f0f0fu;

@@ -198,6 +198,22 @@ def test_biases_of_either_sign_that_cancel_in_a_group(Q, T, score, by):
     check(Q, randn((T, 64), "f32", 3), 4, score, bias, 8, 4, 2)
 
 
+@pytest.mark.parametrize("T", [3, 8002])
+@pytest.mark.parametrize("groups", [1, 2])
+@pytest.mark.parametrize("same", [2, 12])
+def test_equal_inputs_at_the_border_with_a_larger_value_behind(Q, T, groups, same):
+    """Equal inputs take the last place and the next in fp32, and another expert of the same fp32
+    value behind them is the larger: 22 + (1 - 9e-14) against 22 + (1 - 4e-8)."""
+    import torch
+    x = randn((T, 64), "f32", 1)
+    bias = torch.zeros(64, device="cuda")
+    bias[:7] = 30.0
+    bias[10:10 + same] = bias[31] = 22.0
+    x[:, 10:10 + same], x[:, 31] = 17.0, 30.0
+    ids, _ = check(Q, x, 8, "sigmoid", bias, groups, 1, 2)
+    assert bool((ids[:, 7] == 31).all())
+
+
 def test_sigmoids_below_the_normal_range(Q):
     """Scores of 2^-126 and less, whose sum has no fp32 inverse."""
     import torch
