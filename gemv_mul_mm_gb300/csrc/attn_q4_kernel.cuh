@@ -26,7 +26,7 @@
 //
 // Scales as over q8_0: K's multiplies the fp32 sum of a 32-dim block, V's the two
 // f16 terms of the weights, after a power of two for each block of dims where its scales
-// pass 2 or stay below 2^-8. The MMAs have eight columns, and up to four query heads fill half
+// pass 2 or stay below 2^-3 (then 1 to 2 % slower: 134 -> 136, 156 -> 159 us). The MMAs have eight columns, and up to four query heads fill half
 // of them: the other four then take the second terms, of the weights and of fp32 queries, of the
 // same heads (PACK: half the MMAs; 140 -> 134 and 176 -> 156 us). With 16-bit activations (bf16 rows are f16 values once scaled by
 // a power of two) the MMAs sum O, with fp32 ones each tile's part is added with rounding.
@@ -315,9 +315,9 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
             for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
     }
     // V's scales, of either sign, are multiplied by a power of two that keeps them
-    // below 2 (the weights' terms below 2^15), one for each 32-dim block: a block of small
-    // scales keeps its bits beside one of large ones. O carries the factor. Scales
-    // between 2^-8 and 2 need none, and none is applied where all are 1.
+    // below 2 (the weights' terms below 2^15) and a block's largest at 2^-3 or more, one for each
+    // 32-dim block: a block of small scales keeps its bits beside one of large ones. O carries the
+    // factor. None is applied where all are 1.
     __half2 v_mul[C];
     bool v_scaled = true;
 #pragma unroll
@@ -496,10 +496,11 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                         for (int i = 0; i < 2; ++i) m = __hmax2(m, __habs2(as_half2(vd[u][i][c])));
                     const unsigned w = as_u32(m);
                     const unsigned big = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
-                    // below 2^(field - 14) by the exponent's field: from 2^-8 up to 2 they stay,
-                    // larger ones go below 1, smaller ones to 1/4 .. 1/2
+                    // below 2^(field - 14) by the exponent's field: from 2^-3 up to 2 they stay,
+                    // larger ones go below 1, smaller ones to 1/4 .. 1/2. (Products of a scale and a
+                    // weight are held to 2^-25: what a scale is below 1, they lose in bits.)
                     const int field = static_cast<int>(big >> 10);
-                    const int e = field >= 16 ? 14 - field : field >= 7 ? 0 : 13 - field;
+                    const int e = field >= 16 ? 14 - field : field >= 12 ? 0 : 13 - field;
                     const __half2 mul = __hmin2(v_mul[c], __float2half2_rn(exp2f(static_cast<float>(max(-15, min(15, e))))));
                     up[c] = __low2float(mul) / __low2float(v_mul[c]);
                     v_mul[c] = mul;
@@ -543,9 +544,16 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                     for (int i = 0; i < 4; ++i) y[u][n][i] = rel(u, n, i);
             }
         }
-        // ---- weights, as the B operand of the second product: O^T += V^T P^T. Weights
-        // below 2^-32 of the largest go in bands for wide activations (see attn_kernel.cuh).
-        constexpr float kLow = -18.f, kBand = 24.f;
+        // ---- weights, as the B operand of the second product: O^T += V^T P^T. A weight
+        // times V's scale is held to 2^-25, so that a small one keeps few bits, and where those of the
+        // large ones meet values of zero it is all there is. With wide activations, a tile that has
+        // weights below 2^-21 of the largest takes them in bands of 2^21, each scaled into
+        // range: with scales of 2^-3 the least of a band is still off by no more than 2^-15. It costs
+        // nothing where scores stay within 14 of the largest (64 x 8192, fp32 q: 157 us); scores that spread
+        // by 3.2 take 238 us, by 6.4 323. (Bands from 2^-32 on took 194 and 279, and left weights of
+        // 2^-24 with errors of up to 2^-12, those of 2^-32 with 2^-4.)
+        constexpr float kLow = -7.f, kBand = 21.f;
+        constexpr int kBands = 5;                     // down to 2^-105 of the largest
         auto in_band = [&](float x, int k) {
             const float lo = kLow - kBand * static_cast<float>(k);
             return x >= lo && (k == 0 || x < lo + kBand);
@@ -561,7 +569,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
                     for (int i = 0; i < 4; ++i) least = fminf(least, y[u][n][i]);
             if (__any_sync(0xffffffffu, least < kLow)) {
 #pragma unroll 1
-                for (int k = 1; k < 4; ++k) {
+                for (int k = 1; k < kBands; ++k) {
                     bool in = false;
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
@@ -574,7 +582,7 @@ __device__ __forceinline__ void attn_block_q4(const AttnArgs& a, int splits, int
             }
         }
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kBands; ++k) {
             if (HI && !(bands >> k & 1)) {
                 if (bands >> k == 0) break;
                 continue;

@@ -507,6 +507,11 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * cache's type the weights carry 22 bits (16 over bf16), and sums over up to 16384
  * keys are cut off, not rounded, to 24: 2^-16 and less of the result, before the
  * output's one rounding to 16 bits (over Q4_0 f16 and bf16 q count as the cache's type).
+ * Small weights count where the keys of the large ones have values near zero. f16 terms
+ * (every format but bf16) then hold a key's part to 2^-36 of the largest weight times the
+ * largest |v| (Q4_0: of its 32 dims); with fp32 q, or of another 16-bit type than the cache's,
+ * weights of less than 2^-32 (Q4_0: 2^-21) of the largest are scaled up first, so that a
+ * part of values near that |v| keeps 5 bits (f16: 7, Q4_0: 15) and more.
  * Scores in log2 units (times 1.4427) have to
  * be finite floats, and |scale| times the largest |q| of a row below 2^136.
  *

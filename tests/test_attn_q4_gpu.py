@@ -237,3 +237,39 @@ def test_head_dims_without_a_kernel_are_refused(Q):
         Q.qattn_decode(FMT, torch.zeros((1, 2, 160), device="cuda"), kc, vc, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
                        torch.ones(1, dtype=torch.int32, device="cuda"), 16, 1)
     assert e.value.name == "QMM_ERR_UNIMPLEMENTED"
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,group,page,n", [(128, 4, 32, 100), (64, 8, 16, 100), (128, 16, 64, 32), (96, 1, 8, 128), (256, 2, 32, 77),
+                                            (128, 4, 64, 3000)])
+@pytest.mark.parametrize("size", [30.0, 1.0, 0.1, 0.03, 0.003])
+def test_keys_far_below_one_whose_value_is_zero(Q, dt, D, group, page, n, size):
+    """One key takes nearly all of the softmax and has a value of zero: the output is made of
+    the others, whose weights are 2^-12 to 2^-88 of its.
+
+    fp32 queries: the plain form's tolerance, of sum |w v|. 16-bit ones: weights are held
+    to 2^-25 as 2^14 e^(s - m), and so are their products with V's scale d, of which a block's largest is
+    2^-3 or more: 2^-39 (1 / d + 1) of the largest weight and |v|, below 2^-35.8 a key, and
+    2^-37 for what an MMA may cut off 24 bits below the largest weight's product: 2^-35."""
+    import torch
+    p = problem(Q, dt, D, 1, group, page, [n], 3)
+    p["q"].fill_(1.0)
+    g = torch.Generator(device="cuda").manual_seed(n + D)
+    K, V = torch.zeros((n, 1, D), device="cuda"), size * torch.randn((n, 1, D), generator=g, device="cuda")
+    K[7], V[7] = 1.0, 0.0
+    j = np.arange(n)
+    slots = torch.from_numpy(p["host"][0][0, j // page].astype(np.int64) * page + j % page).cuda()
+    Q.qkv_store(FMT, K, V, slots, p["kc"], p["vc"], page)
+    K, V = (L.q4_values(c, page, 1, D)[slots // page, :, slots % page] for c in (p["kc"], p["vc"]))
+    assert bool((K[7] == 1).all()) and bool((V[7] == 0).all())
+    if n <= 128:
+        assert Q.qattn_decode_splits(FMT, U.dtype(dt), 1, group, 1, D, p["table"].shape[1] * page) == 1
+    for below in (12, 20, 24, 28, 32, 33, 40, 56, 75, 88):
+        scale = float(np.float32(below * math.log(2) / D))
+        out = call(Q, p, scale=scale)
+        want, _, tol, _ = U.attend(p["q"][0].double(), K, V, scale, 0.0, dt)
+        if dt != "f32":
+            tol = tol + n * 2.0 ** -35 * float(V.abs().max())
+        err = (out[0].double() - want).abs()
+        worst = float((err / tol).max())
+        assert worst <= 1, f"2^-{below} of the largest: {worst} of the tolerance"
