@@ -119,6 +119,14 @@ __device__ __forceinline__ float score32(bool softmax, float x, float top, float
     if (!softmax) return __fdividef(1.f, 1.f + __expf(-x));
     return top == -INFINITY ? 0.f : __fdividef(__expf(x - top), sum);
 }
+// A chosen expert's sigmoid, times e^-at, at <= 0.
+__device__ __forceinline__ float sigmoid_from(float x, float at) {
+    const float e = expf(-fabsf(x));
+    return (x < 0.f ? (at < 0.f ? expf(x - at) : e) : 1.f) / (1.f + e);
+}
+// Renormalised sigmoids below 2^-11 are taken relative to the largest chosen one's logit: what its
+// exponential would take out of fp32's range drops out of the quotient.
+__device__ __forceinline__ float sigmoid_at(float top) { return top < -8.f && top > -INFINITY ? top : 0.f; }
 // Twice its error at magnitude |c| (k_route's comment), from its part at c = 0.
 __device__ __forceinline__ float tau_of(float base, float v) { return base + 2.384185791015625e-07f * fabsf(v); }   // 2^-22
 
@@ -467,14 +475,15 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
     const int e = expert_in(mine);
     const float lx = biased ? logit(a, t, e) : value_of(key_in(mine));
     float w;
+    auto most_chosen = [&] { return biased ? value_of(__reduce_max_sync(kAll, key_of(lx))) : value_of(key_in(sorted[0])); };
     if (softmax) {
         // renormalised, the row's sum falls out; relative to the largest chosen logit
-        if (a.renorm) top = biased ? value_of(__reduce_max_sync(kAll, key_of(lx))) : value_of(key_in(sorted[0]));
+        if (a.renorm) top = most_chosen();
         w = top == -INFINITY ? 0.f : expf(lx - top);
         if (!a.renorm) w /= sum;
         if (BY_SCORE && isnan(sum)) w = sum;              // by a logit that need not be among the chosen
     } else {
-        w = 1.f / (1.f + expf(-lx));
+        w = sigmoid_from(lx, a.renorm && __any_sync(kAll, lx < -8.f) ? sigmoid_at(most_chosen()) : 0.f);
     }
     if (a.renorm) {
         float s = chosen ? w : 0.f;
@@ -720,13 +729,14 @@ __global__ void __launch_bounds__(256, V > 16 ? 2 : 4) k_route_four(const __grid
     const int e = leave ? 0 : expert_in(own);
     const float lx = leave ? 0.f : biased ? logit(a, t, e) : value_of(key_in(own));
     float w;
+    auto most_chosen = [&] { return biased ? value_of(max8(chosen ? key_of(lx) : 0u)) : value_of(key_in(sorted[0])); };
     if (softmax) {
-        if (a.renorm) top = biased ? value_of(max8(chosen ? key_of(lx) : 0u)) : value_of(key_in(sorted[0]));
+        if (a.renorm) top = most_chosen();
         w = top == -INFINITY ? 0.f : expf(lx - top);
         if (!a.renorm) w /= sum;
         if (BY_SCORE && isnan(sum)) w = sum;              // by a logit that need not be among the chosen
     } else {
-        w = 1.f / (1.f + expf(-lx));
+        w = sigmoid_from(lx, a.renorm && __any_sync(kAll, lx < -8.f) ? sigmoid_at(most_chosen()) : 0.f);
     }
     if (a.renorm) {
         const float s = sum8(chosen ? w : 0.f);

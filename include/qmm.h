@@ -610,7 +610,7 @@ typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
  * the logits themselves are compared. A NaN logit or bias counts as the largest
  * value; weights are NaN where the formula is (softmax: all of the token's). Logits
  * of -Inf have s = 0, a row of only those all s = 0; a bias of -Inf puts an
- * expert behind all others. Where the chosen scores are all zero renormalised
+ * expert behind all others. Where the chosen logits are all -Inf renormalised
  * weights are zero. Ids are always distinct and in range.
  *
  *   logits    device, dtype, token t's n_experts values at t * stride

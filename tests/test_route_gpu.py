@@ -290,3 +290,22 @@ def test_experts_take_the_routing(Q, orc):
                             ids.cpu().numpy(), w.cpu().numpy(), p["d_model"], p["d_ff"], nthreads=8)
     assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
     assert isinstance(y, torch.Tensor)
+
+
+@pytest.mark.parametrize("T", [7, 8002])
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top", [(64, 2, 1, 1, 1), (64, 8, 1, 1, 1), (64, 6, 4, 2, 2), (128, 8, 8, 3, 1), (45, 9, 3, 2, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoids_whose_exponential_passes_fp32(Q, T, E, k, groups, top_groups, group_top, renorm):
+    """Logits below -88.7: the score is not a normal float, and the renormalised weights are its ratios."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for lo, hi in ((-89.5, -88.0), (-110.0, -60.0), (-690.0, -100.0), (-200.0, 20.0)):
+        x = lo + (hi - lo) * torch.rand((T, E), generator=g, device="cuda")
+        x[::3, ::2] = -200.0
+        x[1::4] = -200.0
+        x[2::5, 3:] = -math.inf
+        check(Q, x, k, "sigmoid", None, groups, top_groups, group_top, renorm)
+        check(Q, x, k, "sigmoid", 0.1 * randn((E,), "f32", 2), groups, top_groups, group_top, renorm)
+    x = torch.full((T, E), -1e4, device="cuda")
+    ids, w = Q.qmoe_route(x, k, score="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top, renorm=renorm)
+    assert bool((w == (1 / k if renorm else 0.0)).all() if k in (2, 8) else ((w - (1 / k if renorm else 0.0)).abs() <= 2.0 ** -24).all())
