@@ -107,7 +107,7 @@ __device__ __noinline__ double value64(const RouteArgs& a, int64_t t, int e, flo
         return 1.0 / (1.0 + exp(-x)) + b;
     }
     const double y = x - top;
-    return (top == -INFINITY ? 0.0 : y >= -700.0 ? exp_mid(y) * by_sum : isnan(y) ? y : 0.0) + b;
+    return (top == -INFINITY ? 0.0 : (y >= -700.0 ? exp_mid(y) : exp(y)) * by_sum) + b;
 }
 // Keys of doubles as key_of's of floats.
 __device__ __forceinline__ unsigned long long key64(double v) {

@@ -604,10 +604,12 @@ typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
  *   ids: the top_k largest c of those that stay, the largest first
  *   w_j = s_{ids_j}, divided by their sum if renorm, times scale
  *
- * Equal values go to the lower index. They are compared as real numbers, not as
- * fp32 has them: where fp32's rounding could decide (in a few rows of a thousand),
+ * Equal values go to the lower index. They are compared as 64 bits have them, not as
+ * fp32 does: where fp32's rounding could decide (in a few rows of a thousand),
  * the row is computed in 64 bits. Without a bias, groups of group_top 2 aside,
- * the logits themselves are compared. A NaN logit or bias counts as the largest
+ * the logits themselves are compared; with one, also of zeros, scores that 64 bits do
+ * not tell apart are equal (sigmoids of logits past 37; what is below 2^-53 of the
+ * bias). A NaN logit or bias counts as the largest
  * value; weights are NaN where the formula is (softmax: all of the token's). Logits
  * of -Inf have s = 0, a row of only those all s = 0; a bias of -Inf puts an
  * expert behind all others. Where the chosen logits are all -Inf renormalised

@@ -309,3 +309,36 @@ def test_sigmoids_whose_exponential_passes_fp32(Q, T, E, k, groups, top_groups, 
     x = torch.full((T, E), -1e4, device="cuda")
     ids, w = Q.qmoe_route(x, k, score="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top, renorm=renorm)
     assert bool((w == (1 / k if renorm else 0.0)).all() if k in (2, 8) else ((w - (1 / k if renorm else 0.0)).abs() <= 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("T", [5, 8002])
+@pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+def test_softmax_scores_down_to_the_end_of_64_bits(Q, T, groups, top_groups, group_top):
+    """With a bias of zeros the order is that of the scores, e^-703 and less but one."""
+    import torch
+    x = torch.arange(64, device="cuda", dtype=torch.float32) / 2 - 741.5      # -741.5 .. -710, ascending
+    x[:16] = torch.arange(16, device="cuda") * 3.0 - 748.0                    # -748 .. -703
+    x[3] = 0.0
+    x = x.expand(T, 64) + 0.0
+    x[1::2] = x[1::2].flip(1)
+    check(Q, x, 6, "softmax", torch.zeros(64, device="cuda"), groups, top_groups, group_top)
+
+
+@pytest.mark.parametrize("T", [5, 8002])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_that_64_bits_cannot_tell_apart_go_to_the_lower_index(Q, T, score):
+    """With a bias, also one of zeros, values are compared in 64 bits: logits of 45 and 50 have the same sigmoid there,
+    and scores below 2^-53 of the bias are lost in it. Without one the logits decide."""
+    import torch
+    x = randn((T, 64), "f32", 3, 0.1)
+    if score == "sigmoid":
+        x[:, 10:14] = torch.tensor([45.0, 50.0, 60.0, 47.0], device="cuda")
+        bias = torch.zeros(64, device="cuda")
+    else:
+        x[:, 20] = 90.0                                                       # the others' scores: e^-90
+        bias = torch.full((64,), 0.5, device="cuda")
+    ids, _ = check(Q, x, 3, score, bias)
+    assert ids[0].tolist() == ([10, 11, 12] if score == "sigmoid" else [20, 0, 1])
+    ids, _ = check(Q, x, 3, score)
+    if score == "sigmoid":
+        assert ids[0].tolist() == [12, 11, 13]
