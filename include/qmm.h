@@ -564,8 +564,9 @@ QMM_API int qattn_decode_splits(int fmt, int dtype, int64_t B, int n_q_heads, in
  *
  * The norm takes h before it is rounded for residual_out. H = 1 norms tokens; more
  * norm each head of a projection's rows. A row whose sum of squares passes
- * the fp32 range (values of about 2^60 and more) gives zeros, one that holds an
- * Inf or NaN gives NaN; with eps = 0 one of zeros, or of values so small that
+ * the fp32 range (values of about 2^60 and more) gives zeros, one that holds a
+ * NaN gives NaN, and one that holds an Inf what the formula does: NaN in its place (in
+ * QMM_NORM_Q8_0 rows its block) and zeros elsewhere; with eps = 0 one of zeros, or of values so small that
  * all squares vanish in fp32 (below 2^-75), is divided by zero.
  *
  *   X             device, x_dtype, element (t, h, d) at t * x_ts + h * x_hs + d

@@ -235,3 +235,29 @@ def test_on_another_stream_and_in_a_graph(Q):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(r, after) and torch.equal(out, Q.qrmsnorm(want, w))
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "q8_0"])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("T,D,pad", [(5, 64, 0), (5, 256, 0), (5, 1024, 0), (5, 4096, 0), (700, 2048, 0), (3, 40960, 0), (2, 70016, 0), (5, 4640, 1)])
+def test_an_infinite_value_takes_its_row(Q, out, res, T, D, pad):
+    """h / sqrt(mean h^2): an Inf makes its own element NaN and the others zeros, in Q8_0 rows its block
+    NaN and the others zeros; other rows are as they are without it."""
+    import torch
+    x = randn((T, D + pad), "f32", D)[:, pad:]
+    r = randn((T, D), "f32", 2) if res else None
+    to = "q8_0" if out == "q8_0" else U.dtype(out)
+    want = Q.qrmsnorm(x, None, residual=None if r is None else r.clone(), out_dtype=to)
+    x[1, D - 7] = -math.inf
+    y = Q.qrmsnorm(x, None, residual=r, out_dtype=to)
+    others = [i for i in range(T) if i != 1]
+    assert torch.equal(y[others], want[others])
+    if out == "q8_0":
+        v = Q.qdequant("Q8_0", y[1:2].contiguous(), 1, D)[0]
+        assert bool(torch.isnan(v[D - 32:]).all() and (v[:D - 32] == 0).all())
+    else:
+        hit = torch.zeros(D, dtype=torch.bool, device="cuda")
+        hit[D - 7] = True
+        assert torch.equal(torch.isnan(y[1]), hit) and bool((y[1][~hit] == 0).all())
+    if r is not None:
+        assert float(r[1, D - 7]) == -math.inf
