@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "exp64.cuh"
 #include "layer_common.cuh"
 
 namespace qmm {
@@ -67,28 +68,8 @@ __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
 
 // ---- in 64 bits, for the few tokens that need it. What they take is felt at the end of
 // every call of some thousand tokens, all of which run at once, and is mostly the
-// fetching of code that ran nowhere before: hence a short exponential and quotient.
+// fetching of code that ran nowhere before: hence a short exponential and quotient (exp64.cuh).
 
-// e^x to 2 ulp for |x| <= 700: x = k ln 2 + r with ln 2 in two parts (Cody and Waite),
-// e^r by its Taylor sum to r^13 / 13! (|r| <= 0.35: the next term is 5e-18).
-__device__ __forceinline__ double exp_mid(double x) {
-    const double k = rint(x * 1.4426950408889634);
-    double r = fma(k, -0.6931471805592082, x);                 // ln 2 cut off to 40 bits: k times it is exact
-    r = fma(k, -7.371002565167799e-13, r);                     // the rest of it
-    const double r2 = r * r, r4 = r2 * r2;
-    const double p0 = fma(r, 1.0, 1.0), p1 = fma(r, 1.0 / 6, 0.5), p2 = fma(r, 1.0 / 120, 1.0 / 24), p3 = fma(r, 1.0 / 5040, 1.0 / 720);
-    const double p4 = fma(r, 1.0 / 362880, 1.0 / 40320), p5 = fma(r, 1.0 / 39916800, 1.0 / 3628800);
-    const double p6 = fma(r, 1.0 / 6227020800.0, 1.0 / 479001600);
-    const double q0 = fma(p1, r2, p0), q1 = fma(p3, r2, p2), q2 = fma(p5, r2, p4);
-    const double e = fma(fma(fma(p6, r4, q2), r4, q1), r4, q0);
-    return __hiloint2double(__double2hiint(e) + (static_cast<int>(k) << 20), __double2loint(e));
-}
-// 1 / d to 1 ulp for d in fp32's range: Newton's steps from an fp32 quotient.
-__device__ __forceinline__ double inverse(double d) {
-    double y = static_cast<double>(__fdividef(1.f, static_cast<float>(d)));
-    y = fma(y, fma(-d, y, 1.0), y);
-    return fma(y, fma(-d, y, 1.0), y);
-}
 // The sum of a row's exponentials relative to its largest logit `top`, inverted.
 __device__ __noinline__ double sum64(const RouteArgs& a, int64_t t, float top) {
     if (a.score == QMM_SCORE_SIGMOID || top == -INFINITY) return 1.0;
@@ -127,7 +108,7 @@ __device__ __forceinline__ float sigmoid_from(float x, float at) {
 // Renormalised sigmoids below 2^-11 are taken relative to the largest chosen one's logit: what its
 // exponential would take out of fp32's range drops out of the quotient.
 __device__ __forceinline__ float sigmoid_at(float top) { return top < -8.f && top > -INFINITY ? top : 0.f; }
-// Twice its error at magnitude |c| (k_route's comment), from its part at c = 0.
+// Twice its error at magnitude |c| (see route_token), from its part at c = 0.
 __device__ __forceinline__ float tau_of(float base, float v) { return base + 2.384185791015625e-07f * fabsf(v); }   // 2^-22
 
 // Whether q may come before p, which has the larger or an equal fp32 value: where that is near,
@@ -303,11 +284,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, bool 
     // ---- c in fp32, as keys (the logits themselves where their order is the scores')
     unsigned key[V];
     [[maybe_unused]] float base = 0.f;
-    // Twice the error of a c of magnitude |c|. A sigmoid's exponential is off by (2 + 1.2 |x|)
-    // 2^-23, which s (1 - s) makes 0.6 2^-23 at most, the quotient and its 1 + e by 1.5 2^-23
-    // more: below 2^-21.9. Softmax scores are off, relative to the largest, 1 / sum, by
-    // 2^-22 from the exponential, as much from the quotient, and by a common factor of the
-    // sum's V + 5 roundings. The sum with the bias: 2^-24 |c|.
+    // Twice the error of a c of magnitude |c|. A sigmoid's exponential (2 + 1.2 |x| ulp), its 1 + e
+    // (1/2) and its quotient (2) put it off by 1.8 2^-23 at most, their largest parts not
+    // falling together: twice that is below 2^-21. Two softmax scores, relative to the
+    // largest, 1 / sum, are off from one another by 2 2^-23 from their exponentials, up to 4 from their
+    // quotients, and where one is far below the other by a common factor: the sum's V + 5
+    // roundings, half each, and up to 7 from its small exponentials; 8.4 in all for 32
+    // experts, 27 for 1024. The sum with the bias: 2^-24 |c|.
     auto tau = [&](float v) { return tau_of(base, v); };
     if constexpr (BY_SCORE) {
         base = softmax ? static_cast<float>(V + 12) * 1.1920928955078125e-07f / sum : 4.76837158203125e-07f;   // 2^-23, 2^-21
