@@ -46,8 +46,9 @@ template <int D, bool HI, int NT, int MINB, bool PACK> cudaError_t go_with(const
 }
 
 // Blocks per SM, keys per tile and depth of the ring, measured on 64 sequences of 8192
-// tokens and on one of 131072 (f16 activations, 8 key-value heads of 128). Instructions bound
-// the kernel: tiles of 32 keys, two stages and three blocks take 134 and 39 us, four blocks
+// tokens and on one of 131072 (f16 activations, 8 key-value heads of 128). A warp's chain of
+// instructions bounds the kernel, three warps a scheduler: 63 % of the issue slots, no pipe above
+// half. Tiles of 32 keys, two stages and three blocks take 134 and 39 us, four blocks
 // 135 and 43. (With an MMA for each term, 140 and 40 us, tiles of 16 keys took 154 and 47, of
 // 64 155 and 43, three stages 142 and 42.) Dim 64 fits four blocks (64 x 8192: 88 us; three 89).
 template <int FMT, int D, bool HI, int NT> cudaError_t go(const Launch& l) {

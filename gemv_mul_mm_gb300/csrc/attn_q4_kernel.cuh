@@ -3,14 +3,16 @@
 // mma.sync are those of attn_kernel.cuh; what differs is here.
 //
 // A cached value takes 18 / 32 bytes: half of q8_0's traffic for as many values, so
-// that instructions per value decide. Tiles of 32 keys (two halves of 16 in the MMAs) share
+// that a warp's instructions per value, and the latency of their chain, decide. Tiles of 32 keys (two halves of 16 in the MMAs) share
 // one step of the loop and of the running maximum, and give two chains of
 // dependent instructions to interleave. Pages of 32 keys and more hold whole tiles, which
 // are copied without a look at pages inside; smaller ones take a kernel of their own.
 //
 // Measured, 64 sequences of 8192 tokens, 8 key-value heads of 128, 4 query heads each: 134 us
 // with f16 activations (0.66 of the copy bandwidth, 4.5 TB/s; some 680 instructions a tile
-// of 32 keys, 60 % of the issue slots), 156 us with fp32; one sequence of 131072: 39 and 44 us.
+// of 32 keys, 63 % of the issue slots), 156 us with fp32; one sequence of 131072: 39 and 44 us.
+// A window of 4096 of the 8192 takes 84 and 95 us, of 1024 27 and 31; a softcap (every tile then
+// takes the slow path) 190 and 216. 16 query heads (4 key-value heads) do 126 and 97 TFLOP/s.
 //
 // Codes. ldmatrix reads a row's 32-dim block as eight 16-bit elements, four codes
 // each: lane (g, t) gets codes 8t .. 8t + 7 of key g (K), or dims 4g .. 4g + 3 of
@@ -26,10 +28,11 @@
 //
 // Scales as over q8_0: K's multiplies the fp32 sum of a 32-dim block, V's the two
 // f16 terms of the weights, after a power of two for each block of dims where its scales
-// pass 2 or stay below 2^-3 (then 1 to 2 % slower: 134 -> 136, 156 -> 159 us). The MMAs have eight columns, and up to four query heads fill half
-// of them: the other four then take the second terms, of the weights and of fp32 queries, of the
-// same heads (PACK: half the MMAs; 140 -> 134 and 176 -> 156 us). With 16-bit activations (bf16 rows are f16 values once scaled by
-// a power of two) the MMAs sum O, with fp32 ones each tile's part is added with rounding.
+// pass 2 or stay below 2^-3 (then 1 to 2 % slower: 134 -> 136, 156 -> 159 us). The MMAs have
+// eight columns, and up to four query heads fill half of them: the other four then take the second
+// terms, of the weights and of fp32 queries, of the same heads (PACK: half the MMAs; 140 -> 134
+// and 176 -> 156 us). With 16-bit activations (bf16 rows are f16 values once scaled by a power of
+// two) the MMAs sum O, with fp32 ones each tile's part is added with rounding.
 #pragma once
 
 #include "attn_kernel.cuh"

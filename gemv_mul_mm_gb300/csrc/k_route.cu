@@ -19,12 +19,14 @@
 // the order of the logits, which are compared as they are. With one (and for sums
 // over groups; BY_SCORE) fp32 values of c are off by up to half of `tau`: where two neighbours of
 // the order that matter lie closer than that and do not come from equal inputs,
-// the warp computes the candidates (for groups: all c) in 64 bits and
-// counts again. With the scores of 256 experts that is one token in some hundred.
+// the warp computes the candidates (for groups: the few that may be among a group's largest)
+// in 64 bits and counts again. With the scores of 256 experts that is one token in some hundred.
 //
 // Measured: 65536 tokens x 128 experts, bf16, top 8: 13.6 us (1.5 TB/s; 25.6 with a warp a
 // token, 183 instructions a token against 496); 8192 x 256 in 8 groups, sigmoid with a
-// bias: 12 us, of which 2 are the few tokens in 64 bits; one token 2 to 4 us.
+// bias: 11.5 us and, where a token's groups lie close enough to be decided in 64 bits, up to 21;
+// 65536 x 256 in groups 70 us (450 instructions a token at 31 % of the issue slots: 16 warps an
+// SM, by registers), with a bias and no groups 53 (a warp a token, 710, 62 %); one token 2 to 4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -753,7 +755,8 @@ template <int V, typename T, bool BY_SCORE> cudaError_t go(const RouteArgs& a, c
         // Four tokens a warp from 24 tokens an SM on (128 experts: 4800 tokens 3.1 us, a warp each 3.8;
         // 2400 2.7 and 2.8), by score from 40 on (256 experts in groups: 8192 tokens 11.9 and
         // 14.4 us, 4800 10.0 and 8.3); but not by score with 32 experts a lane and no groups,
-        // where registers decide (8192 tokens 11.8 and 9.9 us).
+        // where registers decide (sigmoids: 8192 tokens 11.0 and 9.3 us, 65536 58.4 and 52.7;
+        // softmax: 20.1 and 18.3, 75.8 and 74.5).
         const int gs = a.E / a.groups, lanes = gs / (4 * V);
         const bool whole = a.groups == 1 || (gs == lanes * 4 * V && (lanes & (lanes - 1)) == 0);
         if (a.top_k <= kFourTopK && a.E % (4 * V) == 0 && at16 && whole && !(BY_SCORE && V == 8 && a.groups == 1) &&

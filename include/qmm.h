@@ -511,7 +511,8 @@ QMM_API int qkv_load(int fmt, const int64_t* slots, const void* k_cache, const v
  * (every format but bf16) then hold a key's part to 2^-36 of the largest weight times the
  * largest |v| (Q4_0: of its 32 dims); with fp32 q, or of another 16-bit type than the cache's,
  * weights of less than 2^-32 (Q4_0: 2^-21) of the largest are scaled up first, so that a
- * part of values near that |v| keeps 5 bits (f16: 7, Q4_0: 15) and more.
+ * part of values near that |v| keeps 5 bits (f16: 7, Q4_0: 15) and more; below 2^-104 of the
+ * largest weight nothing is left.
  * Scores in log2 units (times 1.4427) have to
  * be finite floats, and |scale| times the largest |q| of a row below 2^136.
  *
@@ -610,7 +611,8 @@ typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
  * the row is computed in 64 bits. Without a bias, groups of group_top 2 aside,
  * the logits themselves are compared; with one, also of zeros, scores that 64 bits do
  * not tell apart are equal (sigmoids of logits past 37; what is below 2^-53 of the
- * bias). A NaN logit or bias counts as the largest
+ * bias), and values within 2^-49 of the largest's magnitude are in the order that this
+ * computation rounds them to. A NaN logit or bias counts as the largest
  * value; weights are NaN where the formula is (softmax: all of the token's). Logits
  * of -Inf have s = 0, a row of only those all s = 0; a bias of -Inf puts an
  * expert behind all others. Where the chosen logits are all -Inf renormalised
